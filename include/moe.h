@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 9
+#define MOE_ABI_VERSION 10
 /* Rows per tile of the grouped-GEMM tile list built by moe_permute_meta. */
 #define MOE_TILE_M 256
 #define MOE_MAX_EXPERTS 256
@@ -79,7 +79,8 @@ typedef enum moe_entry {
   MOE_ENTRY_ROUTE_BWD_AUX = 5,
   MOE_ENTRY_SHARED_FFN = 6,    /* shared-expert dims only (E = K = 1) */
   MOE_ENTRY_SHARED_FFN_BWD = 7, /* shared-expert dims only (E = K = 1) */
-  MOE_ENTRY_ROUTE_META = 8
+  MOE_ENTRY_ROUTE_META = 8,
+  MOE_ENTRY_RMS_NORM_BWD = 9 /* (size_t)-1 when H > MOE_NORM_MAX_H */
 } moe_entry;
 
 /* bf16 grouped-GEMM tile family (moe_dims.gemm_tiles).  AUTO lets the
@@ -455,6 +456,111 @@ int moe_shared_ffn_bwd(const moe_dims* ds, const void* x, const void* dy, const 
 int moe_permute_bwd_add(const moe_dims* d, const void* dxs, const int32_t* inv, const int32_t* topk_idx,
                         const float* dlogits, const void* w_r, int32_t dense, const void* dx_add, void* dx, void* ws,
                         size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------ few tokens (decoding) */
+
+/* Most tokens of one moe_decode call. */
+#define MOE_DECODE_MAX_TOKENS 64
+
+/* Workspace bytes of moe_decode for these dims (ds NULL: no shared expert);
+ * (size_t)-1 on invalid dims or more than MOE_DECODE_MAX_TOKENS tokens. */
+size_t moe_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds);
+
+/* The whole layer for the few tokens of a decoding step, forward only:
+ *   l = x.W_r (+ logit_bias), the K experts of largest logit by (l desc, id
+ *   asc), gates = softmax over the K selected logits,
+ *   y[n] = sum_k gates[n,k] FFN_{e_n,k}(x_n) (+ FFN_s(x_n)).
+ * The weights of each chosen expert are read once; nothing is sorted or
+ * grouped, so a call reads about (chosen experts)*3*H*F elements and is bound
+ * by that.  Same layer as moe_route_meta .. moe_combine(_shared) without a
+ * capacity, with fewer roundings: logits are summed in float64 (moe_route:
+ * float32), G, U, A and the expert outputs keep float32 accuracy (there: each
+ * stored rounded) and y is rounded once, so the two agree within the element
+ * type's rounding but not bit for bit, and may choose differently between
+ * experts whose logits differ by less than float32 resolves.  NaN logits rank
+ * last.  A call's result depends on N (how sums are cut), not on timing.
+ *   d: the layer's dims, 0 <= N <= MOE_DECODE_MAX_TOKENS (MOE_EUNSUPPORTED
+ *   above); gemm_tiles is ignored.  x [N,H]; w_r [H,E]; logit_bias [E] f32 or
+ *   NULL; w_gate, w_up [E,H,F]; w_down [E,F,H].
+ *   ds: the shared expert's dims {N, H, Fs, 1, 1, dtype}, with its weights
+ *   ws_gate, ws_up [H,Fs] and ws_down [Fs,H]; or NULL, with all three NULL.
+ *   topk_idx [N,K] int32 out; gates [N,K] f32 out; y [N,H] out, not
+ *   overlapping x.  ws: moe_decode_workspace_bytes(d, ds). */
+int moe_decode(const moe_dims* d, const void* x, const void* w_r, const float* logit_bias, const void* w_gate,
+               const void* w_up, const void* w_down, const moe_dims* ds, const void* ws_gate, const void* ws_up,
+               const void* ws_down, int32_t* topk_idx, float* gates, void* y, void* ws, size_t ws_bytes,
+               hipStream_t stream);
+
+/* ----------------------------------------- norm in front of the layer */
+
+/* Longest row of moe_rms_norm and moe_rms_norm_bwd. */
+#define MOE_NORM_MAX_H 32768
+
+/* Residual addition and root-mean-square norm of the token rows:
+ *   h[n] = x[n] + residual[n]   (float32, stored rounded),
+ *   rstd[n] = 1 / sqrt(mean(h[n]^2) + eps),
+ *   y[n] = h[n] * rstd[n] * weight   (from the stored h, one rounding).
+ * Without a residual h is x, and nothing is stored for it.
+ *   d: N, H and dtype are used; H <= MOE_NORM_MAX_H (MOE_EUNSUPPORTED above).
+ *   x, residual [N,H] act; residual and h are both set or both NULL; h [N,H]
+ *   out, may be x or residual itself; weight [H] act; eps finite and > 0;
+ *   y [N,H] out, overlapping no other argument; rstd [N] f32 out or NULL.
+ * Squares are summed in float32: rows with |h| above 1.8e19 overflow.
+ * Errors: MOE_EINVAL for eps, a null, misaligned or overlapping pointer. */
+int moe_rms_norm(const moe_dims* d, const void* x, const void* residual, const void* weight, float eps, void* h,
+                 void* y, float* rstd, hipStream_t stream);
+
+/* Backward of moe_rms_norm, differentiated at the stored h:
+ *   t = dy * weight, xhat = h * rstd,
+ *   dx = rstd * (t - xhat * mean(t * xhat)) (+ dh)   (float32, one rounding),
+ *   dweight = sum_n dy[n] * xhat[n]   (float32).
+ * dx is the gradient of x and of residual alike.
+ *   dy, h [N,H] act (h: x when there was no residual); rstd [N] f32 from
+ *   moe_rms_norm; dh [N,H] act, the gradient that reaches h beside y (the
+ *   residual stream), or NULL; dx [N,H] out, may be dy or dh itself;
+ *   dweight [H] f32 out.  ws: MOE_ENTRY_RMS_NORM_BWD (a row of H float32
+ *   partial sums per workgroup; any H up to MOE_NORM_MAX_H). */
+int moe_rms_norm_bwd(const moe_dims* d, const void* dy, const void* h, const void* weight, const float* rstd,
+                     const void* dh, void* dx, float* dweight, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* --------------------------------------------- gradient norm, clipping */
+
+/* One gradient of a list: n elements at `in` (moe_dtype in_dtype); for
+ * moe_grad_clip also n elements at `out` (out_dtype).  Pointers are device
+ * memory aligned to their element; a tensor whose pointers are aligned to 16
+ * bytes is read and written faster.  n = 0: the pointers are not looked at. */
+typedef struct moe_grad {
+  const void* in;
+  void* out;
+  int64_t n;
+  int32_t in_dtype, out_dtype;
+} moe_grad;
+
+/* Workspace of moe_grad_norm and moe_grad_clip. */
+#define MOE_GRAD_WS_BYTES 8192
+/* Longest list. */
+#define MOE_GRAD_MAX_TENSORS 65536
+
+/* norm[0] = sqrt(sum over all tensors and elements of g^2), f32 on the device
+ * (never read back by the library), squares summed in float64 in a fixed
+ * order.  list: count tensors, HOST memory, read during the call only (a
+ * captured graph keeps its own copy).  count = 0 gives 0.  Tensors may overlap
+ * or repeat; each occurrence counts.
+ * Errors: MOE_EINVAL for count < 0, a null list, n < 0, an unknown dtype (or
+ * MOE_EUNSUPPORTED for a longer list or more than 2^44 elements in all), a null
+ * or misaligned pointer; MOE_EWORKSPACE. */
+int moe_grad_norm(const moe_grad* list, int64_t count, float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Clipping by the global norm: norm[0] as moe_grad_norm, then for every tensor
+ *   out[i] = in[i] * min(1, max_norm / (norm + 1e-6)),
+ * the factor rounded to float32, the product rounded once to out_dtype.  A NaN
+ * norm makes every output NaN; an infinite one makes finite elements 0 and the
+ * others NaN.
+ *   max_norm finite and >= 0.  out may be in itself (same dtype: in place);
+ *   apart from that no output overlaps another tensor's or its own input or
+ *   another output (MOE_EINVAL), nor norm and ws. */
+int moe_grad_clip(const moe_grad* list, int64_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
 
 /* ------------------------------------------- no-allocation entry point */
 

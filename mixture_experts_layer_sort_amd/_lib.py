@@ -23,7 +23,11 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_ENTRY_PERMUTE_META, MOE_ENTRY_ROUTE_BWD, MOE_ENTRY_PERMUTE_BWD = 1, 2, 3
 MOE_ENTRY_AUX_LOSS, MOE_ENTRY_ROUTE_BWD_AUX = 4, 5
 MOE_ENTRY_SHARED_FFN, MOE_ENTRY_SHARED_FFN_BWD, MOE_ENTRY_ROUTE_META = 6, 7, 8
+MOE_ENTRY_RMS_NORM_BWD = 9
 MOE_TILE_M = 256
+MOE_DECODE_MAX_TOKENS = 64
+MOE_NORM_MAX_H = 32768
+MOE_GRAD_WS_BYTES, MOE_GRAD_MAX_TENSORS = 8192, 65536
 # moe_gemm_tiles (moe_dims.gemm_tiles): AUTO, or one bf16 tile family forced on every GEMM stage
 MOE_TILES_AUTO, MOE_TILES_256, MOE_TILES_128X256, MOE_TILES_128 = 0, 1, 2, 3
 
@@ -40,7 +44,13 @@ class moe_dims(ctypes.Structure):
     _fields_ = [("N", _I64), ("H", _I64), ("F", _I64), ("E", _I64), ("K", _I64), ("dtype", _I32), ("gemm_tiles", _I32)]
 
 
+class moe_grad(ctypes.Structure):
+    # `in` and `out` of the C struct (in is a Python keyword)
+    _fields_ = [("in_", _P), ("out", _P), ("n", _I64), ("in_dtype", _I32), ("out_dtype", _I32)]
+
+
 _DP = ctypes.POINTER(moe_dims)
+_GP = ctypes.POINTER(moe_grad)
 
 SIGNATURES = {
     "moe_abi_version": (ctypes.c_int, []),
@@ -74,6 +84,12 @@ SIGNATURES = {
     "moe_route_meta": (ctypes.c_int, [_DP, _P, _P, _P, _I32] + [_P] * 9 + [_SZ, _P]),
     "moe_route_meta_noalloc": (ctypes.c_int, [_DP, _P, _P, _P, _I32] + [_P] * 8 + [_P]),
     "moe_ffn_bwd_dx_dw_gather": (ctypes.c_int, [_DP] + [_P] * 15 + [_P]),
+    "moe_decode_workspace_bytes": (_SZ, [_DP, _DP]),
+    "moe_decode": (ctypes.c_int, [_DP] + [_P] * 6 + [_DP] + [_P] * 7 + [_SZ, _P]),
+    "moe_rms_norm": (ctypes.c_int, [_DP, _P, _P, _P, _F, _P, _P, _P, _P]),
+    "moe_rms_norm_bwd": (ctypes.c_int, [_DP] + [_P] * 8 + [_SZ, _P]),
+    "moe_grad_norm": (ctypes.c_int, [_GP, _I64, _P, _P, _SZ, _P]),
+    "moe_grad_clip": (ctypes.c_int, [_GP, _I64, _F, _P, _P, _SZ, _P]),
 }
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -308,3 +324,51 @@ def moe_ffn_bwd_dx_dw_gather(d, dg, du, w_gate, w_up, tiles, num_tiles, dxs, x, 
     _call("moe_ffn_bwd_dx_dw_gather", ctypes.byref(d), _ptr(dg), _ptr(du), _ptr(w_gate), _ptr(w_up), _ptr(tiles),
           _ptr(num_tiles), _ptr(dxs), _ptr(x), _ptr(sorted_flat), _ptr(act), _ptr(dys), _ptr(offsets),
           _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _stream(stream))
+
+
+def _dims_ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def moe_decode_workspace_bytes(d: moe_dims, ds: Optional[moe_dims] = None) -> int:
+    return lib().moe_decode_workspace_bytes(ctypes.byref(d), _dims_ref(ds))
+
+
+def moe_decode(d, x, w_r, logit_bias, w_gate, w_up, w_down, ds, ws_gate, ws_up, ws_down, topk_idx, gates, y, ws,
+               stream=None):
+    _call("moe_decode", ctypes.byref(d), _ptr(x), _ptr(w_r), _ptr(logit_bias), _ptr(w_gate), _ptr(w_up),
+          _ptr(w_down), _dims_ref(ds), _ptr(ws_gate), _ptr(ws_up), _ptr(ws_down), _ptr(topk_idx), _ptr(gates),
+          _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def moe_rms_norm(d, x, residual, weight, eps, h, y, rstd, stream=None):
+    _call("moe_rms_norm", ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), float(eps), _ptr(h), _ptr(y),
+          _ptr(rstd), _stream(stream))
+
+
+def moe_rms_norm_bwd(d, dy, h, weight, rstd, dh, dx, dweight, ws, stream=None):
+    _call("moe_rms_norm_bwd", ctypes.byref(d), _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), _ptr(dx),
+          _ptr(dweight), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def grad_list(grads, outs=None):
+    """The moe_grad array of a list of gradients (and of the outputs of moe_grad_clip)."""
+    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+    rows = []
+    for g, o in zip(grads, grads if outs is None else outs):
+        if g.dtype not in code or o.dtype not in code:
+            raise ValueError(f"unsupported dtype {g.dtype if g.dtype not in code else o.dtype}")
+        if g.numel() != o.numel():
+            raise ValueError("a gradient and its output differ in size")
+        rows.append((_ptr(g), _ptr(o), g.numel(), code[g.dtype], code[o.dtype]))
+    return (moe_grad * max(1, len(rows)))(*rows)
+
+
+def moe_grad_norm(grads, norm, ws, stream=None):
+    _call("moe_grad_norm", grad_list(grads), len(grads), _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def moe_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
+    """outs None: in place."""
+    _call("moe_grad_clip", grad_list(grads, outs), len(grads), float(max_norm), _ptr(norm), _ptr(ws), _nbytes(ws),
+          _stream(stream))

@@ -6,7 +6,10 @@
 
 #include <cstdint>
 
+#include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "common.h"
 #include "moe.h"
@@ -52,6 +55,82 @@ int from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 // The shared expert's dims: one expert, every token routed to it once.
 bool is_shared(const Dims& D) { return D.E == 1 && D.K == 1; }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && p < q + nb && q < p + na;
+}
+
+// Bytes of an [N, H] tensor of the element type.
+size_t row_bytes(const Dims& D) { return size_t(D.N) * size_t(D.H) * (D.dtype == MOE_BF16 ? 2 : 4); }
+
+// The dims of a decoding call and of its shared expert (may be null).
+int check_decode(const moe_dims* d, const moe_dims* ds, Dims* D, int64_t* Fs) {
+  int st = check_dims(d, D);
+  if (st != MOE_OK) return st;
+  *Fs = 0;
+  if (ds != nullptr) {
+    Dims S;
+    st = check_dims(ds, &S);
+    if (st != MOE_OK) return st;
+    if (!is_shared(S) || S.N != D->N || S.H != D->H || S.dtype != D->dtype) return MOE_EINVAL;
+    *Fs = S.F;
+  }
+  return D->N > MOE_DECODE_MAX_TOKENS ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+// A list of gradients (out: the outputs count too).
+int check_grads(const moe_grad* g, int64_t count, bool out) {
+  if (count < 0 || (count > 0 && g == nullptr)) return MOE_EINVAL;
+  if (count > MOE_GRAD_MAX_TENSORS) return MOE_EUNSUPPORTED;
+  int64_t total = 0;
+  for (int64_t t = 0; t < count; ++t) {
+    const moe_grad& q = g[t];
+    if (q.n < 0) return MOE_EINVAL;
+    if (q.in_dtype != MOE_F32 && q.in_dtype != MOE_BF16) return MOE_EINVAL;
+    if (out && q.out_dtype != MOE_F32 && q.out_dtype != MOE_BF16) return MOE_EINVAL;
+    if (q.n == 0) continue;
+    const uintptr_t ie = q.in_dtype == MOE_BF16 ? 1 : 3, oe = q.out_dtype == MOE_BF16 ? 1 : 3;
+    if (q.in == nullptr || (reinterpret_cast<uintptr_t>(q.in) & ie) != 0) return MOE_EINVAL;
+    if (out && (q.out == nullptr || (reinterpret_cast<uintptr_t>(q.out) & oe) != 0)) return MOE_EINVAL;
+    if (q.n > (int64_t(1) << 44)) return MOE_EUNSUPPORTED;
+    total += q.n + moe_launch::grad_chunk();
+    if (total > (int64_t(1) << 44)) return MOE_EUNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+// Outputs that overlap anything but their own input in place.
+int check_grad_overlaps(const moe_grad* g, int64_t count, const void* norm, const void* ws) {
+  struct Span {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  std::unique_ptr<Span[]> s(new (std::nothrow) Span[size_t(2 * count + 2)]);
+  if (s == nullptr) return MOE_EUNSUPPORTED;
+  size_t m = 0;
+  auto add = [&](const void* p, uintptr_t bytes, bool written) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    s[m++] = Span{lo, lo + bytes, written};
+  };
+  for (int64_t t = 0; t < count; ++t) {
+    const moe_grad& q = g[t];
+    if (q.n == 0) continue;
+    add(q.out, uintptr_t(q.n) * (q.out_dtype == MOE_BF16 ? 2 : 4), true);
+    if (q.in != q.out || q.in_dtype != q.out_dtype) add(q.in, uintptr_t(q.n) * (q.in_dtype == MOE_BF16 ? 2 : 4), false);
+  }
+  add(norm, sizeof(float), true);
+  add(ws, MOE_GRAD_WS_BYTES, true);
+  std::sort(s.get(), s.get() + m, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t any = 0, written = 0;  // ends of the spans so far
+  for (size_t i = 0; i < m; ++i) {
+    if (s[i].lo < (s[i].written ? any : written)) return MOE_EINVAL;
+    any = std::max(any, s[i].hi);
+    if (s[i].written) written = std::max(written, s[i].hi);
+  }
+  return MOE_OK;
+}
+
 #define MOE_CHECK_DIMS(d, D)            \
   Dims D;                               \
   {                                     \
@@ -95,6 +174,7 @@ size_t moe_workspace_bytes(const moe_dims* d, int32_t entry) {
     case MOE_ENTRY_SHARED_FFN: return is_shared(D) ? moe_launch::shared_ffn_ws(D) : size_t(-1);
     case MOE_ENTRY_SHARED_FFN_BWD: return is_shared(D) ? moe_launch::shared_ffn_bwd_ws(D) : size_t(-1);
     case MOE_ENTRY_ROUTE_META: return moe_launch::route_meta_ws(D);
+    case MOE_ENTRY_RMS_NORM_BWD: return D.H <= MOE_NORM_MAX_H ? moe_launch::rms_norm_bwd_ws(D) : size_t(-1);
     default: return size_t(-1);
   }
 }
@@ -379,6 +459,93 @@ int moe_route_bwd_aux(const moe_dims* d, const void* x, const int32_t* topk_idx,
   if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;
   return from_hip(moe_launch::route_bwd_aux(D, x, topk_idx, gates, dgates, probs, counts, aux_scale, dlogits, dw_r,
                                             ws, stream));
+}
+
+size_t moe_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds) {
+  Dims D;
+  int64_t Fs;
+  if (check_decode(d, ds, &D, &Fs) != MOE_OK) return size_t(-1);
+  return D.N == 0 ? 0 : moe_launch::decode_ws(D, Fs);
+}
+
+int moe_decode(const moe_dims* d, const void* x, const void* w_r, const float* logit_bias, const void* w_gate,
+               const void* w_up, const void* w_down, const moe_dims* ds, const void* ws_gate, const void* ws_up,
+               const void* ws_down, int32_t* topk_idx, float* gates, void* y, void* ws, size_t ws_bytes,
+               hipStream_t stream) {
+  Dims D;
+  int64_t Fs;
+  const int st = check_decode(d, ds, &D, &Fs);
+  if (st != MOE_OK) return st;
+  if (!ptrs_ok(x, w_r, w_gate, w_up, w_down, topk_idx, gates, y)) return MOE_EINVAL;
+  if (logit_bias != nullptr && !aligned16(logit_bias)) return MOE_EINVAL;
+  if (ds != nullptr ? !ptrs_ok(ws_gate, ws_up, ws_down)
+                    : (ws_gate != nullptr || ws_up != nullptr || ws_down != nullptr))
+    return MOE_EINVAL;
+  if (overlap(x, row_bytes(D), y, row_bytes(D))) return MOE_EINVAL;
+  if (D.N == 0) return MOE_OK;
+  const size_t need = moe_launch::decode_ws(D, Fs);
+  if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;
+  return from_hip(moe_launch::decode(D, x, w_r, logit_bias, w_gate, w_up, w_down, Fs, ws_gate, ws_up, ws_down,
+                                     topk_idx, gates, y, ws, stream));
+}
+
+int moe_rms_norm(const moe_dims* d, const void* x, const void* residual, const void* weight, float eps, void* h,
+                 void* y, float* rstd, hipStream_t stream) {
+  MOE_CHECK_DIMS(d, D);
+  if (D.H > MOE_NORM_MAX_H) return MOE_EUNSUPPORTED;
+  if (!std::isfinite(eps) || eps <= 0.f) return MOE_EINVAL;
+  if (!ptrs_ok(x, weight, y)) return MOE_EINVAL;
+  if ((residual == nullptr) != (h == nullptr)) return MOE_EINVAL;
+  if (residual != nullptr && !ptrs_ok(residual, h)) return MOE_EINVAL;
+  if (rstd != nullptr && !aligned16(rstd)) return MOE_EINVAL;
+  const size_t b = row_bytes(D), wb = b / size_t(D.N > 0 ? D.N : 1), rb = size_t(D.N) * 4;
+  if (overlap(y, b, x, b) || overlap(y, b, weight, wb)) return MOE_EINVAL;
+  if (residual != nullptr) {
+    if (overlap(y, b, residual, b) || overlap(y, b, h, b) || overlap(h, b, weight, wb)) return MOE_EINVAL;
+    if ((h != x && overlap(h, b, x, b)) || (h != residual && overlap(h, b, residual, b))) return MOE_EINVAL;
+  }
+  if (rstd != nullptr &&
+      (overlap(rstd, rb, x, b) || overlap(rstd, rb, y, b) || overlap(rstd, rb, weight, wb) ||
+       (residual != nullptr && (overlap(rstd, rb, residual, b) || overlap(rstd, rb, h, b)))))
+    return MOE_EINVAL;
+  if (D.N == 0) return MOE_OK;
+  return from_hip(moe_launch::rms_norm(D, x, residual, weight, eps, h, y, rstd, stream));
+}
+
+int moe_rms_norm_bwd(const moe_dims* d, const void* dy, const void* h, const void* weight, const float* rstd,
+                     const void* dh, void* dx, float* dweight, void* ws, size_t ws_bytes, hipStream_t stream) {
+  MOE_CHECK_DIMS(d, D);
+  if (D.H > MOE_NORM_MAX_H) return MOE_EUNSUPPORTED;
+  if (!ptrs_ok(dy, h, weight, rstd, dx, dweight)) return MOE_EINVAL;
+  if (dh != nullptr && !aligned16(dh)) return MOE_EINVAL;
+  const size_t b = row_bytes(D), wb = b / size_t(D.N > 0 ? D.N : 1), rb = size_t(D.N) * 4;
+  if ((dx != dy && overlap(dx, b, dy, b)) || (dh != nullptr && dx != dh && overlap(dx, b, dh, b)) ||
+      overlap(dx, b, h, b) || overlap(dx, b, weight, wb) || overlap(dx, b, rstd, rb))
+    return MOE_EINVAL;
+  if (D.N == 0) return MOE_OK;
+  const size_t need = moe_launch::rms_norm_bwd_ws(D);
+  if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;
+  return from_hip(moe_launch::rms_norm_bwd(D, dy, h, weight, rstd, dh, dx, dweight, ws, stream));
+}
+
+int moe_grad_norm(const moe_grad* list, int64_t count, float* norm, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const int st = check_grads(list, count, false);
+  if (st != MOE_OK) return st;
+  if (norm == nullptr || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return MOE_EINVAL;
+  if (ws == nullptr || ws_bytes < MOE_GRAD_WS_BYTES || !aligned16(ws)) return MOE_EWORKSPACE;
+  return from_hip(moe_launch::grad_norm(list, int(count), norm, ws, stream));
+}
+
+int moe_grad_clip(const moe_grad* list, int64_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                  hipStream_t stream) {
+  int st = check_grads(list, count, true);
+  if (st != MOE_OK) return st;
+  if (!std::isfinite(max_norm) || max_norm < 0.f) return MOE_EINVAL;
+  if (norm == nullptr || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return MOE_EINVAL;
+  if (ws == nullptr || ws_bytes < MOE_GRAD_WS_BYTES || !aligned16(ws)) return MOE_EWORKSPACE;
+  st = check_grad_overlaps(list, count, norm, ws);
+  if (st != MOE_OK) return st;
+  return from_hip(moe_launch::grad_clip(list, int(count), max_norm, norm, ws, stream));
 }
 
 }  // extern "C"

@@ -222,4 +222,22 @@ hipError_t shared_ffn(const Dims& ds, const void* x, const void* wg, const void*
 hipError_t shared_ffn_bwd(const Dims& ds, const void* x, const void* dy, const void* wg, const void* wu,
                           const void* wd, const void* g, const void* u, const void* a, void* dg, void* du, void* dxs,
                           float* dwg, float* dwu, float* dwd, void* ws, hipStream_t s);
+
+// The layer for few tokens; Fs = 0: no shared expert.
+size_t decode_ws(const Dims& d, int64_t Fs);
+hipError_t decode(const Dims& d, const void* x, const void* w_r, const float* bias, const void* wg, const void* wu,
+                  const void* wd, int64_t Fs, const void* swg, const void* swu, const void* swd, int32_t* topk,
+                  float* gates, void* y, void* ws, hipStream_t s);
+
+// Residual addition and RMS norm; residual and h null: h is x.
+hipError_t rms_norm(const Dims& d, const void* x, const void* residual, const void* weight, float eps, void* h,
+                    void* y, float* rstd, hipStream_t s);
+size_t rms_norm_bwd_ws(const Dims& d);
+hipError_t rms_norm_bwd(const Dims& d, const void* dy, const void* h, const void* weight, const float* rstd,
+                        const void* dh, void* dx, float* dw, void* ws, hipStream_t s);
+
+// Global gradient norm and clipping over a checked list in host memory.
+int64_t grad_chunk();  // elements per chunk; a launch counts its chunks in 31 bits
+hipError_t grad_norm(const moe_grad* g, int count, float* norm, void* ws, hipStream_t s);
+hipError_t grad_clip(const moe_grad* g, int count, float max_norm, float* norm, void* ws, hipStream_t s);
 }  // namespace moe_launch

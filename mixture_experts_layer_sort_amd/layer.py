@@ -21,12 +21,21 @@ its gradients and moe_permute_bwd_add adds its input gradient to dx.
 
 Nothing is read back to the host between the calls.  ``MoEFunction`` wraps
 one runner call pair as a ``torch.autograd.Function``.
+
+Around the layer:
+  MoEDecodeRunner        the whole forward for a few tokens (moe_decode)
+  MoENormRunner, moe_rms_norm   residual addition and RMS norm in front of the
+                         layer, forward and backward (moe_rms_norm, moe_rms_norm_bwd)
+  moe_grad_norm, moe_clip_grads   the global 2-norm of a list of gradients, and
+                         clipping by it (moe_grad_norm, moe_grad_clip)
 """
 from __future__ import annotations
 
-from typing import Optional
+import contextlib
+from typing import Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -270,6 +279,18 @@ class MoELayerRunner:
             out.update(dw_gate_s=self.dw_gate_s, dw_up_s=self.dw_up_s, dw_down_s=self.dw_down_s)
         return out
 
+    def clip_grads(self, max_norm: float, extra: Sequence[torch.Tensor] = ()):
+        """Scale the weight gradients of the last backward, and the tensors of
+        ``extra`` (the norm's gradient, other layers'), in place so that their
+        joint 2-norm is at most max_norm; returns the norm before, a device
+        tensor [1].  Runs on the current stream."""
+        if not self.with_backward:
+            raise RuntimeError("runner was built without backward buffers")
+        grads = [self.dw_r, self.dw_gate, self.dw_up, self.dw_down]
+        if self.shared_ffn is not None:
+            grads += [self.dw_gate_s, self.dw_up_s, self.dw_down_s]
+        return moe_clip_grads(grads + list(extra), max_norm)[1]
+
 
 class MoEFunction(torch.autograd.Function):
     """y = MoE(x) with gradients for x, W_r, W_gate, W_up, W_down and, with a
@@ -327,3 +348,230 @@ def moe_layer(x, w_r, w_gate, w_up, w_down, K: int, bias=None, *, capacity: Opti
     y, aux = MoEFunction.apply(x, w_r, w_gate, w_up, w_down, ws[0], ws[1], ws[2], K, bias, capacity, aux_alpha,
                                aux_grad, dw_gather)
     return (y, aux) if aux_alpha is not None else y
+
+
+# ------------------------------------------------------------ around the layer
+def _cuda_device(device) -> torch.device:
+    dev = torch.device(device)
+    return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
+
+
+def _on(dev: torch.device):
+    """The launches of a call go to the tensors' device, whatever device is current."""
+    if dev.type != "cuda" or torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _expect(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: torch.device):
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class MoEDecodeRunner:
+    """The layer's forward for the few tokens of a decoding step: buffers for up
+    to ``max_tokens`` (at most MOE_DECODE_MAX_TOKENS) tokens.  ``forward`` takes
+    any number up to that; its outputs are the runner's own buffers and live
+    until the next call, so one runner serves one call at a time."""
+
+    def __init__(self, max_tokens: int, H: int, F: int, E: int, K: int, dtype: torch.dtype, device="cuda",
+                 shared_ffn: Optional[int] = None):
+        self.max_tokens, self.H, self.F, self.E, self.K = max_tokens, H, F, E, K
+        self.dtype, self.shared_ffn = dtype, shared_ffn
+        code = L.dtype_code(dtype)
+        self._dims = [(L.dims(n, H, F, E, K, code), None if shared_ffn is None else L.dims(n, H, shared_ffn, 1, 1, code))
+                      for n in range(max_tokens + 1)]
+        # how the work is cut, and so the scratch, depends on the number of tokens
+        need = [L.moe_decode_workspace_bytes(*p) for p in self._dims]
+        if not need or max(need) == 2 ** 64 - 1:
+            raise L.MoEError("moe_decode_workspace_bytes",
+                             L.MOE_EUNSUPPORTED if max_tokens > L.MOE_DECODE_MAX_TOKENS else L.MOE_EINVAL)
+        self.device = dev = _cuda_device(device)
+        self.ws = torch.empty((max(16, max(need)),), dtype=torch.uint8, device=dev)
+        self._topk = torch.empty((max_tokens, K), dtype=torch.int32, device=dev)
+        self._gates = torch.empty((max_tokens, K), dtype=torch.float32, device=dev)
+        self._y = torch.empty((max_tokens, H), dtype=dtype, device=dev)
+        self.topk, self.gates, self.y = self._topk, self._gates, self._y
+
+    def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None, shared=None):
+        """Returns y [n, H] of x [n, H], n <= max_tokens; topk and gates [n, K]
+        are attributes.  ``shared`` as in MoELayerRunner.forward."""
+        H, F, E, dt, dev = self.H, self.F, self.E, self.dtype, self.device
+        n = x.shape[0]
+        if n > self.max_tokens:
+            raise ValueError(f"{n} tokens, the runner holds {self.max_tokens}")
+        if (shared is None) != (self.shared_ffn is None):
+            raise ValueError("shared weights must be given exactly when the runner has a shared expert")
+        _expect("x", x, (n, H), dt, dev)
+        _expect("w_r", w_r, (H, E), dt, dev)
+        _expect("w_gate", w_gate, (E, H, F), dt, dev)
+        _expect("w_up", w_up, (E, H, F), dt, dev)
+        _expect("w_down", w_down, (E, F, H), dt, dev)
+        if bias is not None:
+            _expect("bias", bias, (E,), torch.float32, dev)
+        sg = su = sd = None
+        if shared is not None:
+            sg, su, sd = shared
+            Fs = self.shared_ffn
+            _expect("shared w_gate", sg, (H, Fs), dt, dev)
+            _expect("shared w_up", su, (H, Fs), dt, dev)
+            _expect("shared w_down", sd, (Fs, H), dt, dev)
+        if n != self.y.shape[0]:
+            self.topk, self.gates, self.y = self._topk[:n], self._gates[:n], self._y[:n]
+        d, ds = self._dims[n]
+        if n:
+            with _on(dev):
+                L.moe_decode(d, x, w_r, bias, w_gate, w_up, w_down, ds, sg, su, sd, self.topk, self.gates, self.y,
+                             self.ws, stream)
+        return self.y
+
+
+class MoENormRunner:
+    """Residual addition and RMS norm of up to N token rows of H values, in
+    buffers of its own: h (the new residual stream), y and rstd; dx and dweight
+    with ``backward``.  One call at a time, as the layer's runner."""
+
+    def __init__(self, N: int, H: int, dtype: torch.dtype, device="cuda", eps: float = 1e-6, backward: bool = True):
+        self.N, self.H, self.dtype, self.eps, self.with_backward = N, H, dtype, eps, backward
+        self.device = dev = _cuda_device(device)
+        # the norm uses N, H and the type of the layer's dims; F, E and K only have to be legal
+        self.d = L.dims(N, H, 128, 1, 1, L.dtype_code(dtype))
+        need = L.moe_workspace_bytes(self.d, L.MOE_ENTRY_RMS_NORM_BWD)
+        if need == 2 ** 64 - 1:
+            raise L.MoEError("moe_workspace_bytes", L.MOE_EUNSUPPORTED if H > L.MOE_NORM_MAX_H else L.MOE_EINVAL)
+        self._h = torch.empty((N, H), dtype=dtype, device=dev)
+        self._y = torch.empty((N, H), dtype=dtype, device=dev)
+        self._rstd = torch.empty((N,), dtype=torch.float32, device=dev)
+        if backward:
+            self._dx = torch.empty((N, H), dtype=dtype, device=dev)
+            self.dweight = torch.empty((H,), dtype=torch.float32, device=dev)
+            self.ws = torch.empty((max(16, need),), dtype=torch.uint8, device=dev)
+        self.h, self.y, self.rstd = self._h, self._y, self._rstd
+        self.inputs = None
+
+    def forward(self, x, weight, residual=None, stream=None):
+        """Returns y of x [n, H], n <= N; h (x itself without a residual) and
+        rstd are attributes."""
+        n = x.shape[0]
+        if n > self.N:
+            raise ValueError(f"{n} rows, the runner holds {self.N}")
+        _expect("x", x, (n, self.H), self.dtype, self.device)
+        _expect("weight", weight, (self.H,), self.dtype, self.device)
+        if residual is not None:
+            _expect("residual", residual, (n, self.H), self.dtype, self.device)
+        if n != self.d.N:
+            self.d = L.dims(n, self.H, 128, 1, 1, L.dtype_code(self.dtype))
+        if n != self.y.shape[0]:
+            self.y, self.rstd = self._y[:n], self._rstd[:n]
+        h = None if residual is None else (self._h if n == self.N else self._h[:n])
+        self.h = x if h is None else h
+        if n:
+            with _on(self.device):
+                L.moe_rms_norm(self.d, x, residual, weight, self.eps, h, self.y, self.rstd, stream)
+        self.inputs = weight
+        return self.y
+
+    def backward(self, dy, dh=None, stream=None):
+        """(dx, dweight) of the last forward: dx is the gradient of x and of the
+        residual, dweight float32.  dh: the gradient that reaches h along the
+        residual stream."""
+        if not self.with_backward:
+            raise RuntimeError("runner was built without backward buffers")
+        if self.inputs is None:
+            raise RuntimeError("backward before forward")
+        n = self.y.shape[0]
+        _expect("dy", dy, (n, self.H), self.dtype, self.device)
+        if dh is not None:
+            _expect("dh", dh, (n, self.H), self.dtype, self.device)
+        dx = self._dx if n == self.N else self._dx[:n]
+        if n:
+            with _on(self.device):
+                L.moe_rms_norm_bwd(self.d, dy, self.h, self.inputs, self.rstd, dh, dx, self.dweight, self.ws, stream)
+        else:
+            self.dweight.zero_()
+        return dx, self.dweight
+
+
+class MoERMSNormFunction(torch.autograd.Function):
+    """(y, h) of x and a residual, or y of x alone, with gradients for x, the
+    weight and the residual."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        H = x.shape[-1]
+        _expect("weight", weight, (H,), x.dtype, x.device)
+        if residual is not None:
+            _expect("residual", residual, x.shape, x.dtype, x.device)
+        x = x.contiguous()
+        d = L.dims(x.numel() // H if H else 0, H, 128, 1, 1, L.dtype_code(x.dtype))
+        y = torch.empty_like(x)
+        rstd = torch.empty((d.N,), dtype=torch.float32, device=x.device)
+        h = None if residual is None else torch.empty_like(x)
+        with _on(x.device):
+            if d.N:
+                L.moe_rms_norm(d, x, None if residual is None else residual.contiguous(), weight.contiguous(), eps, h,
+                               y, rstd)
+        ctx.save_for_backward(x if h is None else h, weight, rstd)
+        ctx.d = d
+        ctx.set_materialize_grads(False)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, weight, rstd = ctx.saved_tensors
+        d = ctx.d
+        if dy is None:
+            return dh, None, dh, None
+        dx = torch.empty_like(h)
+        dw = torch.zeros((d.H,), dtype=torch.float32, device=h.device) if d.N == 0 else torch.empty(
+            (d.H,), dtype=torch.float32, device=h.device)
+        if d.N:
+            ws = torch.empty((L.moe_workspace_bytes(d, L.MOE_ENTRY_RMS_NORM_BWD),), dtype=torch.uint8, device=h.device)
+            with _on(h.device):
+                L.moe_rms_norm_bwd(d, dy.contiguous(), h, weight.contiguous(), rstd,
+                                   None if dh is None else dh.contiguous(), dx, dw, ws)
+        return dx, dw.to(weight.dtype), dx if ctx.needs_input_grad[2] else None, None
+
+
+def moe_rms_norm(x, weight, residual=None, eps: float = 1e-6):
+    """RMS norm of the rows of x [..., H] with autograd support, the step in
+    front of moe_layer: y = x / sqrt(mean(x^2) + eps) * weight.  With a
+    residual, h = x + residual is normalised instead and (y, h) is returned, h
+    being the residual stream that the layer's output is added to."""
+    return MoERMSNormFunction.apply(x, weight, residual, eps)
+
+
+def _grad_call(grads, outs):
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(grads) != len(outs):
+        raise ValueError("as many outputs as gradients are needed")
+    dev = grads[0].device if grads else _cuda_device("cuda")
+    for t in (*grads, *outs):
+        if t.device != dev:
+            raise ValueError("all gradients and outputs must be on one device")
+    ws = torch.empty((L.MOE_GRAD_WS_BYTES + 16,), dtype=torch.uint8, device=dev)
+    # workspace and result in one buffer
+    return grads, outs, dev, ws[:L.MOE_GRAD_WS_BYTES], ws[L.MOE_GRAD_WS_BYTES:L.MOE_GRAD_WS_BYTES + 4].view(torch.float32)
+
+
+def moe_grad_norm(grads: Sequence[torch.Tensor]):
+    """The 2-norm over all elements of a list of gradients (float32 or bfloat16,
+    contiguous), a device tensor [1]; nothing is read back to the host."""
+    grads, _, dev, ws, norm = _grad_call(grads, None)
+    with _on(dev):
+        L.moe_grad_norm(grads, norm, ws)
+    return norm
+
+
+def moe_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None):
+    """Scale a list of gradients by min(1, max_norm / (norm + 1e-6)), norm their
+    joint 2-norm, in place or into ``out`` (tensors of the same sizes, float32
+    or bfloat16: an optimiser's gradients from float32 accumulators).  Returns
+    (outputs, norm), norm a device tensor [1]; nothing is read back to the host.
+    An output may be its own gradient; any other overlap is refused."""
+    grads, outs, dev, ws, norm = _grad_call(grads, out)
+    with _on(dev):
+        L.moe_grad_clip(grads, outs, max_norm, norm, ws)
+    return outs, norm
