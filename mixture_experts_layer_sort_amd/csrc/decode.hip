@@ -179,7 +179,7 @@ template <int CW, int NA> struct Panel<bf16_t, CW, NA> {
   };
   __device__ __forceinline__ void load(const bf16_t* p, int64_t ld) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const raw_t*>(p + j * ld);
+    for (int j = 0; j < 8; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const raw_t*>(p + j * ld));
   }
   template <int MT>
   __device__ __forceinline__ void multiply(const A (&a)[MT], f32x4_t (&acc)[MT][CW]) const {
@@ -212,7 +212,7 @@ template <int CW> struct Panel<float, CW, 1> {
   };
   __device__ __forceinline__ void load(const float* p, int64_t ld) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const raw_t*>(p + j * ld);
+    for (int j = 0; j < 8; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const raw_t*>(p + j * ld));
   }
   template <int MT>
   __device__ __forceinline__ void multiply(const A (&a)[MT], f32x4_t (&acc)[MT][CW]) const {

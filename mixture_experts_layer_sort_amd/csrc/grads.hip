@@ -18,12 +18,11 @@
 namespace {
 using namespace moe;
 
-constexpr int kTable = 64;                    // tensors in one launch
+constexpr int kTable = 64;      // tensors in one launch
 constexpr int kThreads = 256;
-constexpr int kGroup = 8;                     // elements a thread handles at once
-constexpr int kUnroll = 4;
-constexpr int64_t kChunk = kThreads * kGroup * kUnroll;
-constexpr int kMaxPart = 1024;                // partial sums (workgroups of the norm)
+constexpr int kChunk = 4096;    // elements
+constexpr uint32_t kMaxBlocks = 1 << 20;  // workgroups of a scaling launch
+constexpr int kMaxPart = 1024;  // partial sums (workgroups of the norm)
 static_assert(kMaxPart * sizeof(double) == MOE_GRAD_WS_BYTES, "the header states the workspace");
 
 struct Table {
@@ -35,23 +34,6 @@ struct Table {
   int count;
 };
 
-// Elements [i, i + 8) of a 16-byte aligned tensor, i a multiple of 8.
-__device__ __forceinline__ void load8(const void* p, int dtype, int64_t i, float* v) {
-  if (dtype == MOE_BF16) {
-    Vec16<bf16_t>::load(static_cast<const bf16_t*>(p) + i, v);
-  } else {
-    Vec16<float>::load(static_cast<const float*>(p) + i, v);
-    Vec16<float>::load(static_cast<const float*>(p) + i + 4, v + 4);
-  }
-}
-__device__ __forceinline__ void store8(void* p, int dtype, int64_t i, const float* v) {
-  if (dtype == MOE_BF16) {
-    Vec16<bf16_t>::store(static_cast<bf16_t*>(p) + i, v);
-  } else {
-    Vec16<float>::store(static_cast<float*>(p) + i, v);
-    Vec16<float>::store(static_cast<float*>(p) + i + 4, v + 4);
-  }
-}
 __device__ __forceinline__ float load1(const void* p, int dtype, int64_t i) {
   return dtype == MOE_BF16 ? bf16_to_f32(static_cast<const bf16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
@@ -62,30 +44,74 @@ __device__ __forceinline__ void store1(void* p, int dtype, int64_t i, float v) {
     static_cast<float*>(p)[i] = v;
 }
 
-// Calls f8(tensor, i) for the whole groups of 8 elements and f1(tensor, i) for
-// the single ones (tails, tensors that are not 16-byte aligned) of the chunks
-// that this workgroup takes.
-template <typename F8, typename F1>
-__device__ __forceinline__ void for_chunks(const Table& tab, F8 f8, F1 f1) {
-  int t = 0;
+// V consecutive elements in one access of 8 or 16 bytes.
+template <typename T, int V> struct Group {
+  typedef T vec_t __attribute__((ext_vector_type(V)));
+  vec_t v;
+  __device__ __forceinline__ void load(const T* p) { v = __builtin_nontemporal_load(reinterpret_cast<const vec_t*>(p)); }
+  __device__ __forceinline__ float get(int i) const { return Elt<T>::to_f32(v[i]); }
+  __device__ __forceinline__ void set(int i, float f) { v[i] = Elt<T>::from_f32(f); }
+  __device__ __forceinline__ void store(T* p) const {
+    __builtin_nontemporal_store(v, reinterpret_cast<vec_t*>(p));
+  }
+};
+
+// acc += squares of a whole chunk.
+template <typename T>
+__device__ __forceinline__ void chunk_squares(const void* in, int64_t lo, double& acc) {
+  constexpr int V = Vec16<T>::n, U = kChunk / (kThreads * V);
+  const T* p = static_cast<const T*>(in) + lo + threadIdx.x * V;
+  Group<T, V> g[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) g[u].load(p + u * kThreads * V);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const double f = g[u].get(i);
+      acc = fma(f, f, acc);
+    }
+}
+
+// A whole chunk, scaled by factor(), which is asked for once the loads are on
+// their way.
+template <typename I, typename O, typename F>
+__device__ __forceinline__ void chunk_scale(const void* in, void* out, int64_t lo, F factor) {
+  constexpr int V = sizeof(I) == 2 && sizeof(O) == 2 ? 8 : 4, U = kChunk / (kThreads * V);
+  const I* p = static_cast<const I*>(in) + lo + threadIdx.x * V;
+  O* q = static_cast<O*>(out) + lo + threadIdx.x * V;
+  Group<I, V> g[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) g[u].load(p + u * kThreads * V);
+  const float coef = factor();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    Group<O, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.set(i, coef * g[u].get(i));
+    o.store(q + u * kThreads * V);
+  }
+}
+
+// Calls whole(tensor, first element) for the whole chunks of 16-byte aligned
+// tensors and rest(tensor, first, end) for the other chunks, among those that
+// this workgroup takes.  REVERSE: from the last chunk on.
+template <bool REVERSE, typename W, typename R>
+__device__ __forceinline__ void for_chunks(const Table& tab, W whole, R rest) {
   const uint32_t total = tab.first[tab.count];
-  for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
-    while (c >= tab.first[t + 1]) ++t;
+  int t = REVERSE ? tab.count - 1 : 0;
+  for (uint32_t b = blockIdx.x; b < total; b += gridDim.x) {
+    const uint32_t c = REVERSE ? total - 1 - b : b;
+    if (REVERSE)
+      while (c < tab.first[t]) --t;
+    else
+      while (c >= tab.first[t + 1]) ++t;
     const int64_t lo = int64_t(c - tab.first[t]) * kChunk;
     const int64_t n = tab.n[t];
-    if (tab.vec[t]) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int64_t i = lo + (int64_t(u) * kThreads + threadIdx.x) * kGroup;
-        if (i + kGroup <= n)
-          f8(t, i);
-        else
-          for (int64_t j = i; j < n; ++j) f1(t, j);
-      }
-    } else {
-      const int64_t hi = min(n, lo + kChunk);
-      for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) f1(t, i);
-    }
+    if (tab.vec[t] && lo + kChunk <= n)
+      whole(t, lo);
+    else
+      rest(t, lo, min(n, lo + kChunk));
   }
 }
 
@@ -108,17 +134,19 @@ __device__ __forceinline__ double block_sum64(double v) {
 
 __global__ __launch_bounds__(kThreads) void k_grad_squares(Table tab, double* __restrict__ part, int add) {
   double acc = 0.0;
-  for_chunks(
+  for_chunks<false>(
       tab,
-      [&](int t, int64_t i) {
-        float v[kGroup];
-        load8(tab.in[t], tab.in_dtype[t], i, v);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) acc = fma(double(v[j]), double(v[j]), acc);
+      [&](int t, int64_t lo) {
+        if (tab.in_dtype[t] == MOE_BF16)
+          chunk_squares<bf16_t>(tab.in[t], lo, acc);
+        else
+          chunk_squares<float>(tab.in[t], lo, acc);
       },
-      [&](int t, int64_t i) {
-        const double v = load1(tab.in[t], tab.in_dtype[t], i);
-        acc = fma(v, v, acc);
+      [&](int t, int64_t lo, int64_t hi) {
+        for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
+          const double v = load1(tab.in[t], tab.in_dtype[t], i);
+          acc = fma(v, v, acc);
+        }
       });
   acc = block_sum64(acc);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + acc : acc;
@@ -138,20 +166,39 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const double* __restrict
 
 __global__ __launch_bounds__(kThreads) void k_grad_scale(Table tab, const double* __restrict__ part, int P,
                                                          float max_norm, float* __restrict__ norm) {
-  const double v = norm_of(part, P);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = float(v);
-  const double c = double(max_norm) / (v + 1e-6);
-  const float coef = float(c > 1.0 ? 1.0 : c);  // NaN stays NaN
-  for_chunks(
+  // The same factor in every workgroup, found while its first chunk is loading
+  // (all threads ask for it together: it holds a barrier).
+  float coef = 0.f;
+  bool known = false;
+  auto factor = [&]() {
+    if (!known) {
+      const double v = norm_of(part, P);
+      if (blockIdx.x == 0 && threadIdx.x == 0) *norm = float(v);
+      const double c = double(max_norm) / (v + 1e-6);
+      coef = float(c > 1.0 ? 1.0 : c);  // NaN stays NaN
+      known = true;
+    }
+    return coef;
+  };
+  for_chunks<true>(
       tab,
-      [&](int t, int64_t i) {
-        float a[kGroup];
-        load8(tab.in[t], tab.in_dtype[t], i, a);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) a[j] *= coef;
-        store8(tab.out[t], tab.out_dtype[t], i, a);
+      [&](int t, int64_t lo) {
+        const bool bi = tab.in_dtype[t] == MOE_BF16, bo = tab.out_dtype[t] == MOE_BF16;
+        if (bi && bo)
+          chunk_scale<bf16_t, bf16_t>(tab.in[t], tab.out[t], lo, factor);
+        else if (bi)
+          chunk_scale<bf16_t, float>(tab.in[t], tab.out[t], lo, factor);
+        else if (bo)
+          chunk_scale<float, bf16_t>(tab.in[t], tab.out[t], lo, factor);
+        else
+          chunk_scale<float, float>(tab.in[t], tab.out[t], lo, factor);
       },
-      [&](int t, int64_t i) { store1(tab.out[t], tab.out_dtype[t], i, coef * load1(tab.in[t], tab.in_dtype[t], i)); });
+      [&](int t, int64_t lo, int64_t hi) {
+        const float f = factor();
+        for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
+          store1(tab.out[t], tab.out_dtype[t], i, f * load1(tab.in[t], tab.in_dtype[t], i));
+      });
+  factor();  // a workgroup without a chunk: norm is written all the same
 }
 
 // Tensors [from, ...) of the list that fit one launch; returns the next one.
@@ -220,7 +267,7 @@ hipError_t grad_clip(const moe_grad* g, int count, float max_norm, float* norm, 
   int from = 0;
   do {
     from = fill(g, count, from, true, &tab);
-    const uint32_t blocks = std::max(1u, std::min(tab.first[tab.count], 2048u));
+    const uint32_t blocks = std::max(1u, std::min(tab.first[tab.count], kMaxBlocks));
     k_grad_scale<<<dim3(blocks), dim3(kThreads), 0, s>>>(tab, part, P, max_norm, norm);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
