@@ -8,23 +8,28 @@
 // With few rows per expert the weights of the chosen experts are all that
 // matters: they are read once, and HBM bounds the call.  So there is no sort,
 // no row tile list and no staging of weights through LDS:
-//  - A wave reads 32 rows of a weight matrix times 16 * CW columns straight
-//    into registers: lane (g, c) = (lane / 16, lane % 16) takes the CW columns
-//    CW*c .. of rows 8g .. 8g+7, so each row is read as one contiguous segment.
-//    Those eight rows of one column are exactly a lane's share of a 16x16x32
+//  - A wave reads a panel of 32 rows of a weight matrix straight into
+//    registers: lane (g, c) = (lane / 16, lane % 16) takes, of rows 8g .. 8g+7,
+//    16 bytes at c*16 of each of S segments of 256 bytes.  S = 2 puts 512
+//    contiguous bytes of a row on their way at once: reading a matrix in
+//    column strips ran at 6.5 TB/s with 256-byte segments and 7.0 with 512
+//    (1024: 7.0, but half the workgroups), without the streaming hint at 6.
+//  - Those eight rows of one column are exactly a lane's share of a 16x16x32
 //    bf16 matrix operand with column index c, so column i of every lane forms
-//    one operand after packing row pairs (4 byte permutes for 8 values): CW
-//    matrix instructions use up the 32 x 16*CW panel.  float32 needs no packing:
-//    row j of the eight is one operand of a 16x16x4 instruction.
-//  - The other operand holds up to 16 token rows; rows past the expert's last
-//    repeat row 0 and their results are dropped.
+//    one operand after packing row pairs (4 byte permutes for 8 values).
+//    float32 needs no packing: row j of the eight is one operand of a 16x16x4
+//    instruction.
+//  - The other operand holds up to 16 token rows; rows past the last repeat
+//    row 0 and their results are dropped.
 //  - The waves of a workgroup split the contraction; their float32 sums meet
-//    in LDS in a fixed order.
-// The activation silu(g)*u keeps float32 accuracy on its way to the second
-// product: for bf16 it is stored as the sum of two bf16 values (hi + lo).  y is
-// rounded once.  Router logits are summed in float64, so the choice of experts
-// does not depend on the order of the sum.
+//    in LDS in a fixed order, those of several workgroups in the next kernel.
+// gate/up leaves float32 sums; the down kernel forms gate * silu(G) * U as it
+// loads them, for bf16 as the sum of two bf16 values (hi + lo), so the
+// activation keeps float32 accuracy.  y is rounded once.  Router logits are
+// summed in float64, so the choice of experts does not depend on the order of
+// the sum.
 #include <algorithm>
+#include <cmath>
 
 #include "common.h"
 
@@ -33,448 +38,1028 @@ using namespace moe;
 
 constexpr int kTok = MOE_DECODE_MAX_TOKENS;
 constexpr int kSlots = kTok * MOE_MAX_TOPK;
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kNT = kWaves * kWave;
-static_assert(kSlots <= kNT, "one thread per (token, k) slot builds the row lists");
+
+typedef uint32_t words4_t __attribute__((ext_vector_type(4)));
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ router
 
-constexpr int kLogitRows = 128;  // rows of W_r per workgroup
-constexpr int kLogitTok = 8;     // tokens per thread
+constexpr int kLogitWaves = 16;
+constexpr int kLogitRows = 32 * kLogitWaves;  // rows of W_r per workgroup
 
-// Partial logits part[s][n][e] over rows s*128 .. of W_r.  Thread (e, token
-// group, h slice); the h slices meet in LDS.
+// 8 consecutive elements as double.
 template <typename T>
-__global__ __launch_bounds__(256) void k_decode_logits(const T* __restrict__ x, const T* __restrict__ w_r,
-                                                       double* __restrict__ part, int N, int H, int E) {
-  __shared__ float xs[kTok][kLogitRows];
-  __shared__ double red[256 * kLogitTok];
-  const int h0 = blockIdx.x * kLogitRows;
-  const int tid = threadIdx.x;
-  for (int i = tid; i < N * kLogitRows; i += 256)
-    xs[i / kLogitRows][i % kLogitRows] = Elt<T>::load(x + int64_t(i / kLogitRows) * H + h0 + i % kLogitRows);
-  __syncthreads();
-  const int groups = (N + kLogitTok - 1) / kLogitTok;
-  int slices = 1;  // h slices per (expert, group): fill the workgroup
-  while (slices < 32 && 2 * slices * E <= 256) slices *= 2;
-  const int e = tid % E, q = tid / E;  // q: slice
-  for (int g = 0; g < groups; ++g) {
-    double acc[kLogitTok];
+__device__ __forceinline__ void load8_f64(const T* p, double* out) {
+  float v[8];
+  Vec16<T>::load(p, v);
+  if (Vec16<T>::n == 4) Vec16<T>::load(p + 4, v + 4);
 #pragma unroll
-    for (int j = 0; j < kLogitTok; ++j) acc[j] = 0.0;
-    if (q < slices) {
-      const int len = kLogitRows / slices;
-      for (int h = q * len; h < (q + 1) * len; ++h) {
-        const double w = Elt<T>::load(w_r + int64_t(h0 + h) * E + e);
+  for (int j = 0; j < 8; ++j) out[j] = double(v[j]);
+}
+
+// acc += x.W_r for 16 tokens (rows of x) and 16 experts over the 32 rows of W_r
+// from h, on the float64 matrix instruction (16 x 16 x 4): lane (g, c) holds row
+// 8g + j of step j, for token c and for expert e.
+template <typename T>
+__device__ __forceinline__ void logit_panel(const T* __restrict__ px, const T* __restrict__ w_r, int h, int E, int e,
+                                            f64x4_t& acc) {
+  const int g = lane_id() / 16;
+  T w[8];
 #pragma unroll
-        for (int j = 0; j < kLogitTok; ++j) acc[j] = fma(double(xs[min(g * kLogitTok + j, N - 1)][h]), w, acc[j]);
+  for (int j = 0; j < 8; ++j) w[j] = w_r[int64_t(h + 8 * g + j) * E + e];
+  double a[8];
+  load8_f64(px + h + 8 * g, a);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[j], double(Elt<T>::to_f32(w[j])), acc, 0, 0, 0);
+}
+
+// A wave's 16 x 16 sums to red [token][expert]: element r is token 4r + g, expert c.
+__device__ __forceinline__ void park_logits(const f64x4_t& acc, double* red) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) red[(4 * r + lane_id() / 16) * 16 + lane_id() % 16] = acc[r];
+}
+
+// Partial logits part[s][n][e] over rows s*512 .. of W_r for 16 experts.  A wave
+// has 32 rows; the waves' sums meet in LDS in wave order.  The first workgroup
+// of each row range also packs x as xp [H/32][N][32], so that the row operand of
+// a panel is one contiguous piece.
+template <typename T>
+__global__ __launch_bounds__(kLogitWaves * kWave) void k_decode_logits(const T* __restrict__ x,
+                                                                      const T* __restrict__ w_r,
+                                                                      double* __restrict__ part, T* __restrict__ xp,
+                                                                      int N, int H, int E) {
+  __shared__ double red[kLogitWaves][256];
+  const int wave = threadIdx.x / kWave, g = lane_id() / 16, c = lane_id() % 16;
+  const int e0 = blockIdx.y * 16;
+  const int h = blockIdx.x * kLogitRows + wave * 32;
+  const bool live = h < H;  // the same in the whole wave: H is a multiple of 128
+  for (int n0 = 0; n0 < N; n0 += 16) {
+    f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
+    const int n = min(n0 + c, N - 1);
+    if (live) {
+      const T* px = x + int64_t(n) * H;
+      logit_panel(px, w_r, h, E, min(e0 + c, E - 1), acc);
+      if (blockIdx.y == 0 && n == n0 + c) {
+        const uint4* from = reinterpret_cast<const uint4*>(px + h + 8 * g);
+        uint4* to = reinterpret_cast<uint4*>(xp + (int64_t(h / 32) * N + n) * 32 + 8 * g);
+#pragma unroll
+        for (int j = 0; j < 8 * int(sizeof(T)) / 16; ++j) to[j] = from[j];
       }
-#pragma unroll
-      for (int j = 0; j < kLogitTok; ++j) red[(q * kLogitTok + j) * E + e] = acc[j];
     }
+    park_logits(acc, red[wave]);
     __syncthreads();
-    for (int i = tid; i < kLogitTok * E; i += 256) {
-      const int n = g * kLogitTok + i / E;
-      if (n < N) {
-        double v = 0.0;
-        for (int s = 0; s < slices; ++s) v += red[s * kLogitTok * E + i];
-        part[(int64_t(blockIdx.x) * N + n) * E + i % E] = v;
-      }
+    const int tok = n0 + threadIdx.x / 16, ex = e0 + threadIdx.x % 16;
+    if (threadIdx.x < 256 && tok < N && ex < E) {
+      double v = 0.0;
+#pragma unroll
+      for (int i = 0; i < kLogitWaves; ++i) v += red[i][threadIdx.x];
+      part[(int64_t(blockIdx.x) * N + tok) * E + ex] = v;
     }
     __syncthreads();
   }
 }
 
-// Top-K and gates of token blockIdx.x: expert e's place is the number of
-// experts before it in the order (logit desc, id asc); NaN logits come last.
-__global__ __launch_bounds__(256) void k_decode_topk(const double* __restrict__ part, const float* __restrict__ bias,
-                                                     int32_t* __restrict__ topk, float* __restrict__ gates, int N,
-                                                     int E, int K, int S) {
-  __shared__ double l[MOE_MAX_EXPERTS];
-  __shared__ double sel[MOE_MAX_TOPK];
-  const int n = blockIdx.x, e = threadIdx.x;
+// Scratch of token_topk.
+struct TopK {
+  double l[MOE_MAX_EXPERTS], sel[MOE_MAX_TOPK];
+};
+
+// Logit of expert e of token n from S partial sums.
+__device__ __forceinline__ double sum_parts(const double* __restrict__ part, int n, int e, int N, int E, int S) {
   double v = 0.0;
+  for (int s0 = 0; s0 < S; s0 += 16) {
+    double t[16];  // loads of one round trip
+#pragma unroll
+    for (int s = 0; s < 16; ++s) t[s] = s0 + s < S ? part[(int64_t(s0 + s) * N + n) * E + e] : 0.0;
+#pragma unroll
+    for (int s = 0; s < 16; ++s) v += t[s];
+  }
+  return v;
+}
+
+// Top-K and gates of one token by 256 threads, thread e < E with expert e's
+// logit v: its place is the number of experts before it in the order (logit
+// desc, id asc); NaN logits come last.  Writes ids and gates of the K places.
+__device__ __forceinline__ void token_topk(double v, const float* __restrict__ bias, int E, int K, TopK* s,
+                                           int32_t* ids, float* gates) {
+  const int e = threadIdx.x;
   if (e < E) {
-    for (int s = 0; s < S; ++s) v += part[(int64_t(s) * N + n) * E + e];
     if (bias != nullptr) v += double(bias[e]);
     if (v != v) v = -INFINITY;
-    l[e] = v;
+    s->l[e] = v;
   }
   __syncthreads();
   if (e < E) {
     int before = 0;
-    for (int i = 0; i < E; ++i) before += l[i] > v || (l[i] == v && i < e);
+#pragma unroll 8
+    for (int i = 0; i < E; ++i) before += s->l[i] > v || (s->l[i] == v && i < e);
     if (before < K) {
-      topk[n * K + before] = e;
-      sel[before] = v;
+      ids[before] = e;
+      s->sel[before] = v;
     }
   }
   __syncthreads();
   if (e < K) {
     float sum = 0.f, mine = 0.f;
     for (int k = 0; k < K; ++k) {
-      const float z = expf(float(sel[k] - sel[0]));
+      const float z = expf(float(s->sel[k] - s->sel[0]));
       sum += z;
       if (k == e) mine = z;
     }
-    gates[n * K + e] = mine / sum;
+    gates[e] = mine / sum;
+  }
+}
+
+__global__ __launch_bounds__(256) void k_decode_topk(const double* __restrict__ part, const float* __restrict__ bias,
+                                                     int32_t* __restrict__ topk, float* __restrict__ gates, int N,
+                                                     int E, int K, int S) {
+  __shared__ TopK s;
+  const int n = blockIdx.x;
+  const double v = int(threadIdx.x) < E ? sum_parts(part, n, threadIdx.x, N, E, S) : 0.0;
+  token_topk(v, bias, E, K, &s, topk + n * K, gates + n * K);
+}
+
+// Routing of one or two tokens by every workgroup of gate/up for itself.
+constexpr int kRouteTok = 2;
+template <typename T> struct Route {
+  const T *x, *w_r;
+  const double* part;  // null: the workgroup forms the logits as well
+  const float* bias;
+  int S;
+};
+struct Routed {
+  TopK top;
+  int32_t ids[kRouteTok * MOE_MAX_TOPK];
+  float gates[kRouteTok * MOE_MAX_TOPK];
+  double logits[kRouteTok][MOE_MAX_EXPERTS];
+};
+
+// red: 2 KiB per wave.
+template <typename T>
+__device__ __forceinline__ void route_here(const Route<T>& r, int N, int H, int E, int K, Routed* out, double* red) {
+  const int t = threadIdx.x, wave = t / kWave, c = lane_id() % 16;
+  if (r.part == nullptr) {
+    const T* px = r.x + int64_t(min(c, N - 1)) * H;
+    for (int e0 = 0; e0 < E; e0 += 16) {
+      f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 2
+      for (int h = wave * 32; h < H; h += kWaves * 32) logit_panel(px, r.w_r, h, E, min(e0 + c, E - 1), acc);
+      __syncthreads();
+      park_logits(acc, red + wave * 256);
+      __syncthreads();
+      if (t < 16 * N && e0 + t % 16 < E) {
+        double v = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) v += red[i * 256 + t];
+        out->logits[t / 16][e0 + t % 16] = v;
+      }
+    }
+    __syncthreads();
+  }
+  for (int n = 0; n < N; ++n) {
+    double v = 0.0;
+    if (t < E) v = r.part == nullptr ? out->logits[n][t] : sum_parts(r.part, n, t, N, E, r.S);
+    token_topk(v, r.bias, E, K, &out->top, out->ids + n * K, out->gates + n * K);
+    __syncthreads();
   }
 }
 
 // ------------------------------------------------------- rows of an expert
 
+// The chosen experts, ascending, and the slots' experts, in LDS.  Workgroups are
+// numbered over the chosen experts only: they go to the XCDs in turn by their
+// number, so numbers that had nothing to do would leave some XCDs with more
+// weights to read than others.
+struct Chosen {
+  int ids[kSlots];
+  int expert[MOE_MAX_EXPERTS];
+  int counts[2 * kSlots / kWave];
+};
+
+// Builds it; returns the number of chosen experts.  All threads call it.
+__device__ __forceinline__ int chosen_experts(const int32_t* __restrict__ topk, int NK, Chosen* c) {
+  static_assert(kNT == MOE_MAX_EXPERTS, "a thread per expert");
+  const int t = threadIdx.x;
+  c->expert[t] = 0;
+  __syncthreads();
+  for (int i = t; i < NK; i += kNT) {
+    const int e = topk[i];
+    c->ids[i] = e;
+    c->expert[e] = 1;
+  }
+  __syncthreads();
+  const bool mine = c->expert[t] != 0;
+  const uint64_t mask = __ballot(mine);
+  if (lane_id() == 0) c->counts[t / kWave] = __popcll(mask);
+  __syncthreads();
+  int active = 0, at = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w == t / kWave) at = active + __popcll(mask & ((uint64_t(1) << lane_id()) - 1));
+    active += c->counts[w];
+  }
+  if (mine) c->expert[at] = t;  // every thread has read its own flag
+  __syncthreads();
+  return active;
+}
+
 // Slots n*K + k of expert e in ascending order to rows[0, count); the count.
 // All threads of the workgroup call it.
-__device__ __forceinline__ int expert_slots(const int32_t* __restrict__ topk, int NK, int e, int* rows) {
-  __shared__ int wave_count[kWaves];
-  const int t = threadIdx.x, w = t / kWave;
-  const bool mine = t < NK && topk[t] == e;
-  const uint64_t mask = __ballot(mine);
-  if (lane_id() == 0) wave_count[w] = __popcll(mask);
-  __syncthreads();
-  int base = 0, count = 0;
+__device__ __forceinline__ int expert_slots(Chosen* c, int NK, int e, int* rows) {
+  constexpr int R = kSlots / kNT;
+  const int w = threadIdx.x / kWave;
+  bool mine[R];
+  uint64_t mask[R];
+  __syncthreads();  // rows and counts are free
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    if (i < w) base += wave_count[i];
-    count += wave_count[i];
+  for (int r = 0; r < R; ++r) {
+    const int t = r * kNT + threadIdx.x;
+    mine[r] = t < NK && c->ids[t] == e;
+    mask[r] = __ballot(mine[r]);
+    if (lane_id() == 0) c->counts[r * kWaves + w] = __popcll(mask[r]);
   }
-  // one token names an expert once, so count <= N <= kTok for any legal topk
-  const int at = base + __popcll(mask & ((uint64_t(1) << lane_id()) - 1));
-  if (mine && at < kTok) rows[at] = t;
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < R * kWaves; ++i) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i == r * kWaves + w && mine[r]) {
+        // one token names an expert once, so there are at most N <= kTok slots
+        const int at = count + __popcll(mask[r] & ((uint64_t(1) << lane_id()) - 1));
+        if (at < kTok) rows[at] = r * kNT + threadIdx.x;
+      }
+    count += c->counts[i];
+  }
   __syncthreads();
   return min(count, kTok);
 }
 
-// Unit u of the grid's expert axis: with at most E slots it is a slot, whose
-// expert is worked on by the first slot that names it, else expert u.  Builds
-// the expert's rows; returns their number, 0 when there is nothing to do.
-__device__ __forceinline__ int unit_rows(const int32_t* __restrict__ topk, int NK, int E, int u, int* e, int* rows) {
-  *e = NK <= E ? topk[u] : u;
-  const int M = expert_slots(topk, NK, *e, rows);
-  return NK <= E && rows[0] != u ? 0 : M;
+// The rows of unit u: the u-th chosen expert's slots; their number, 0 when there
+// is no such unit.
+__device__ __forceinline__ int unit_rows(const int32_t* __restrict__ topk, int NK, int u, Chosen* c, int* e,
+                                         int* rows) {
+  if (u >= chosen_experts(topk, NK, c)) return 0;
+  *e = c->expert[u];
+  return expert_slots(c, NK, *e, rows);
 }
 
 // --------------------------------------------------------------- the panels
 
-template <int BYTES> struct Raw;
-template <> struct Raw<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
-template <> struct Raw<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+// A wave's share of a panel: 32 rows x S segments of 16 lanes x 16 bytes, and
+// the row operand of 16 rows over the same 32 contraction indices.
+template <typename T, int S> struct Panel;
 
-// A wave's share of 32 rows x 16*CW columns of a weight matrix, and of the
-// same 32 columns of the row operand.  NA: row operands added up (bf16
-// activations are hi + lo).
-template <typename T, int CW, int NA> struct Panel;
-
-template <int CW, int NA> struct Panel<bf16_t, CW, NA> {
-  typedef typename Raw<CW * 2>::type raw_t;
-  typedef uint32_t words4 __attribute__((ext_vector_type(4)));
-  raw_t w[8];
-  // row operand of one tile of 16 rows: 8 consecutive bf16 of row lane%16
+template <int S> struct Panel<bf16_t, S> {
+  static constexpr int CW = 8;  // columns per lane and segment
+  words4_t w[S][8];
   struct A {
-    words4 a[NA];
-    __device__ __forceinline__ void load(const bf16_t* const* p, int64_t off) {
+    words4_t a;
+    __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const words4_t*>(p); }
+  };
+  // float32 values as the sum of two bf16 operands; stored, lo lies a plane behind hi
+  struct A2 {
+    words4_t hi, lo;
+    __device__ __forceinline__ void load(const bf16_t* p, int64_t plane) {
+      hi = *reinterpret_cast<const words4_t*>(p);
+      lo = *reinterpret_cast<const words4_t*>(p + plane);
+    }
+    __device__ __forceinline__ void store(bf16_t* p, int64_t plane) const {
+      *reinterpret_cast<words4_t*>(p) = hi;
+      *reinterpret_cast<words4_t*>(p + plane) = lo;
+    }
+    __device__ __forceinline__ void set(const float* v) {
 #pragma unroll
-      for (int i = 0; i < NA; ++i) a[i] = *reinterpret_cast<const words4*>(p[i] + off);
+      for (int j = 0; j < 4; ++j) {
+        hi[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        const float h0 = __uint_as_float(hi[j] << 16), h1 = __uint_as_float(hi[j] & 0xffff0000u);
+        // an infinite or NaN value is all in hi
+        lo[j] = pack_bf16x2(isfinite(h0) ? v[2 * j] - h0 : 0.f, isfinite(h1) ? v[2 * j + 1] - h1 : 0.f);
+      }
     }
   };
   __device__ __forceinline__ void load(const bf16_t* p, int64_t ld) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const raw_t*>(p + j * ld));
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        w[s][j] = __builtin_nontemporal_load(reinterpret_cast<const words4_t*>(p + j * ld + s * 16 * CW));
   }
-  template <int MT>
-  __device__ __forceinline__ void multiply(const A (&a)[MT], f32x4_t (&acc)[MT][CW]) const {
+  __device__ __forceinline__ bf16x8_t column(int s, int i) const {
+    words4_t b;
 #pragma unroll
-    for (int i = 0; i < CW; ++i) {
-      words4 b;
+    for (int d = 0; d < 4; ++d)
+      b[d] = __builtin_amdgcn_perm(w[s][2 * d + 1][i / 2], w[s][2 * d][i / 2], i % 2 ? 0x07060302u : 0x05040100u);
+    return __builtin_bit_cast(bf16x8_t, b);
+  }
+  static __device__ __forceinline__ void fma(words4_t a, bf16x8_t b, f32x4_t& acc) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), b, acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void fma(const A& a, bf16x8_t b, f32x4_t& acc) { fma(a.a, b, acc); }
+  static __device__ __forceinline__ void fma(const A2& a, bf16x8_t b, f32x4_t& acc) {
+    fma(a.lo, b, acc);
+    fma(a.hi, b, acc);
+  }
+  template <int MT, typename Op>
+  __device__ __forceinline__ void multiply(const Op (&a)[MT], f32x4_t (&acc)[MT][S][CW]) const {
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
-        b[d] = __builtin_amdgcn_perm(w[2 * d + 1][i / 2], w[2 * d][i / 2], i % 2 ? 0x07060302u : 0x05040100u);
-      const bf16x8_t bv = __builtin_bit_cast(bf16x8_t, b);
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < CW; ++i) {
+        const bf16x8_t b = column(s, i);
 #pragma unroll
-        for (int q = 0; q < NA; ++q)
-          acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[m].a[q]), bv, acc[m][i],
-                                                              0, 0, 0);
-    }
+        for (int m = 0; m < MT; ++m) fma(a[m], b, acc[m][s][i]);
+      }
   }
 };
 
-template <int CW> struct Panel<float, CW, 1> {
-  typedef float raw_t __attribute__((ext_vector_type(CW)));
-  raw_t w[8];
+template <int S> struct Panel<float, S> {
+  static constexpr int CW = 4;
+  f32x4_t w[S][8];
   struct A {
     float a[8];
-    __device__ __forceinline__ void load(const float* const* p, int64_t off) {
-      Vec16<float>::load(p[0] + off, a);
-      Vec16<float>::load(p[0] + off + 4, a + 4);
+    __device__ __forceinline__ void load(const float* p) {
+      Vec16<float>::load(p, a);
+      Vec16<float>::load(p + 4, a + 4);
+    }
+    __device__ __forceinline__ void load(const float* p, int64_t) { load(p); }
+    __device__ __forceinline__ void store(float* p, int64_t) const {
+      Vec16<float>::store(p, a);
+      Vec16<float>::store(p + 4, a + 4);
+    }
+    __device__ __forceinline__ void set(const float* v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = v[j];
     }
   };
+  typedef A A2;
   __device__ __forceinline__ void load(const float* p, int64_t ld) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __builtin_nontemporal_load(reinterpret_cast<const raw_t*>(p + j * ld));
-  }
-  template <int MT>
-  __device__ __forceinline__ void multiply(const A (&a)[MT], f32x4_t (&acc)[MT][CW]) const {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
-      for (int i = 0; i < CW; ++i)
+      for (int s = 0; s < S; ++s)
+        w[s][j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p + j * ld + s * 16 * CW));
+  }
+  template <int MT>
+  __device__ __forceinline__ void multiply(const A (&a)[MT], f32x4_t (&acc)[MT][S][CW]) const {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m].a[j], w[j][i], acc[m][i], 0, 0, 0);
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            acc[m][s][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m].a[j], w[s][j][i], acc[m][s][i], 0, 0, 0);
   }
 };
 
-// acc[m] += rows of tile m (pa[m], NA pointers at this lane's row and first
-// column) . W over the panels first, first + stride, ... below `panels`.
-// wp: this lane's first element of panel 0.  The next panel's loads are issued
-// before this one's products.
-template <typename T, int CW, int NA, int MT>
-__device__ __forceinline__ void stream(const T* wp, int64_t ld, const T* const (&pa)[MT][NA], int first, int stride,
-                                       int panels, f32x4_t (&acc)[MT][CW]) {
-  typedef Panel<T, CW, NA> P;
-  P p[2];
-  typename P::A a[2][MT];
-  auto fetch = [&](P& q, typename P::A (&b)[MT], int i) {
-    q.load(wp + int64_t(i) * 32 * ld, ld);
+// Columns of one workgroup: two segments.
+template <typename T>
+constexpr int kCols = 2 * 16 * Panel<T, 1>::CW;
+
+template <int MT, int S, int CW>
+__device__ __forceinline__ void clear(f32x4_t (&acc)[MT][S][CW]) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) b[m].load(pa[m], int64_t(i) * 32);
-  };
-  if (first >= panels) return;
-  fetch(p[0], a[0], first);
-  int i = first;
-  while (true) {
-    const int i1 = i + stride, i2 = i + 2 * stride;
-    if (i1 < panels) fetch(p[1], a[1], i1);
-    p[0].template multiply<MT>(a[0], acc);
-    if (i1 >= panels) break;
-    if (i2 < panels) fetch(p[0], a[0], i2);
-    p[1].template multiply<MT>(a[1], acc);
-    if (i2 >= panels) break;
-    i = i2;
-  }
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < CW; ++i) acc[m][s][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 }
 
-// Writes a wave's 16 x 16*CW sums to red [16][16*CW] (the matrix instruction
-// leaves row 4*(lane/16) + r, operand column lane%16 in element r).
+// A wave's 16 x 16*CW sums to mine [16][16*CW]: the matrix instruction leaves
+// row 4g + r, operand column c in element r.
 template <int CW>
-__device__ __forceinline__ void park(const f32x4_t (&acc)[CW], float* red) {
+__device__ __forceinline__ void park(const f32x4_t (&acc)[CW], float* mine) {
   const int g = lane_id() / 16, c = lane_id() % 16;
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int i = 0; i < CW; ++i) red[(4 * g + r) * 16 * CW + c * CW + i] = acc[i][r];
+    for (int i = 0; i < CW; i += 4)
+      *reinterpret_cast<f32x4_t*>(mine + (4 * g + r) * 16 * CW + c * CW + i) =
+          f32x4_t{acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]};
+}
+
+// The waves' sums of each 16 x 16*CW piece added in wave order; out(m, s, row,
+// first of 4 columns, their sums) for all of it, by all threads.  red: 16 * 16
+// * CW floats per wave.
+template <int MT, int S, int CW, typename F>
+__device__ __forceinline__ void join_waves(const f32x4_t (&acc)[MT][S][CW], float* red, F out) {
+  constexpr int W = 16 * CW, PIECE = 16 * W;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      __syncthreads();
+      park(acc[m][s], red + threadIdx.x / kWave * PIECE);
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < PIECE / 4 / kNT; ++t) {
+        const int i = 4 * (t * kNT + threadIdx.x);
+        f32x4_t v = *reinterpret_cast<const f32x4_t*>(red + i);
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(red + w * PIECE + i);
+        out(m, s, i / W, i % W, v);
+      }
+    }
 }
 
 // ------------------------------------------------------------ gate and up
 
-template <typename T> struct ActStore;
-template <> struct ActStore<bf16_t> {
-  static constexpr int n = 2;  // hi and lo
-  static __device__ __forceinline__ void put(bf16_t* act, int64_t plane, int64_t at, float v) {
-    const bf16_t hi = f32_to_bf16(v);
-    const float rest = v - bf16_to_f32(hi);
-    act[at] = hi;
-    act[plane + at] = isfinite(rest) ? f32_to_bf16(rest) : bf16_t(0);  // infinite or NaN activations: hi says it all
+// gate * silu(G) * U of 8 consecutive columns from the parts' sums: part p's G
+// at gu + 2*p*stride, its U behind at + stride.  load() before the panel's
+// weights are asked for, so that finish() runs while they are on their way.
+struct Act {
+  float gs[8], us[8];
+  __device__ __forceinline__ void load(const float* __restrict__ gu, int64_t stride, int parts) {
+    Vec16<float>::load(gu, gs);
+    Vec16<float>::load(gu + 4, gs + 4);
+    Vec16<float>::load(gu + stride, us);
+    Vec16<float>::load(gu + stride + 4, us + 4);
+    for (int p = 1; p < parts; ++p) {
+      gu += 2 * stride;
+      float t[16];
+      Vec16<float>::load(gu, t);
+      Vec16<float>::load(gu + 4, t + 4);
+      Vec16<float>::load(gu + stride, t + 8);
+      Vec16<float>::load(gu + stride + 4, t + 12);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        gs[j] += t[j];
+        us[j] += t[j + 8];
+      }
+    }
+  }
+  // four consecutive ones from sums at hand
+  __device__ __forceinline__ void take(int j, f32x4_t g, f32x4_t u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      gs[j + i] = g[i];
+      us[j + i] = u[i];
+    }
+  }
+  __device__ __forceinline__ void finish(float gate, float* v) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = gate * (gs[j] / (1.0f + expf(-gs[j])) * us[j]);
   }
 };
-template <> struct ActStore<float> {
-  static constexpr int n = 1;
-  static __device__ __forceinline__ void put(float* act, int64_t, int64_t at, float v) { act[at] = v; }
-};
 
-// Rows rows[0, M) (token = row / div) of one expert: silu(x.wg) * (x.wu) for
-// the 16*CW columns from col0, to act[row][ld].  Waves 2s and 2s+1 take every
-// fourth panel from s of W_gate and W_up.
-template <typename T, int CW, int MT>
-__device__ __forceinline__ void gate_up_rows(const T* __restrict__ x, const T* wg, const T* wu, int H, int64_t ld,
-                                             int64_t col0, const int* rows, int M, int div, T* act, int64_t plane,
-                                             float* red) {
-  const int wave = threadIdx.x / kWave, g = lane_id() / 16, c = lane_id() % 16;
-  f32x4_t acc[MT][CW];
+
+// As join_waves for waves that hold G (even) and U (odd): out(m, s, row, first
+// of 8 columns, their G and U).
+template <int MT, int S, int CW, typename F>
+__device__ __forceinline__ void join_pairs(const f32x4_t (&acc)[MT][S][CW], float* red, F out) {
+  constexpr int W = 16 * CW, PIECE = 16 * W;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < CW; ++i) acc[m][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const T* pa[MT][1];
+    for (int s = 0; s < S; ++s) {
+      __syncthreads();
+      park(acc[m][s], red + threadIdx.x / kWave * PIECE);
+      __syncthreads();
+      const int i = 8 * threadIdx.x;
+      if (i < PIECE) {
+        Act a;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          f32x4_t v[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            v[k] = *reinterpret_cast<const f32x4_t*>(red + k * PIECE + i + j);
+#pragma unroll
+            for (int w = k + 2; w < kWaves; w += 2) v[k] += *reinterpret_cast<const f32x4_t*>(red + w * PIECE + i + j);
+          }
+          a.take(j, v[0], v[1]);
+        }
+        out(m, s, i / W, i % W, a);
+      }
+    }
+}
+
+// Where the sums of gate and up go.
+template <typename T, bool JOINT> struct GuOut;
+// One matrix: its sums, [row][ld].
+template <typename T> struct GuOut<T, false> {
+  float* sums;
+};
+// Both: the activations, as the down kernels load them ([ld/32][R][32], planes);
+// gates null: 1.
+template <typename T> struct GuOut<T, true> {
+  T* act;
+  const float* gates;
+  int R;
+};
+
+// The token rows: element (row, k) at p[row * row_step + k / 32 * panel_step + k % 32].
+template <typename T> struct XRows {
+  const T* p;
+  int row_step, panel_step;
+};
+
+// x times W for up to 16*MT rows (row r: token rows[r] /
+// div) and S segments from col0, over panels first, first + step, ....  JOINT:
+// even waves have W_gate, odd ones W_up.
+template <typename T, int S, int MT, bool JOINT>
+__device__ __forceinline__ void gate_up_rows(const XRows<T>& x, const T* w, int H, int64_t ld,
+                                             int64_t col0, const int* rows, int M, int div, int first, int step,
+                                             const GuOut<T, JOINT>& out, float* red) {
+  typedef Panel<T, S> P;
+  const int g = lane_id() / 16, c = lane_id() % 16;
+  f32x4_t acc[MT][S][P::CW];
+  clear(acc);
+  const T* px[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int r = 16 * m + c;
-    pa[m][0] = x + int64_t(rows[r < M ? r : 0] / div) * H + 8 * g;
+    px[m] = x.p + int64_t(rows[r < M ? r : 0] / div) * x.row_step + 8 * g;
   }
-  stream<T, CW, 1, MT>((wave & 1 ? wu : wg) + 8 * g * ld + col0 + CW * c, ld, pa, wave / 2, kWaves / 2, H / 32, acc);
-  constexpr int TILE = 16 * 16 * CW;
+  const T* pw = w + 8 * g * ld + col0 + P::CW * c;
+  for (int i = first; i < H / 32; i += step) {
+    P p;
+    typename P::A a[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    __syncthreads();
-    park<CW>(acc[m], red + wave * TILE);
-    __syncthreads();
-    for (int i = threadIdx.x; i < TILE; i += kNT) {
-      const int r = 16 * m + i / (16 * CW);
-      if (r >= M) break;
-      float gv = 0.f, uv = 0.f;
-#pragma unroll
-      for (int s = 0; s < kWaves / 2; ++s) {
-        gv += red[2 * s * TILE + i];
-        uv += red[(2 * s + 1) * TILE + i];
+    for (int m = 0; m < MT; ++m) a[m].load(px[m] + int64_t(i) * x.panel_step);
+    p.load(pw + int64_t(i) * 32 * ld, ld);
+    p.template multiply<MT>(a, acc);
+  }
+  if constexpr (JOINT) {
+    join_pairs(acc, red, [&](int m, int s, int row, int col, const Act& act) {
+      const int r = 16 * m + row;
+      if (r < M) {
+        float v[8];
+        act.finish(out.gates != nullptr ? out.gates[rows[r]] : 1.f, v);
+        typename P::A2 o;
+        o.set(v);
+        const int64_t at = col0 + s * 16 * P::CW + col;
+        o.store(out.act + (at / 32 * out.R + rows[r]) * 32 + at % 32, ld * out.R);
       }
-      ActStore<T>::put(act, plane, rows[r] * ld + col0 + i % (16 * CW), gv / (1.0f + expf(-gv)) * uv);
+    });
+  } else {
+    join_waves(acc, red, [&](int m, int s, int row, int col, f32x4_t v) {
+      const int r = 16 * m + row;
+      if (r < M) *reinterpret_cast<f32x4_t*>(out.sums + rows[r] * ld + col0 + s * 16 * P::CW + col) = v;
+    });
+  }
+}
+
+// All M rows of one expert and the workgroup's columns.
+template <typename T, int MTMAX, bool JOINT>
+__device__ __forceinline__ void gate_up(const XRows<T>& x, const T* w, int H, int64_t ld, int64_t col0,
+                                        const int* rows, int M, int div, int first, int step,
+                                        const GuOut<T, JOINT>& out, float* red) {
+  constexpr int HALF = kCols<T> / 2;
+  if (col0 + kCols<T> <= ld && M <= 32) {
+    if (M <= 16 || MTMAX == 1)
+      gate_up_rows<T, 2, 1, JOINT>(x, w, H, ld, col0, rows, M, div, first, step, out, red);
+    else
+      gate_up_rows<T, 2, (MTMAX > 1 ? 2 : 1), JOINT>(x, w, H, ld, col0, rows, M, div, first, step, out, red);
+  } else {
+    // a last single segment, or more rows than two segments' sums leave registers for
+    for (int64_t col = col0; col < col0 + kCols<T> && col < ld; col += HALF) {
+      if (M <= 16 || MTMAX == 1)
+        gate_up_rows<T, 1, 1, JOINT>(x, w, H, ld, col, rows, M, div, first, step, out, red);
+      else
+        gate_up_rows<T, 1, MTMAX, JOINT>(x, w, H, ld, col, rows, M, div, first, step, out, red);
     }
   }
 }
 
-template <typename T, int CW, int MT>
-__global__ __launch_bounds__(kNT) void k_decode_gate_up(const T* __restrict__ x, const T* __restrict__ wg,
-                                                        const T* __restrict__ wu, const T* __restrict__ swg,
-                                                        const T* __restrict__ swu, const int32_t* __restrict__ topk,
-                                                        T* __restrict__ act, T* __restrict__ sact, int N, int H,
-                                                        int F, int Fs, int E, int K, int units) {
+// What the experts' kernels share.
+struct Shape {
+  int N, H, F, Fs, E, K;
+  int units;     // experts that can be chosen at most
+  int gu_parts;  // workgroups that share the contraction over H
+  int dn_parts;  // ... over F (N > 16), or over all experts' F (N <= 16)
+  int sdn_parts;  // ... over Fs (N > 16)
+};
+
+// G and U sums, a workgroup having one matrix's columns and part of its
+// contraction: gu [part][2][slot][F], sgu [part][2][token][Fs].  ROUTE: the
+// workgroup finds topk and gates itself, the first one writes them.  The first
+// workgroup clears the n_arrived counters of k_decode_down_all.
+template <typename T, int MTMAX, bool ROUTE>
+__global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* __restrict__ wg,
+                                                           const T* __restrict__ wu, const T* __restrict__ swg,
+                                                           const T* __restrict__ swu, int32_t* __restrict__ topk_out,
+                                                           float* __restrict__ gates, Route<T> route,
+                                                           int32_t* __restrict__ arrived, int n_arrived,
+                                                           float* __restrict__ gu, float* __restrict__ sgu, Shape q) {
+  __shared__ Chosen chosen;
   __shared__ int rows[kTok];
-  __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * 16 * CW];
-  const int chunks = F / (16 * CW);
-  const int b = blockIdx.x;
-  int M, div;
-  const T *mg, *mu;
-  T* out;
-  int64_t ld, col0, plane;
-  if (b < units * chunks) {
-    int e;
-    M = unit_rows(topk, N * K, E, b / chunks, &e, rows);
-    div = K;
-    ld = F;
-    col0 = int64_t(b % chunks) * 16 * CW;
-    mg = wg + int64_t(e) * H * F;
-    mu = wu + int64_t(e) * H * F;
-    out = act;
-    plane = int64_t(N) * K * F;
+  __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
+  const int32_t* topk = topk_out;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
+  if constexpr (ROUTE) {
+    __shared__ Routed routed;
+    route_here(route, q.N, q.H, q.E, q.K, &routed, reinterpret_cast<double*>(red));
+    topk = routed.ids;
+    if (blockIdx.x == 0 && int(threadIdx.x) < q.N * q.K) {
+      topk_out[threadIdx.x] = routed.ids[threadIdx.x];
+      gates[threadIdx.x] = routed.gates[threadIdx.x];
+    }
+  }
+  const int wave = threadIdx.x / kWave;
+  const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
+  const int schunks = (q.Fs + kCols<T> - 1) / kCols<T>, shared = 2 * q.gu_parts * schunks;
+  int b = int(blockIdx.x) - shared;
+  if (b >= 0) {
+    const int chunk = b % chunks;
+    b /= chunks;
+    const int mat = b % 2, part = b / 2 % q.gu_parts;
+    int e = 0;
+    const int M = unit_rows(topk, q.N * q.K, b / 2 / q.gu_parts, &chosen, &e, rows);
+    if (M == 0) return;
+    gate_up<T, MTMAX, false>(x, (mat ? wu : wg) + int64_t(e) * q.H * q.F, q.H, q.F, int64_t(chunk) * kCols<T>,
+                             rows, M, q.K, part * kWaves + wave, q.gu_parts * kWaves,
+                             GuOut<T, false>{gu + int64_t(part * 2 + mat) * q.N * q.K * q.F}, red);
   } else {
+    b += shared;
+    const int chunk = b % schunks;
+    b /= schunks;
+    const int mat = b % 2, part = b / 2;
     if (threadIdx.x < kTok) rows[threadIdx.x] = threadIdx.x;
     __syncthreads();
-    M = N;
-    div = 1;
-    ld = Fs;
-    col0 = int64_t(b - units * chunks) * 16 * CW;
-    mg = swg;
-    mu = swu;
-    out = sact;
-    plane = int64_t(N) * Fs;
+    gate_up<T, MTMAX, false>(x, mat ? swu : swg, q.H, q.Fs, int64_t(chunk) * kCols<T>, rows, q.N, 1,
+                             part * kWaves + wave, q.gu_parts * kWaves,
+                             GuOut<T, false>{sgu + int64_t(part * 2 + mat) * q.N * q.Fs}, red);
   }
-  for (int m0 = 0; m0 < M; m0 += 16 * MT)
-    gate_up_rows<T, CW, MT>(x, mg, mu, H, ld, col0, rows + m0, min(M - m0, 16 * MT), div, out, plane, red);
+}
+
+// Activations, a workgroup having the same columns of both matrices (two waves
+// each) and the whole contraction.
+template <typename T, int MTMAX>
+__global__ __launch_bounds__(kNT, 2) void k_decode_gate_up_act(XRows<T> x, const T* __restrict__ wg,
+                                                               const T* __restrict__ wu, const T* __restrict__ swg,
+                                                               const T* __restrict__ swu,
+                                                               const int32_t* __restrict__ topk,
+                                                               const float* __restrict__ gates,
+                                                               int32_t* __restrict__ arrived, int n_arrived,
+                                                               T* __restrict__ act, T* __restrict__ sact, Shape q) {
+  __shared__ Chosen chosen;
+  __shared__ int rows[kTok];
+  __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
+  const int wave = threadIdx.x / kWave;
+  const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
+  const int shared = (q.Fs + kCols<T> - 1) / kCols<T>;
+  int b = int(blockIdx.x) - shared;
+  if (b >= 0) {
+    int e = 0;
+    const int M = unit_rows(topk, q.N * q.K, b / chunks, &chosen, &e, rows);
+    if (M == 0) return;
+    gate_up<T, MTMAX, true>(x, (wave % 2 ? wu : wg) + int64_t(e) * q.H * q.F, q.H, q.F,
+                            int64_t(b % chunks) * kCols<T>, rows, M, q.K, wave / 2, kWaves / 2,
+                            GuOut<T, true>{act, gates, q.N * q.K}, red);
+  } else {
+    b += shared;
+    if (threadIdx.x < kTok) rows[threadIdx.x] = threadIdx.x;
+    __syncthreads();
+    gate_up<T, MTMAX, true>(x, wave % 2 ? swu : swg, q.H, q.Fs, int64_t(b) * kCols<T>, rows, q.N, 1, wave / 2,
+                            kWaves / 2, GuOut<T, true>{sact, nullptr, q.N}, red);
+  }
 }
 
 // ------------------------------------------------------------------- down
 
-// Rows of one expert: act.wd over this split's panels, for the 16*CW columns
-// from col0, to ysp[row][H].
-template <typename T, int CW, int MT>
-__device__ __forceinline__ void down_rows(const T* act, int64_t plane, const T* wd, int F, int64_t H, int64_t col0,
-                                          const int* rows, int M, int split, int splits, float* ysp, float* red) {
-  constexpr int NA = ActStore<T>::n;
-  const int wave = threadIdx.x / kWave, g = lane_id() / 16, c = lane_id() % 16;
-  f32x4_t acc[MT][CW];
+// The activations of all slots, then of the shared expert's tokens, in the form
+// that the down kernels load: act [F/32][slot][32] and sact [Fs/32][token][32],
+// planes of hi and lo for bf16.  A thread has 8 columns.
+template <typename T>
+__global__ __launch_bounds__(256) void k_decode_act(const float* __restrict__ gu, const float* __restrict__ sgu,
+                                                    const float* __restrict__ gates, T* __restrict__ act,
+                                                    T* __restrict__ sact, Shape q) {
+  const int64_t NK = int64_t(q.N) * q.K, routed = NK * (q.F / 8), all = routed + int64_t(q.N) * (q.Fs / 8);
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const bool sh = i >= routed;
+    const int64_t at = (sh ? i - routed : i) * 8, R = sh ? q.N : NK, F = sh ? q.Fs : q.F;
+    const int64_t panel = at / (32 * R);
+    const int row = int(at % (32 * R)) / 32;
+    Act a;
+    float v[8];
+    a.load((sh ? sgu : gu) + row * F + panel * 32 + at % 32, R * F, q.gu_parts);
+    a.finish(sh ? 1.f : gates[row], v);
+    typename Panel<T, 1>::A2 o;
+    o.set(v);
+    o.store((sh ? sact : act) + at, R * F);
+  }
+}
+
+// One expert's rows (slots rows[0, M)) times its W_down, panels first, first +
+// step, ...: sums to out[rows[r]][H].
+template <typename T, int S, int MT>
+__device__ __forceinline__ void down_rows(const T* __restrict__ act, int64_t plane, const T* wd, int F, int64_t H,
+                                          int64_t col0, const int* rows, int M, int first, int step, float* out,
+                                          float* red) {
+  typedef Panel<T, S> P;
+  const int g = lane_id() / 16, c = lane_id() % 16;
+  f32x4_t acc[MT][S][P::CW];
+  clear(acc);
+  const T* pa[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m) pa[m] = act + rows[16 * m + c < M ? 16 * m + c : 0] * 32 + 8 * g;
+  const T* pw = wd + 8 * g * H + col0 + P::CW * c;
+  for (int i = first; i < F / 32; i += step) {
+    P p;
+    typename P::A2 a[MT];
 #pragma unroll
-    for (int i = 0; i < CW; ++i) acc[m][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const T* pa[MT][NA];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int q = 0; q < NA; ++q) {
-      const int r = 16 * m + c;
-      pa[m][q] = act + q * plane + int64_t(rows[r < M ? r : 0]) * F + 8 * g;
-    }
-  stream<T, CW, NA, MT>(wd + 8 * g * H + col0 + CW * c, H, pa, split * kWaves + wave, splits * kWaves, F / 32, acc);
-  constexpr int TILE = 16 * 16 * CW;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    __syncthreads();
-    park<CW>(acc[m], red + wave * TILE);
-    __syncthreads();
-    for (int i = threadIdx.x; i < TILE; i += kNT) {
-      const int r = 16 * m + i / (16 * CW);
-      if (r >= M) break;
-      float v = 0.f;
-#pragma unroll
-      for (int s = 0; s < kWaves; ++s) v += red[s * TILE + i];
-      ysp[rows[r] * H + col0 + i % (16 * CW)] = v;
+    for (int m = 0; m < MT; ++m) a[m].load(pa[m] + int64_t(i) * 32 * (plane / F), plane);
+    p.load(pw + int64_t(i) * 32 * H, H);
+    p.template multiply<MT>(a, acc);
+  }
+  join_waves(acc, red, [&](int m, int s, int row, int col, f32x4_t v) {
+    const int r = 16 * m + row;
+    if (r < M) *reinterpret_cast<f32x4_t*>(out + rows[r] * H + col0 + s * 16 * P::CW + col) = v;
+  });
+}
+
+template <typename T, int MTMAX>
+__device__ __forceinline__ void down(const T* __restrict__ act, int64_t plane, const T* wd, int F, int64_t H,
+                                     int64_t col0, const int* rows, int M, int first, int step, float* out,
+                                     float* red) {
+  constexpr int HALF = kCols<T> / 2;
+  if (col0 + kCols<T> <= H && M <= 32) {
+    if (M <= 16)
+      down_rows<T, 2, 1>(act, plane, wd, F, H, col0, rows, M, first, step, out, red);
+    else
+      down_rows<T, 2, 2>(act, plane, wd, F, H, col0, rows, M, first, step, out, red);
+  } else {
+    for (int64_t col = col0; col < col0 + kCols<T> && col < H; col += HALF) {
+      if (M <= 16)
+        down_rows<T, 1, 1>(act, plane, wd, F, H, col, rows, M, first, step, out, red);
+      else
+        down_rows<T, 1, MTMAX>(act, plane, wd, F, H, col, rows, M, first, step, out, red);
     }
   }
 }
 
-template <typename T, int CW, int MT>
-__global__ __launch_bounds__(kNT) void k_decode_down(const T* __restrict__ act, const T* __restrict__ sact,
-                                                     const T* __restrict__ wd, const T* __restrict__ swd,
-                                                     const int32_t* __restrict__ topk, float* __restrict__ ysp,
-                                                     float* __restrict__ sysp, int N, int H, int F, int Fs, int E,
-                                                     int K, int units, int splits, int ssplits) {
+// More than 16 tokens: a workgroup has one expert's columns and part of its
+// contraction; ysp [part][slot][H], then sysp [part][token][H].
+template <typename T, int MTMAX>
+__global__ __launch_bounds__(kNT, 2) void k_decode_down(const T* __restrict__ act, const T* __restrict__ sact,
+                                                        const T* __restrict__ wd, const T* __restrict__ swd,
+                                                        const int32_t* __restrict__ topk, float* __restrict__ ysp,
+                                                        float* __restrict__ sysp, Shape q) {
+  __shared__ Chosen chosen;
   __shared__ int rows[kTok];
-  __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * 16 * CW];
-  const int chunks = H / (16 * CW);
+  __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
+  const int wave = threadIdx.x / kWave;
+  const int chunks = (q.H + kCols<T> - 1) / kCols<T>;
   int b = blockIdx.x;
-  const int64_t col0 = int64_t(b % chunks) * 16 * CW;
+  const int64_t col0 = int64_t(b % chunks) * kCols<T>;
   b /= chunks;
-  if (b < units * splits) {
-    int e;
-    const int M = unit_rows(topk, N * K, E, b / splits, &e, rows);
-    const int sp = b % splits;
-    for (int m0 = 0; m0 < M; m0 += 16 * MT)
-      down_rows<T, CW, MT>(act, int64_t(N) * K * F, wd + int64_t(e) * F * H, F, H, col0, rows + m0,
-                           min(M - m0, 16 * MT), sp, splits, ysp + int64_t(sp) * N * K * H, red);
+  b -= q.sdn_parts;
+  if (b >= 0) {
+    const int part = b % q.dn_parts, u = b / q.dn_parts, first = part * kWaves + wave, step = q.dn_parts * kWaves;
+    int e = 0;
+    const int M = unit_rows(topk, q.N * q.K, u, &chosen, &e, rows);
+    if (M == 0) return;
+    down<T, MTMAX>(act, int64_t(q.N) * q.K * q.F, wd + int64_t(e) * q.F * q.H, q.F, q.H, col0, rows, M, first, step,
+                   ysp + int64_t(part) * q.N * q.K * q.H, red);
   } else {
+    const int part = b + q.sdn_parts, first = part * kWaves + wave, step = q.sdn_parts * kWaves;
     if (threadIdx.x < kTok) rows[threadIdx.x] = threadIdx.x;
     __syncthreads();
-    const int sp = b - units * splits;
-    for (int m0 = 0; m0 < N; m0 += 16 * MT)
-      down_rows<T, CW, MT>(sact, int64_t(N) * Fs, swd, Fs, H, col0, rows + m0, min(N - m0, 16 * MT), sp, ssplits,
-                           sysp + int64_t(sp) * N * H, red);
+    down<T, MTMAX>(sact, int64_t(q.N) * q.Fs, swd, q.Fs, q.H, col0, rows, q.N, first, step,
+                   sysp + int64_t(part) * q.N * q.H, red);
   }
 }
 
-// y[n] = sum_k gates[n,k] * (sum over the splits) (+ the shared expert's sum),
-// k and splits ascending, float32, one rounding.
+// Where k_decode_down_all finds the activations: FUSED, in the sums of gate and
+// up (formed here, once per workgroup that needs them: for few tokens cheaper
+// than a launch), else as k_decode_act left them.
+template <typename T, bool FUSED> struct Rows;
+template <typename T> struct Rows<T, true> {
+  const float *gu, *sgu;
+};
+template <typename T> struct Rows<T, false> {
+  const T *act, *sact;
+};
+
+// At most 16 tokens: the row operand's rows are the tokens themselves, zero
+// where a token did not choose the panel's expert, so that the sum over the
+// experts is part of the contraction.  All panels of the chosen experts (and of
+// the shared one) are dealt evenly to the waves of dn_parts workgroups; yp
+// [part][token][H].  With `arrived` (one counter per column strip, zero) the
+// strip's last workgroup adds the parts up and writes y, else k_decode_combine
+// does.
+template <typename T, int S, bool FUSED>
+__device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __restrict__ wd,
+                                         const T* __restrict__ swd, const Shape& q, int64_t col0, const int* expert,
+                                         const int16_t (*slot)[16], const float* gate, int active, int part,
+                                         float* yp, float* red) {
+  typedef Panel<T, S> P;
+  const int wave = threadIdx.x / kWave, g = lane_id() / 16, c = lane_id() % 16;
+  const int64_t H = q.H, plane = int64_t(q.N) * q.K * q.F, splane = int64_t(q.N) * q.Fs;
+  f32x4_t acc[1][S][P::CW];
+  clear(acc);
+  const int per = q.F / 32, routed = active * per, all = routed + q.Fs / 32;
+  const int64_t lane0 = 8 * g * H + col0 + P::CW * c;
+  for (int i = part * kWaves + wave; i < all; i += q.dn_parts * kWaves) {
+    const bool sh = i >= routed;
+    const int u = sh ? 0 : i / per, f = (sh ? i - routed : i % per) * 32;
+    const int row = sh ? (c < q.N ? c : -1) : slot[u][c];  // -1: no such row
+    const int64_t at = FUSED ? int64_t(row < 0 ? 0 : row) * (sh ? q.Fs : q.F) + f + 8 * g
+                             : int64_t(f) * (sh ? q.N : q.N * q.K) + (row < 0 ? 0 : row) * 32 + 8 * g;
+    P p;
+    typename P::A2 a[1];
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    a[0].set(v);
+    const T* pw = (sh ? swd + int64_t(f) * H : wd + (int64_t(expert[u]) * q.F + f) * H) + lane0;
+    if constexpr (FUSED) {
+      Act act;
+      if (row >= 0) act.load((sh ? in.sgu : in.gu) + at, sh ? splane : plane, q.gu_parts);
+      p.load(pw, H);
+      if (row >= 0) {
+        act.finish(sh ? 1.f : gate[row], v);
+        a[0].set(v);
+      }
+    } else {
+      if (row >= 0) a[0].load((sh ? in.sact : in.act) + at, sh ? splane : plane);
+      p.load(pw, H);
+    }
+    p.template multiply<1>(a, acc);
+  }
+  join_waves(acc, red, [&](int, int s, int row, int col, f32x4_t v) {
+    if (row < q.N)
+      *reinterpret_cast<f32x4_t*>(yp + (int64_t(part) * q.N + row) * H + col0 + s * 16 * P::CW + col) = v;
+  });
+}
+
+template <typename T, bool FUSED>
+__global__ __launch_bounds__(kNT, 2) void k_decode_down_all(Rows<T, FUSED> in, const T* __restrict__ wd,
+                                                            const T* __restrict__ swd,
+                                                            const int32_t* __restrict__ topk,
+                                                            const float* __restrict__ gates, float* __restrict__ yp,
+                                                            int32_t* __restrict__ arrived, T* __restrict__ y,
+                                                            Shape q) {
+  constexpr int SL = 16 * MOE_MAX_TOPK;
+  __shared__ int expert[SL];
+  __shared__ int16_t slot[SL][16];
+  __shared__ float gate[SL];
+  __shared__ int ids[SL], unit[SL], counts[kWaves];
+  __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
+  const int NK = q.N * q.K, t = threadIdx.x;
+  static_assert(SL <= kNT, "a thread per slot");
+  if (t < NK) {
+    ids[t] = topk[t];
+    gate[t] = gates[t];
+  }
+  for (int i = t; i < SL * 16; i += kNT) slot[i / 16][i % 16] = -1;
+  __syncthreads();
+  // a slot's unit: how many experts' first slots come before its expert's first slot
+  int first = t;
+  if (t < NK)
+    for (first = 0; ids[first] != ids[t]; ++first) {}
+  const bool head = t < NK && first == t;
+  const uint64_t heads = __ballot(head);
+  if (lane_id() == 0) counts[t / kWave] = __popcll(heads);
+  __syncthreads();
+  int active = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w == t / kWave && head) unit[t] = active + __popcll(heads & ((uint64_t(1) << lane_id()) - 1));
+    active += counts[w];
+  }
+  __syncthreads();
+  if (t < NK) {
+    expert[unit[first]] = ids[t];  // the same value from all of the expert's slots
+    slot[unit[first]][t / q.K] = int16_t(t);
+  }
+  __syncthreads();
+  const int chunks = (q.H + kCols<T> - 1) / kCols<T>;
+  const int64_t col0 = int64_t(blockIdx.x % chunks) * kCols<T>;
+  const int part = blockIdx.x / chunks;
+  if (col0 + kCols<T> <= q.H)
+    down_all<T, 2, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
+  else
+    down_all<T, 1, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
+  if (arrived == nullptr) return;
+  // every thread's part is in memory before the count says so, and the last
+  // workgroup reads the parts only after it has counted all of them
+  __syncthreads();
+  if (t == 0) {
+    __threadfence();
+    counts[0] = atomicAdd(&arrived[blockIdx.x % chunks], 1) == q.dn_parts - 1;
+  }
+  __syncthreads();
+  if (!counts[0]) return;
+  __threadfence();
+  const int64_t h = col0 + t;
+  if (t >= kCols<T> || h >= q.H) return;
+  for (int n = 0; n < q.N; ++n) {
+    float v = 0.f;
+    for (int s0 = 0; s0 < q.dn_parts; s0 += 16) {
+      float p[16];
+#pragma unroll
+      for (int s = 0; s < 16; ++s) p[s] = s0 + s < q.dn_parts ? yp[(int64_t(s0 + s) * q.N + n) * q.H + h] : 0.f;
+#pragma unroll
+      for (int s = 0; s < 16; ++s) v += p[s];
+    }
+    y[n * int64_t(q.H) + h] = Elt<T>::from_f32(v);
+  }
+}
+
+// y[n] = sum over the parts of a token's `per` rows (+ the shared expert's
+// parts), float32, one rounding.  64 columns a workgroup; thread (slice, column)
+// sums every fourth row, eight loads in flight, and the slices meet in order.
 template <typename T>
 __global__ __launch_bounds__(256) void k_decode_combine(const float* __restrict__ ysp, const float* __restrict__ sysp,
-                                                        const float* __restrict__ gates, T* __restrict__ y, int N,
-                                                        int H, int K, int splits, int ssplits) {
-  const int h = blockIdx.x * 256 + threadIdx.x;
-  const int n = blockIdx.y;
-  if (h >= H) return;
+                                                        T* __restrict__ y, int N, int H, int per, int parts,
+                                                        int sparts) {
+  __shared__ float s[4][64];
+  const int col = threadIdx.x % 64, slice = threadIdx.x / 64;
+  const int h = blockIdx.x * 64 + col, n = blockIdx.y;
+  const int routed = per * parts, all = routed + sparts;
   float v = 0.f;
-  for (int k = 0; k < K; ++k) {
-    float a = 0.f;
-    for (int s = 0; s < splits; ++s) a += ysp[(int64_t(s) * N * K + n * K + k) * H + h];
-    v = fmaf(gates[n * K + k], a, v);
+  for (int i0 = slice; i0 < all; i0 += 32) {
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + 4 * j;
+      const float* p = i < routed ? ysp + (int64_t(i / per) * N + n) * per * H + int64_t(i % per) * H
+                                  : sysp + (int64_t(i - routed) * N + n) * H;
+      t[j] = i < all ? p[h] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += t[j];
   }
-  for (int s = 0; s < ssplits; ++s) v += sysp[(int64_t(s) * N + n) * H + h];
-  y[int64_t(n) * H + h] = Elt<T>::from_f32(v);
+  s[slice][col] = v;
+  __syncthreads();
+  if (slice == 0) y[int64_t(n) * H + h] = Elt<T>::from_f32(((s[0][col] + s[1][col]) + s[2][col]) + s[3][col]);
 }
 
 // ------------------------------------------------------------------- host
 
 // How the call is cut up, and where its scratch lies.
 struct Plan {
-  int logit_parts, units, splits, ssplits;
-  size_t logits, act, sact, ysp, sysp, bytes;
+  Shape q;
+  int logit_parts;
+  bool few;    // at most 16 tokens: k_decode_down_all
+  bool joint;  // k_decode_gate_up_act; else k_decode_gate_up, and then
+  bool route;  // ... which finds topk itself, and with logit_parts == 0 the logits too
+  bool last;   // the last workgroups of k_decode_down_all write y
+  bool fused;  // k_decode_down_all forms the activations itself, else k_decode_act does
+  size_t logits, xp, arrived, gu, sgu, act, sact, ysp, sysp, bytes;
 };
 
-int splits_of(int64_t f, int64_t blocks) {
-  // enough workgroups for two on each of 256 CUs, with two panels per wave at least
-  int s = 1;
-  while (s * blocks < 512 && f / 32 >= int64_t(4) * s * kWaves) s *= 2;
-  return s;
+constexpr int64_t kCUs = 256;
+
+// Workgroups that share a strip of `panels` panels when there are about
+// `strips` strips.  Every CU takes its workgroups' panels at the same rate, so the
+// fullest CU sets the time: ceil(strips * p / CUs) / p strips' worth; three
+// workgroups fit a CU at once, and a fourth would wait for their end.  0.6 us a
+// panel for a CU, about 1.2 us of latency for each of a wave's first panels.
+int cut(double strips, int64_t panels) {
+  int best = 1;
+  double least = 0.0;
+  for (int p = 1; p <= 4 && kWaves * p <= panels && (p == 1 || strips * p <= 3.0 * kCUs); ++p) {
+    const double t = std::ceil(strips * p / double(kCUs)) / p * 0.6 * double(panels) +
+                     1.2 * std::min(4.0, double(panels) / (kWaves * p));
+    if (p == 1 || t < least) {
+      best = p;
+      least = t;
+    }
+  }
+  return best;
 }
 
-Plan plan_of(const moe_launch::Dims& d, int64_t Fs) {
+template <typename T>
+Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
+  constexpr int cols = kCols<T>;
   Plan p;
-  const int cw = d.dtype == MOE_BF16 ? 8 : 4;
-  const int64_t chunks = d.H / (16 * cw), NK = d.NK();
-  p.logit_parts = int(d.H / kLogitRows);
-  p.units = int(std::min(NK, d.E));
-  p.splits = splits_of(d.F, chunks * p.units);
-  p.ssplits = Fs > 0 ? splits_of(Fs, chunks) : 0;
+  Shape& q = p.q;
+  q = Shape{};
+  q.N = int(d.N); q.H = int(d.H); q.F = int(d.F); q.Fs = int(Fs); q.E = int(d.E); q.K = int(d.K);
+  const int64_t NK = d.NK();
+  const int64_t fchunks = (d.F + cols - 1) / cols, schunks = (Fs + cols - 1) / cols, chunks = (d.H + cols - 1) / cols;
+  q.units = int(std::min(NK, d.E));
+  // experts that N tokens choose if they choose evenly
+  const double used = double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N)));
+  p.few = d.N <= 16;
+  p.joint = q.units * fchunks + schunks >= 200 && NK >= 8 * q.units;
+  q.gu_parts = p.joint ? 1 : cut(2.0 * (used * double(fchunks) + double(schunks)), d.H / 32);
+  p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
+  p.route = !p.joint && d.N <= kRouteTok;
+  p.logit_parts = int((d.H + kLogitRows - 1) / kLogitRows);
+  if (p.route && (d.E + 15) / 16 * (d.H / 32) <= 8 * kWaves) p.logit_parts = 0;
+  if (p.few) {
+    const double panels = used * double(d.F / 32) + double(Fs / 32);
+    const int64_t want = std::max(kCUs / chunks, int64_t(panels / (4 * kWaves)));
+    q.dn_parts = int(std::max<int64_t>(1, std::min({int64_t(panels / kWaves), 2 * kCUs / chunks, want})));
+  } else {
+    // two workgroups fit a CU (row tiles take the registers); a longer shared strip is cut more often
+    q.dn_parts = 1;
+    while (used * double(chunks) * 2 * q.dn_parts <= 2.2 * kCUs && d.F / 32 >= int64_t(2) * q.dn_parts * kWaves)
+      q.dn_parts *= 2;
+    q.sdn_parts = int(Fs == 0 ? 0 : std::min(Fs / (32 * kWaves), q.dn_parts * ((Fs + d.F - 1) / d.F)));
+  }
+  p.last = p.few && chunks * q.dn_parts <= 64;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -482,72 +1067,131 @@ Plan plan_of(const moe_launch::Dims& d, int64_t Fs) {
     return here;
   };
   p.logits = take(size_t(p.logit_parts) * d.N * d.E * sizeof(double));
-  p.act = take(size_t(NK) * d.F * 4);  // bf16: hi and lo planes; float32: one plane
-  p.sact = take(size_t(d.N) * Fs * 4);
-  p.ysp = take(size_t(p.splits) * NK * d.H * 4);
-  p.sysp = take(size_t(p.ssplits) * d.N * d.H * 4);
+  p.xp = take(size_t(d.N) * d.H * sizeof(T));
+  p.arrived = take(size_t(chunks) * sizeof(int32_t));
+  p.gu = take(p.joint ? 0 : size_t(q.gu_parts) * 2 * NK * d.F * 4);
+  p.sgu = take(p.joint ? 0 : size_t(q.gu_parts) * 2 * d.N * Fs * 4);
+  p.act = take(p.fused ? 0 : size_t(NK) * d.F * 4);
+  p.sact = take(p.fused ? 0 : size_t(d.N) * Fs * 4);
+  p.ysp = take(size_t(q.dn_parts) * (p.few ? d.N : NK) * d.H * 4);
+  p.sysp = take(p.few ? 0 : size_t(q.sdn_parts) * d.N * d.H * 4);
   p.bytes = at;
   return p;
 }
 
-template <typename T, int CW, int MT>
-hipError_t decode_experts(const moe_launch::Dims& d, const Plan& p, const T* x, const T* wg, const T* wu, const T* wd,
-                          int64_t Fs, const T* swg, const T* swu, const T* swd, const int32_t* topk, char* ws,
-                          hipStream_t s) {
-  const int N = int(d.N), H = int(d.H), F = int(d.F), E = int(d.E), K = int(d.K);
-  T* act = reinterpret_cast<T*>(ws + p.act);
-  T* sact = reinterpret_cast<T*>(ws + p.sact);
-  const unsigned gu = unsigned(p.units * (F / (16 * CW)) + Fs / (16 * CW));
-  k_decode_gate_up<T, CW, MT><<<dim3(gu), dim3(kNT), 0, s>>>(x, wg, wu, swg, swu, topk, act, sact, N, H, F, int(Fs), E,
-                                                             K, p.units);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const unsigned dn = unsigned((p.units * p.splits + p.ssplits) * (H / (16 * CW)));
-  k_decode_down<T, CW, MT><<<dim3(dn), dim3(kNT), 0, s>>>(act, sact, wd, swd, topk, reinterpret_cast<float*>(ws + p.ysp),
-                                                          reinterpret_cast<float*>(ws + p.sysp), N, H, F, int(Fs), E,
-                                                          K, p.units, p.splits, p.ssplits);
+// Pointers of one call.
+template <typename T> struct Args {
+  const T *x, *w_r;
+  const float* bias;
+  const T *wg, *wu, *wd, *swg, *swu, *swd;
+  int32_t* topk;
+  float* gates;
+  T* y;
+  char* ws;
+};
+
+#define MOE_LAUNCHED()                 \
+  {                                    \
+    const hipError_t e = hipGetLastError(); \
+    if (e != hipSuccess) return e;     \
+  }
+
+template <typename T, int MTMAX>
+hipError_t decode_experts(const Plan& p, const Args<T>& a, hipStream_t s) {
+  const Shape& q = p.q;
+  constexpr int cols = kCols<T>;
+  const unsigned chunks = (q.H + cols - 1) / cols;
+  float* gu = reinterpret_cast<float*>(a.ws + p.gu);
+  float* sgu = reinterpret_cast<float*>(a.ws + p.sgu);
+  T* act = reinterpret_cast<T*>(a.ws + p.act);
+  T* sact = reinterpret_cast<T*>(a.ws + p.sact);
+  float* ysp = reinterpret_cast<float*>(a.ws + p.ysp);
+  float* sysp = reinterpret_cast<float*>(a.ws + p.sysp);
+  int32_t* arrived = p.last ? reinterpret_cast<int32_t*>(a.ws + p.arrived) : nullptr;
+  const int n_arrived = p.last ? int(chunks) : 0;
+  const T* xp = reinterpret_cast<const T*>(a.ws + p.xp);
+  const XRows<T> x = p.logit_parts > 0 ? XRows<T>{xp, 32, 32 * q.N} : XRows<T>{a.x, q.H, 32};
+  const Route<T> route{a.x, a.w_r, p.logit_parts > 0 ? reinterpret_cast<const double*>(a.ws + p.logits) : nullptr,
+                       a.bias, p.logit_parts};
+  const unsigned strips = 2 * (unsigned(q.units) * ((q.F + cols - 1) / cols) + (q.Fs + cols - 1) / cols) * q.gu_parts;
+  if (p.joint) {
+    k_decode_gate_up_act<T, MTMAX><<<dim3(strips / 2), dim3(kNT), 0, s>>>(x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates,
+                                                                          arrived, n_arrived, act, sact, q);
+  } else {
+    bool done = false;
+    if constexpr (MTMAX == 1)
+      if (p.route) {
+        k_decode_gate_up<T, 1, true><<<dim3(strips), dim3(kNT), 0, s>>>(x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates,
+                                                                        route, arrived, n_arrived, gu, sgu, q);
+        done = true;
+      }
+    if (!done)
+      k_decode_gate_up<T, MTMAX, false><<<dim3(strips), dim3(kNT), 0, s>>>(
+          x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates, route, arrived, n_arrived, gu, sgu, q);
+    MOE_LAUNCHED()
+    if (!p.fused) {
+      const int64_t groups = (int64_t(q.N) * q.K * q.F + int64_t(q.N) * q.Fs) / 8;
+      k_decode_act<T><<<dim3(unsigned(std::min<int64_t>((groups + 255) / 256, 1 << 16))), dim3(256), 0, s>>>(
+          gu, sgu, a.gates, act, sact, q);
+    }
+  }
+  MOE_LAUNCHED()
+  if constexpr (MTMAX == 1) {
+    const dim3 grid(chunks * q.dn_parts);
+    if (p.fused)
+      k_decode_down_all<T, true><<<grid, dim3(kNT), 0, s>>>(Rows<T, true>{gu, sgu}, a.wd, a.swd, a.topk, a.gates, ysp,
+                                                            arrived, a.y, q);
+    else
+      k_decode_down_all<T, false><<<grid, dim3(kNT), 0, s>>>(Rows<T, false>{act, sact}, a.wd, a.swd, a.topk, a.gates,
+                                                             ysp, arrived, a.y, q);
+  } else {
+    k_decode_down<T, MTMAX><<<dim3((q.units * q.dn_parts + q.sdn_parts) * chunks), dim3(kNT), 0, s>>>(
+        act, sact, a.wd, a.swd, a.topk, ysp, sysp, q);
+  }
+  if (!p.last) {
+    MOE_LAUNCHED()
+    k_decode_combine<T><<<dim3(q.H / 64, q.N), dim3(256), 0, s>>>(ysp, sysp, a.y, q.N, q.H, MTMAX == 1 ? 1 : q.K,
+                                                                  q.dn_parts, MTMAX == 1 ? 0 : q.sdn_parts);
+  }
   return hipGetLastError();
 }
 
-template <typename T, int CW>
-hipError_t decode_t(const moe_launch::Dims& d, const T* x, const T* w_r, const float* bias, const T* wg, const T* wu,
-                    const T* wd, int64_t Fs, const T* swg, const T* swu, const T* swd, int32_t* topk, float* gates,
-                    T* y, char* ws, hipStream_t s) {
-  const Plan p = plan_of(d, Fs);
-  const int N = int(d.N), H = int(d.H), E = int(d.E), K = int(d.K);
-  double* logits = reinterpret_cast<double*>(ws + p.logits);
-  k_decode_logits<T><<<dim3(p.logit_parts), dim3(256), 0, s>>>(x, w_r, logits, N, H, E);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_decode_topk<<<dim3(N), dim3(256), 0, s>>>(logits, bias, topk, gates, N, E, K, p.logit_parts);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (N <= 16)
-    e = decode_experts<T, CW, 1>(d, p, x, wg, wu, wd, Fs, swg, swu, swd, topk, ws, s);
-  else
-    e = decode_experts<T, CW, 2>(d, p, x, wg, wu, wd, Fs, swg, swu, swd, topk, ws, s);
-  if (e != hipSuccess) return e;
-  k_decode_combine<T><<<dim3((H + 255) / 256, N), dim3(256), 0, s>>>(
-      reinterpret_cast<const float*>(ws + p.ysp), reinterpret_cast<const float*>(ws + p.sysp), gates, y, N, H, K,
-      p.splits, p.ssplits);
-  return hipGetLastError();
+template <typename T>
+hipError_t decode_t(const moe_launch::Dims& d, int64_t Fs, const Args<T>& a, hipStream_t s) {
+  const Plan p = plan_t<T>(d, Fs);
+  const Shape& q = p.q;
+  double* logits = reinterpret_cast<double*>(a.ws + p.logits);
+  if (p.logit_parts > 0) {
+    k_decode_logits<T><<<dim3(p.logit_parts, (q.E + 15) / 16), dim3(kLogitWaves * kWave), 0, s>>>(
+        a.x, a.w_r, logits, reinterpret_cast<T*>(a.ws + p.xp), q.N, q.H, q.E);
+    MOE_LAUNCHED()
+  }
+  if (!p.route) {
+    k_decode_topk<<<dim3(q.N), dim3(256), 0, s>>>(logits, a.bias, a.topk, a.gates, q.N, q.E, q.K, p.logit_parts);
+    MOE_LAUNCHED()
+  }
+  if (q.N <= 16) return decode_experts<T, 1>(p, a, s);
+  if (q.N <= 32) return decode_experts<T, 2>(p, a, s);
+  return decode_experts<T, 4>(p, a, s);
 }
 
 }  // namespace
 
 namespace moe_launch {
 
-size_t decode_ws(const Dims& d, int64_t Fs) { return plan_of(d, Fs).bytes; }
+size_t decode_ws(const Dims& d, int64_t Fs) {
+  return d.dtype == MOE_BF16 ? plan_t<bf16_t>(d, Fs).bytes : plan_t<float>(d, Fs).bytes;
+}
 
 hipError_t decode(const Dims& d, const void* x, const void* w_r, const float* bias, const void* wg, const void* wu,
                   const void* wd, int64_t Fs, const void* swg, const void* swu, const void* swd, int32_t* topk,
                   float* gates, void* y, void* ws, hipStream_t s) {
-  char* w = static_cast<char*>(ws);
-#define MOE_DECODE(T, CW)                                                                                          \
-  decode_t<T, CW>(d, static_cast<const T*>(x), static_cast<const T*>(w_r), bias, static_cast<const T*>(wg),        \
-                  static_cast<const T*>(wu), static_cast<const T*>(wd), Fs, static_cast<const T*>(swg),            \
-                  static_cast<const T*>(swu), static_cast<const T*>(swd), topk, gates, static_cast<T*>(y), w, s)
-  return d.dtype == MOE_BF16 ? MOE_DECODE(bf16_t, 8) : MOE_DECODE(float, 4);
+#define MOE_DECODE(T)                                                                                              \
+  decode_t<T>(d, Fs, Args<T>{static_cast<const T*>(x), static_cast<const T*>(w_r), bias, static_cast<const T*>(wg),  \
+                             static_cast<const T*>(wu), static_cast<const T*>(wd), static_cast<const T*>(swg),     \
+                             static_cast<const T*>(swu), static_cast<const T*>(swd), topk, gates,                  \
+                             static_cast<T*>(y), static_cast<char*>(ws)}, s)
+  return d.dtype == MOE_BF16 ? MOE_DECODE(bf16_t) : MOE_DECODE(float);
 #undef MOE_DECODE
 }
 
