@@ -444,12 +444,36 @@ __device__ __forceinline__ void park(const f32x4_t (&acc)[CW], float* mine) {
           f32x4_t{acc[i][r], acc[i + 1][r], acc[i + 2][r], acc[i + 3][r]};
 }
 
-// The waves' sums of each 16 x 16*CW piece added in wave order; out(m, s, row,
-// first of 4 columns, their sums) for all of it, by all threads.  red: 16 * 16
-// * CW floats per wave.
-template <int MT, int S, int CW, typename F>
-__device__ __forceinline__ void join_waves(const f32x4_t (&acc)[MT][S][CW], float* red, F out) {
-  constexpr int W = 16 * CW, PIECE = 16 * W;
+// How the four waves of a workgroup share its columns and its contraction:
+//   all split the contraction (the sums of a piece are all waves');
+//   JOINT: even waves have W_gate, odd ones W_up;
+//   HALVES: the first two waves have the first segment, the others the second,
+//   so that twice the row tiles fit the registers and a row's 512 bytes are
+//   still read together.
+template <bool JOINT, bool HALVES>
+struct Role {
+  static constexpr int KW = kWaves / (JOINT ? 2 : 1) / (HALVES ? 2 : 1);  // waves along the contraction
+  int mat, seg, k;
+  __device__ __forceinline__ Role() {
+    const int w = threadIdx.x / kWave;
+    mat = JOINT ? w % 2 : 0;
+    seg = HALVES ? w / 2 : 0;
+    k = HALVES ? (JOINT ? 0 : w % 2) : JOINT ? w / 2 : w;
+  }
+  // wave of a role
+  static __device__ __forceinline__ int wave(int mat, int seg, int k) {
+    return HALVES ? 2 * seg + (JOINT ? mat : k) : JOINT ? 2 * k + mat : k;
+  }
+};
+
+// The waves' sums of each 16 x 16*CW piece added in wave order; out(row tile,
+// segment, row, first of 4 columns, their sums), with JOINT out(..., first of 8
+// columns, their G and U sums as 4 vectors), for all of it.  red: 16 * 16 * CW
+// floats per wave.
+template <bool JOINT, bool HALVES, int MT, int S, int CW, typename F>
+__device__ __forceinline__ void join(const f32x4_t (&acc)[MT][S][CW], float* red, F out) {
+  typedef Role<JOINT, HALVES> R;
+  constexpr int W = 16 * CW, PIECE = 16 * W, C = JOINT ? 8 : 4;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -457,13 +481,17 @@ __device__ __forceinline__ void join_waves(const f32x4_t (&acc)[MT][S][CW], floa
       __syncthreads();
       park(acc[m][s], red + threadIdx.x / kWave * PIECE);
       __syncthreads();
+      for (int j = C * threadIdx.x; j < (HALVES ? 2 : 1) * PIECE; j += C * kNT) {
+        const int h = j / PIECE, i = j % PIECE;
+        f32x4_t v[JOINT ? 4 : 1];
 #pragma unroll
-      for (int t = 0; t < PIECE / 4 / kNT; ++t) {
-        const int i = 4 * (t * kNT + threadIdx.x);
-        f32x4_t v = *reinterpret_cast<const f32x4_t*>(red + i);
+        for (int n = 0; n < (JOINT ? 4 : 1); ++n) {  // G, U of the first four columns, then of the others
+          const float* p = red + i + n / 2 * 4;
+          v[n] = *reinterpret_cast<const f32x4_t*>(p + R::wave(n % 2, h, 0) * PIECE);
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(red + w * PIECE + i);
-        out(m, s, i / W, i % W, v);
+          for (int k = 1; k < R::KW; ++k) v[n] += *reinterpret_cast<const f32x4_t*>(p + R::wave(n % 2, h, k) * PIECE);
+        }
+        out(m, s + h, i / W, i % W, v);
       }
     }
 }
@@ -509,37 +537,6 @@ struct Act {
 };
 
 
-// As join_waves for waves that hold G (even) and U (odd): out(m, s, row, first
-// of 8 columns, their G and U).
-template <int MT, int S, int CW, typename F>
-__device__ __forceinline__ void join_pairs(const f32x4_t (&acc)[MT][S][CW], float* red, F out) {
-  constexpr int W = 16 * CW, PIECE = 16 * W;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      __syncthreads();
-      park(acc[m][s], red + threadIdx.x / kWave * PIECE);
-      __syncthreads();
-      const int i = 8 * threadIdx.x;
-      if (i < PIECE) {
-        Act a;
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          f32x4_t v[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            v[k] = *reinterpret_cast<const f32x4_t*>(red + k * PIECE + i + j);
-#pragma unroll
-            for (int w = k + 2; w < kWaves; w += 2) v[k] += *reinterpret_cast<const f32x4_t*>(red + w * PIECE + i + j);
-          }
-          a.take(j, v[0], v[1]);
-        }
-        out(m, s, i / W, i % W, a);
-      }
-    }
-}
-
 // Where the sums of gate and up go.
 template <typename T, bool JOINT> struct GuOut;
 // One matrix: its sums, [row][ld].
@@ -560,14 +557,16 @@ template <typename T> struct XRows {
   int row_step, panel_step;
 };
 
-// x times W for up to 16*MT rows (row r: token rows[r] /
-// div) and S segments from col0, over panels first, first + step, ....  JOINT:
-// even waves have W_gate, odd ones W_up.
-template <typename T, int S, int MT, bool JOINT>
-__device__ __forceinline__ void gate_up_rows(const XRows<T>& x, const T* w, int H, int64_t ld,
-                                             int64_t col0, const int* rows, int M, int div, int first, int step,
+// x times W for up to 16*MT rows (row r: token rows[r] / div) and the columns
+// from col0 (S segments, or two with HALVES), part `part` of `parts` of the
+// contraction.
+template <typename T, int S, int MT, bool JOINT, bool HALVES>
+__device__ __forceinline__ void gate_up_rows(const XRows<T>& x, const T* wg, const T* wu, int H, int64_t ld,
+                                             int64_t col0, const int* rows, int M, int div, int part, int parts,
                                              const GuOut<T, JOINT>& out, float* red) {
   typedef Panel<T, S> P;
+  constexpr int SEG = 16 * P::CW;
+  const Role<JOINT, HALVES> role;
   const int g = lane_id() / 16, c = lane_id() % 16;
   f32x4_t acc[MT][S][P::CW];
   clear(acc);
@@ -577,55 +576,51 @@ __device__ __forceinline__ void gate_up_rows(const XRows<T>& x, const T* w, int 
     const int r = 16 * m + c;
     px[m] = x.p + int64_t(rows[r < M ? r : 0] / div) * x.row_step + 8 * g;
   }
-  const T* pw = w + 8 * g * ld + col0 + P::CW * c;
-  for (int i = first; i < H / 32; i += step) {
-    P p;
-    typename P::A a[MT];
+  const T* pw = (JOINT && role.mat ? wu : wg) + 8 * g * ld + col0 + role.seg * SEG + P::CW * c;
+  if (!HALVES || col0 + role.seg * SEG < ld)
+    for (int i = part * role.KW + role.k; i < H / 32; i += parts * role.KW) {
+      P p;
+      typename P::A a[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) a[m].load(px[m] + int64_t(i) * x.panel_step);
-    p.load(pw + int64_t(i) * 32 * ld, ld);
-    p.template multiply<MT>(a, acc);
-  }
-  if constexpr (JOINT) {
-    join_pairs(acc, red, [&](int m, int s, int row, int col, const Act& act) {
-      const int r = 16 * m + row;
-      if (r < M) {
-        float v[8];
-        act.finish(out.gates != nullptr ? out.gates[rows[r]] : 1.f, v);
-        typename P::A2 o;
-        o.set(v);
-        const int64_t at = col0 + s * 16 * P::CW + col;
-        o.store(out.act + (at / 32 * out.R + rows[r]) * 32 + at % 32, ld * out.R);
-      }
-    });
-  } else {
-    join_waves(acc, red, [&](int m, int s, int row, int col, f32x4_t v) {
-      const int r = 16 * m + row;
-      if (r < M) *reinterpret_cast<f32x4_t*>(out.sums + rows[r] * ld + col0 + s * 16 * P::CW + col) = v;
-    });
-  }
+      for (int m = 0; m < MT; ++m) a[m].load(px[m] + int64_t(i) * x.panel_step);
+      p.load(pw + int64_t(i) * 32 * ld, ld);
+      p.template multiply<MT>(a, acc);
+    }
+  join<JOINT, HALVES>(acc, red, [&](int m, int s, int row, int col, const f32x4_t* v) {
+    const int r = 16 * m + row;
+    const int64_t at = col0 + s * SEG + col;
+    if (r >= M || (HALVES && at >= ld)) return;
+    if constexpr (JOINT) {
+      Act act;
+      act.take(0, v[0], v[1]);
+      act.take(4, v[2], v[3]);
+      float f[8];
+      act.finish(out.gates != nullptr ? out.gates[rows[r]] : 1.f, f);
+      typename P::A2 o;
+      o.set(f);
+      o.store(out.act + (at / 32 * out.R + rows[r]) * 32 + at % 32, ld * out.R);
+    } else {
+      *reinterpret_cast<f32x4_t*>(out.sums + rows[r] * ld + at) = v[0];
+    }
+  });
 }
 
 // All M rows of one expert and the workgroup's columns.
 template <typename T, int MTMAX, bool JOINT>
-__device__ __forceinline__ void gate_up(const XRows<T>& x, const T* w, int H, int64_t ld, int64_t col0,
-                                        const int* rows, int M, int div, int first, int step,
+__device__ __forceinline__ void gate_up(const XRows<T>& x, const T* wg, const T* wu, int H, int64_t ld, int64_t col0,
+                                        const int* rows, int M, int div, int part, int parts,
                                         const GuOut<T, JOINT>& out, float* red) {
-  constexpr int HALF = kCols<T> / 2;
-  if (col0 + kCols<T> <= ld && M <= 32) {
-    if (M <= 16 || MTMAX == 1)
-      gate_up_rows<T, 2, 1, JOINT>(x, w, H, ld, col0, rows, M, div, first, step, out, red);
-    else
-      gate_up_rows<T, 2, (MTMAX > 1 ? 2 : 1), JOINT>(x, w, H, ld, col0, rows, M, div, first, step, out, red);
-  } else {
-    // a last single segment, or more rows than two segments' sums leave registers for
-    for (int64_t col = col0; col < col0 + kCols<T> && col < ld; col += HALF) {
-      if (M <= 16 || MTMAX == 1)
-        gate_up_rows<T, 1, 1, JOINT>(x, w, H, ld, col, rows, M, div, first, step, out, red);
-      else
-        gate_up_rows<T, 1, MTMAX, JOINT>(x, w, H, ld, col, rows, M, div, first, step, out, red);
-    }
-  }
+  const bool wide = col0 + kCols<T> <= ld;  // else a last single segment
+  if constexpr (MTMAX > 2)
+    if (M > 32) return gate_up_rows<T, 1, 4, JOINT, true>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
+  if constexpr (MTMAX > 1)
+    if (M > 16)
+      return wide ? gate_up_rows<T, 2, 2, JOINT, false>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red)
+                  : gate_up_rows<T, 1, 2, JOINT, false>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
+  if (wide)
+    gate_up_rows<T, 2, 1, JOINT, false>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
+  else
+    gate_up_rows<T, 1, 1, JOINT, false>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
 }
 
 // What the experts' kernels share.
@@ -663,7 +658,6 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* 
       gates[threadIdx.x] = routed.gates[threadIdx.x];
     }
   }
-  const int wave = threadIdx.x / kWave;
   const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
   const int schunks = (q.Fs + kCols<T> - 1) / kCols<T>, shared = 2 * q.gu_parts * schunks;
   int b = int(blockIdx.x) - shared;
@@ -674,8 +668,8 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* 
     int e = 0;
     const int M = unit_rows(topk, q.N * q.K, b / 2 / q.gu_parts, &chosen, &e, rows);
     if (M == 0) return;
-    gate_up<T, MTMAX, false>(x, (mat ? wu : wg) + int64_t(e) * q.H * q.F, q.H, q.F, int64_t(chunk) * kCols<T>,
-                             rows, M, q.K, part * kWaves + wave, q.gu_parts * kWaves,
+    gate_up<T, MTMAX, false>(x, (mat ? wu : wg) + int64_t(e) * q.H * q.F, nullptr, q.H, q.F,
+                             int64_t(chunk) * kCols<T>, rows, M, q.K, part, q.gu_parts,
                              GuOut<T, false>{gu + int64_t(part * 2 + mat) * q.N * q.K * q.F}, red);
   } else {
     b += shared;
@@ -684,8 +678,8 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* 
     const int mat = b % 2, part = b / 2;
     if (threadIdx.x < kTok) rows[threadIdx.x] = threadIdx.x;
     __syncthreads();
-    gate_up<T, MTMAX, false>(x, mat ? swu : swg, q.H, q.Fs, int64_t(chunk) * kCols<T>, rows, q.N, 1,
-                             part * kWaves + wave, q.gu_parts * kWaves,
+    gate_up<T, MTMAX, false>(x, mat ? swu : swg, nullptr, q.H, q.Fs, int64_t(chunk) * kCols<T>, rows, q.N, 1, part,
+                             q.gu_parts,
                              GuOut<T, false>{sgu + int64_t(part * 2 + mat) * q.N * q.Fs}, red);
   }
 }
@@ -705,7 +699,6 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up_act(XRows<T> x, const
   __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
-  const int wave = threadIdx.x / kWave;
   const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
   const int shared = (q.Fs + kCols<T> - 1) / kCols<T>;
   int b = int(blockIdx.x) - shared;
@@ -713,15 +706,15 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up_act(XRows<T> x, const
     int e = 0;
     const int M = unit_rows(topk, q.N * q.K, b / chunks, &chosen, &e, rows);
     if (M == 0) return;
-    gate_up<T, MTMAX, true>(x, (wave % 2 ? wu : wg) + int64_t(e) * q.H * q.F, q.H, q.F,
-                            int64_t(b % chunks) * kCols<T>, rows, M, q.K, wave / 2, kWaves / 2,
+    const int64_t at = int64_t(e) * q.H * q.F;
+    gate_up<T, MTMAX, true>(x, wg + at, wu + at, q.H, q.F, int64_t(b % chunks) * kCols<T>, rows, M, q.K, 0, 1,
                             GuOut<T, true>{act, gates, q.N * q.K}, red);
   } else {
     b += shared;
     if (threadIdx.x < kTok) rows[threadIdx.x] = threadIdx.x;
     __syncthreads();
-    gate_up<T, MTMAX, true>(x, wave % 2 ? swu : swg, q.H, q.Fs, int64_t(b) * kCols<T>, rows, q.N, 1, wave / 2,
-                            kWaves / 2, GuOut<T, true>{sact, nullptr, q.N}, red);
+    gate_up<T, MTMAX, true>(x, swg, swu, q.H, q.Fs, int64_t(b) * kCols<T>, rows, q.N, 1, 0, 1,
+                            GuOut<T, true>{sact, nullptr, q.N}, red);
   }
 }
 
@@ -750,52 +743,52 @@ __global__ __launch_bounds__(256) void k_decode_act(const float* __restrict__ gu
   }
 }
 
-// One expert's rows (slots rows[0, M)) times its W_down, panels first, first +
-// step, ...: sums to out[rows[r]][H].
-template <typename T, int S, int MT>
+// One expert's rows (slots rows[0, M)) times its W_down, part `part` of `parts` of
+// the contraction: sums to out[rows[r]][H].
+template <typename T, int S, int MT, bool HALVES>
 __device__ __forceinline__ void down_rows(const T* __restrict__ act, int64_t plane, const T* wd, int F, int64_t H,
-                                          int64_t col0, const int* rows, int M, int first, int step, float* out,
+                                          int64_t col0, const int* rows, int M, int part, int parts, float* out,
                                           float* red) {
   typedef Panel<T, S> P;
+  constexpr int SEG = 16 * P::CW;
+  const Role<false, HALVES> role;
   const int g = lane_id() / 16, c = lane_id() % 16;
   f32x4_t acc[MT][S][P::CW];
   clear(acc);
   const T* pa[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) pa[m] = act + rows[16 * m + c < M ? 16 * m + c : 0] * 32 + 8 * g;
-  const T* pw = wd + 8 * g * H + col0 + P::CW * c;
-  for (int i = first; i < F / 32; i += step) {
-    P p;
-    typename P::A2 a[MT];
+  const T* pw = wd + 8 * g * H + col0 + role.seg * SEG + P::CW * c;
+  if (!HALVES || col0 + role.seg * SEG < H)
+    for (int i = part * role.KW + role.k; i < F / 32; i += parts * role.KW) {
+      P p;
+      typename P::A2 a[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) a[m].load(pa[m] + int64_t(i) * 32 * (plane / F), plane);
-    p.load(pw + int64_t(i) * 32 * H, H);
-    p.template multiply<MT>(a, acc);
-  }
-  join_waves(acc, red, [&](int m, int s, int row, int col, f32x4_t v) {
+      for (int m = 0; m < MT; ++m) a[m].load(pa[m] + int64_t(i) * 32 * (plane / F), plane);
+      p.load(pw + int64_t(i) * 32 * H, H);
+      p.template multiply<MT>(a, acc);
+    }
+  join<false, HALVES>(acc, red, [&](int m, int s, int row, int col, const f32x4_t* v) {
     const int r = 16 * m + row;
-    if (r < M) *reinterpret_cast<f32x4_t*>(out + rows[r] * H + col0 + s * 16 * P::CW + col) = v;
+    const int64_t at = col0 + s * SEG + col;
+    if (r < M && (!HALVES || at < H)) *reinterpret_cast<f32x4_t*>(out + rows[r] * H + at) = v[0];
   });
 }
 
 template <typename T, int MTMAX>
 __device__ __forceinline__ void down(const T* __restrict__ act, int64_t plane, const T* wd, int F, int64_t H,
-                                     int64_t col0, const int* rows, int M, int first, int step, float* out,
+                                     int64_t col0, const int* rows, int M, int part, int parts, float* out,
                                      float* red) {
-  constexpr int HALF = kCols<T> / 2;
-  if (col0 + kCols<T> <= H && M <= 32) {
-    if (M <= 16)
-      down_rows<T, 2, 1>(act, plane, wd, F, H, col0, rows, M, first, step, out, red);
-    else
-      down_rows<T, 2, 2>(act, plane, wd, F, H, col0, rows, M, first, step, out, red);
-  } else {
-    for (int64_t col = col0; col < col0 + kCols<T> && col < H; col += HALF) {
-      if (M <= 16)
-        down_rows<T, 1, 1>(act, plane, wd, F, H, col, rows, M, first, step, out, red);
-      else
-        down_rows<T, 1, MTMAX>(act, plane, wd, F, H, col, rows, M, first, step, out, red);
-    }
-  }
+  const bool wide = col0 + kCols<T> <= H;
+  if constexpr (MTMAX > 2)
+    if (M > 32) return down_rows<T, 1, 4, true>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
+  if (M > 16)
+    return wide ? down_rows<T, 2, 2, false>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red)
+                : down_rows<T, 1, 2, false>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
+  if (wide)
+    down_rows<T, 2, 1, false>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
+  else
+    down_rows<T, 1, 1, false>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
 }
 
 // More than 16 tokens: a workgroup has one expert's columns and part of its
@@ -808,24 +801,23 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down(const T* __restrict__ ac
   __shared__ Chosen chosen;
   __shared__ int rows[kTok];
   __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
-  const int wave = threadIdx.x / kWave;
   const int chunks = (q.H + kCols<T> - 1) / kCols<T>;
   int b = blockIdx.x;
   const int64_t col0 = int64_t(b % chunks) * kCols<T>;
   b /= chunks;
   b -= q.sdn_parts;
   if (b >= 0) {
-    const int part = b % q.dn_parts, u = b / q.dn_parts, first = part * kWaves + wave, step = q.dn_parts * kWaves;
+    const int part = b % q.dn_parts, u = b / q.dn_parts;
     int e = 0;
     const int M = unit_rows(topk, q.N * q.K, u, &chosen, &e, rows);
     if (M == 0) return;
-    down<T, MTMAX>(act, int64_t(q.N) * q.K * q.F, wd + int64_t(e) * q.F * q.H, q.F, q.H, col0, rows, M, first, step,
+    down<T, MTMAX>(act, int64_t(q.N) * q.K * q.F, wd + int64_t(e) * q.F * q.H, q.F, q.H, col0, rows, M, part, q.dn_parts,
                    ysp + int64_t(part) * q.N * q.K * q.H, red);
   } else {
-    const int part = b + q.sdn_parts, first = part * kWaves + wave, step = q.sdn_parts * kWaves;
+    const int part = b + q.sdn_parts;
     if (threadIdx.x < kTok) rows[threadIdx.x] = threadIdx.x;
     __syncthreads();
-    down<T, MTMAX>(sact, int64_t(q.N) * q.Fs, swd, q.Fs, q.H, col0, rows, q.N, first, step,
+    down<T, MTMAX>(sact, int64_t(q.N) * q.Fs, swd, q.Fs, q.H, col0, rows, q.N, part, q.sdn_parts,
                    sysp + int64_t(part) * q.N * q.H, red);
   }
 }
@@ -885,9 +877,9 @@ __device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __re
     }
     p.template multiply<1>(a, acc);
   }
-  join_waves(acc, red, [&](int, int s, int row, int col, f32x4_t v) {
+  join<false, false>(acc, red, [&](int, int s, int row, int col, const f32x4_t* v) {
     if (row < q.N)
-      *reinterpret_cast<f32x4_t*>(yp + (int64_t(part) * q.N + row) * H + col0 + s * 16 * P::CW + col) = v;
+      *reinterpret_cast<f32x4_t*>(yp + (int64_t(part) * q.N + row) * H + col0 + s * 16 * P::CW + col) = v[0];
   });
 }
 
