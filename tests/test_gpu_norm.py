@@ -58,7 +58,7 @@ def check_backward(h, w, dy, dh, dx, dw, eps=EPS):
     assert ((dw.double() - (g * xh).sum(0)).abs() <= tol + 34 * U * (g * xh).abs().sum(0)).all()
 
 
-SHAPES = [(1, 128), (1, 7168), (2, 512), (3, 640), (5, 1024), (4, 1152), (7, 2048), (9, 2176), (513, 256), (1030, 2048),
+SHAPES = [(1, 128), (1, 7168), (2, 512), (3, 640), (5, 1024), (4, 1152), (7, 2048), (9, 2176), (513, 256), (1030, 2048), (8200, 2048),
           (600, 4096), (5, 8192), (3, 12288), (2, 16384), (2, 16512), (3, 32768)]
 
 
