@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -146,7 +147,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the same handle as torch.cuda.current_stream().cuda_stream, without building the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -351,24 +353,34 @@ def moe_rms_norm_bwd(d, dy, h, weight, rstd, dh, dx, dweight, ws, stream=None):
           _ptr(dweight), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
+_GRAD_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_GRAD_ROW = struct.Struct("PPqii")
+assert _GRAD_ROW.size == ctypes.sizeof(moe_grad)
+
+
 def grad_list(grads, outs=None):
     """The moe_grad array of a list of gradients (and of the outputs of moe_grad_clip)."""
-    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-    rows = []
+    arr = (moe_grad * max(1, len(grads)))()
+    at = 0
     for g, o in zip(grads, grads if outs is None else outs):
-        if g.dtype not in code or o.dtype not in code:
-            raise ValueError(f"unsupported dtype {g.dtype if g.dtype not in code else o.dtype}")
-        if g.numel() != o.numel():
+        gi, oi = _GRAD_CODE.get(g.dtype), _GRAD_CODE.get(o.dtype)
+        if gi is None or oi is None:
+            raise ValueError(f"unsupported dtype {g.dtype if gi is None else o.dtype}")
+        n = g.numel()
+        if n != o.numel():
             raise ValueError("a gradient and its output differ in size")
-        rows.append((_ptr(g), _ptr(o), g.numel(), code[g.dtype], code[o.dtype]))
-    return (moe_grad * max(1, len(rows)))(*rows)
+        gp = _ptr(g)
+        _GRAD_ROW.pack_into(arr, at, gp, gp if o is g else _ptr(o), n, gi, oi)
+        at += _GRAD_ROW.size
+    return arr
 
 
-def moe_grad_norm(grads, norm, ws, stream=None):
-    _call("moe_grad_norm", grad_list(grads), len(grads), _ptr(norm), _ptr(ws), _nbytes(ws), _stream(stream))
+def moe_grad_norm(grads, norm, ws, stream=None, ws_bytes=None):
+    _call("moe_grad_norm", grad_list(grads), len(grads), _ptr(norm), _ptr(ws),
+          _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
 
 
-def moe_grad_clip(grads, outs, max_norm, norm, ws, stream=None):
-    """outs None: in place."""
-    _call("moe_grad_clip", grad_list(grads, outs), len(grads), float(max_norm), _ptr(norm), _ptr(ws), _nbytes(ws),
-          _stream(stream))
+def moe_grad_clip(grads, outs, max_norm, norm, ws, stream=None, ws_bytes=None):
+    """outs None: in place.  ws: a tensor, or an address and ws_bytes."""
+    _call("moe_grad_clip", grad_list(grads, outs), len(grads), float(max_norm), _ptr(norm), _ptr(ws),
+          _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))

@@ -356,10 +356,13 @@ def _cuda_device(device) -> torch.device:
     return torch.device("cuda", torch.cuda.current_device()) if dev.type == "cuda" and dev.index is None else dev
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev: torch.device):
     """The launches of a call go to the tensors' device, whatever device is current."""
     if dev.type != "cuda" or torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(dev)
 
 
@@ -402,11 +405,9 @@ class MoEDecodeRunner:
             raise ValueError(f"{n} tokens, the runner holds {self.max_tokens}")
         if (shared is None) != (self.shared_ffn is None):
             raise ValueError("shared weights must be given exactly when the runner has a shared expert")
-        _expect("x", x, (n, H), dt, dev)
-        _expect("w_r", w_r, (H, E), dt, dev)
-        _expect("w_gate", w_gate, (E, H, F), dt, dev)
-        _expect("w_up", w_up, (E, H, F), dt, dev)
-        _expect("w_down", w_down, (E, F, H), dt, dev)
+        for name, t, shape in (("x", x, (n, H)), ("w_r", w_r, (H, E)), ("w_gate", w_gate, (E, H, F)),
+                               ("w_up", w_up, (E, H, F)), ("w_down", w_down, (E, F, H))):
+            _expect(name, t, shape, dt, dev)
         if bias is not None:
             _expect("bias", bias, (E,), torch.float32, dev)
         sg = su = sd = None
@@ -543,25 +544,25 @@ def moe_rms_norm(x, weight, residual=None, eps: float = 1e-6):
 
 
 def _grad_call(grads, outs):
+    """The checked lists, their device, the result and the address of the scratch behind it."""
     grads = list(grads)
     outs = grads if outs is None else list(outs)
     if len(grads) != len(outs):
         raise ValueError("as many outputs as gradients are needed")
     dev = grads[0].device if grads else _cuda_device("cuda")
-    for t in (*grads, *outs):
+    for t in grads if outs is grads else grads + outs:
         if t.device != dev:
             raise ValueError("all gradients and outputs must be on one device")
-    ws = torch.empty((L.MOE_GRAD_WS_BYTES + 16,), dtype=torch.uint8, device=dev)
-    # workspace and result in one buffer
-    return grads, outs, dev, ws[:L.MOE_GRAD_WS_BYTES], ws[L.MOE_GRAD_WS_BYTES:L.MOE_GRAD_WS_BYTES + 4].view(torch.float32)
+    buf = torch.empty((L.MOE_GRAD_WS_BYTES // 4 + 1,), dtype=torch.float32, device=dev)  # scratch, then norm
+    return grads, outs, dev, buf[L.MOE_GRAD_WS_BYTES // 4:], buf.data_ptr()
 
 
 def moe_grad_norm(grads: Sequence[torch.Tensor]):
     """The 2-norm over all elements of a list of gradients (float32 or bfloat16,
     contiguous), a device tensor [1]; nothing is read back to the host."""
-    grads, _, dev, ws, norm = _grad_call(grads, None)
+    grads, _, dev, norm, ws = _grad_call(grads, None)
     with _on(dev):
-        L.moe_grad_norm(grads, norm, ws)
+        L.moe_grad_norm(grads, norm, ws, ws_bytes=L.MOE_GRAD_WS_BYTES)
     return norm
 
 
@@ -571,7 +572,7 @@ def moe_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     or bfloat16: an optimiser's gradients from float32 accumulators).  Returns
     (outputs, norm), norm a device tensor [1]; nothing is read back to the host.
     An output may be its own gradient; any other overlap is refused."""
-    grads, outs, dev, ws, norm = _grad_call(grads, out)
+    grads, outs, dev, norm, ws = _grad_call(grads, out)
     with _on(dev):
-        L.moe_grad_clip(grads, outs, max_norm, norm, ws)
+        L.moe_grad_clip(grads, outs, max_norm, norm, ws, ws_bytes=L.MOE_GRAD_WS_BYTES)
     return outs, norm
