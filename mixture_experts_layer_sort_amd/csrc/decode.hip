@@ -299,12 +299,19 @@ __device__ __forceinline__ int expert_slots(Chosen* c, int NK, int e, int* rows)
 }
 
 // The rows of unit u: the u-th chosen expert's slots; their number, 0 when there
-// is no such unit.
-__device__ __forceinline__ int unit_rows(const int32_t* __restrict__ topk, int NK, int u, Chosen* c, int* e,
+// is no such unit.  One token's experts are its slots as they stand.
+__device__ __forceinline__ int unit_rows(const int32_t* __restrict__ topk, int N, int K, int u, Chosen* c, int* e,
                                          int* rows) {
-  if (u >= chosen_experts(topk, NK, c)) return 0;
+  if (N == 1) {
+    if (u >= K) return 0;
+    *e = topk[u];
+    if (threadIdx.x == 0) rows[0] = u;
+    __syncthreads();
+    return 1;
+  }
+  if (u >= chosen_experts(topk, N * K, c)) return 0;
   *e = c->expert[u];
-  return expert_slots(c, NK, *e, rows);
+  return expert_slots(c, N * K, *e, rows);
 }
 
 // --------------------------------------------------------------- the panels
@@ -666,7 +673,7 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* 
     b /= chunks;
     const int mat = b % 2, part = b / 2 % q.gu_parts;
     int e = 0;
-    const int M = unit_rows(topk, q.N * q.K, b / 2 / q.gu_parts, &chosen, &e, rows);
+    const int M = unit_rows(topk, q.N, q.K, b / 2 / q.gu_parts, &chosen, &e, rows);
     if (M == 0) return;
     gate_up<T, MTMAX, false>(x, (mat ? wu : wg) + int64_t(e) * q.H * q.F, nullptr, q.H, q.F,
                              int64_t(chunk) * kCols<T>, rows, M, q.K, part, q.gu_parts,
@@ -704,7 +711,7 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up_act(XRows<T> x, const
   int b = int(blockIdx.x) - shared;
   if (b >= 0) {
     int e = 0;
-    const int M = unit_rows(topk, q.N * q.K, b / chunks, &chosen, &e, rows);
+    const int M = unit_rows(topk, q.N, q.K, b / chunks, &chosen, &e, rows);
     if (M == 0) return;
     const int64_t at = int64_t(e) * q.H * q.F;
     gate_up<T, MTMAX, true>(x, wg + at, wu + at, q.H, q.F, int64_t(b % chunks) * kCols<T>, rows, M, q.K, 0, 1,
@@ -809,7 +816,7 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down(const T* __restrict__ ac
   if (b >= 0) {
     const int part = b % q.dn_parts, u = b / q.dn_parts;
     int e = 0;
-    const int M = unit_rows(topk, q.N * q.K, u, &chosen, &e, rows);
+    const int M = unit_rows(topk, q.N, q.K, u, &chosen, &e, rows);
     if (M == 0) return;
     down<T, MTMAX>(act, int64_t(q.N) * q.K * q.F, wd + int64_t(e) * q.F * q.H, q.F, q.H, col0, rows, M, part, q.dn_parts,
                    ysp + int64_t(part) * q.N * q.K * q.H, red);
@@ -902,26 +909,34 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down_all(Rows<T, FUSED> in, c
     ids[t] = topk[t];
     gate[t] = gates[t];
   }
-  for (int i = t; i < SL * 16; i += kNT) slot[i / 16][i % 16] = -1;
+  for (int i = t; i < NK * 16; i += kNT) slot[i / 16][i % 16] = -1;
   __syncthreads();
-  // a slot's unit: how many experts' first slots come before its expert's first slot
-  int first = t;
-  if (t < NK)
-    for (first = 0; ids[first] != ids[t]; ++first) {}
-  const bool head = t < NK && first == t;
-  const uint64_t heads = __ballot(head);
-  if (lane_id() == 0) counts[t / kWave] = __popcll(heads);
-  __syncthreads();
-  int active = 0;
+  int active = NK;
+  if (q.N == 1) {  // its slots are its experts
+    if (t < NK) {
+      expert[t] = ids[t];
+      slot[t][0] = int16_t(t);
+    }
+  } else {
+    // a slot's unit: how many experts' first slots come before its expert's first slot
+    int first = t;
+    if (t < NK)
+      for (first = 0; ids[first] != ids[t]; ++first) {}
+    const bool head = t < NK && first == t;
+    const uint64_t heads = __ballot(head);
+    if (lane_id() == 0) counts[t / kWave] = __popcll(heads);
+    __syncthreads();
+    active = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w == t / kWave && head) unit[t] = active + __popcll(heads & ((uint64_t(1) << lane_id()) - 1));
-    active += counts[w];
-  }
-  __syncthreads();
-  if (t < NK) {
-    expert[unit[first]] = ids[t];  // the same value from all of the expert's slots
-    slot[unit[first]][t / q.K] = int16_t(t);
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == t / kWave && head) unit[t] = active + __popcll(heads & ((uint64_t(1) << lane_id()) - 1));
+      active += counts[w];
+    }
+    __syncthreads();
+    if (t < NK) {
+      expert[unit[first]] = ids[t];  // the same value from all of the expert's slots
+      slot[unit[first]][t / q.K] = int16_t(t);
+    }
   }
   __syncthreads();
   const int chunks = (q.H + kCols<T> - 1) / kCols<T>;
@@ -1051,7 +1066,7 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
       q.dn_parts *= 2;
     q.sdn_parts = int(Fs == 0 ? 0 : std::min(Fs / (32 * kWaves), q.dn_parts * ((Fs + d.F - 1) / d.F)));
   }
-  p.last = p.few && chunks * q.dn_parts <= 64;
+  p.last = d.N == 1 && chunks * q.dn_parts <= 64;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;

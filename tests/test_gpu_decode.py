@@ -120,6 +120,15 @@ SHAPES = [
     (64, 128, 128, 256, 8, 0, False),
     (5, 2048, 128, 6, 2, 0, False),
     (4, 128, 2048, 6, 2, 0, False),
+    # many strips of columns and many rows each: gate and up in one workgroup
+    (16, 128, 6528, 8, 8, 128, False),
+    (40, 256, 6528, 8, 4, 384, True),     # a last single segment, two row tiles
+    (64, 128, 6656, 8, 8, 0, False),      # more rows than two row tiles
+    (64, 128, 6528, 8, 8, 128, False),
+    (24, 1152, 256, 4, 3, 1408, False),   # a shared expert much longer than the routed ones
+    (2, 640, 384, 64, 8, 256, True),      # the workgroups route by themselves, logits from the first kernel
+    (2, 256, 128, 16, 4, 0, True),        # ... and the logits too
+    (1, 128, 384, 200, 7, 0, True),
 ]
 
 
@@ -129,6 +138,26 @@ def test_decode_matches_float64(shape, dtype):
     N, H, F, E, K, Fs, bias = shape
     t = _inputs(N, H, F, E, K, dtype, Fs, bias, seed=N + E)
     r = _runner(N, t, K, Fs)
+    y = _forward(r, t)
+    torch.cuda.synchronize()
+    check(t, K, r, y)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sizes(seed):
+    """Sizes spread over the whole range of tokens, experts and types."""
+    import random
+    rng = random.Random(1000 + seed)
+    N = rng.choice([1, 2, 3, rng.randint(4, 16), rng.randint(17, 32), rng.randint(33, 64)])
+    E = rng.choice([1, 2, rng.randint(3, 16), rng.randint(17, 64), rng.randint(65, 256)])
+    K, dtype = rng.randint(1, min(8, E)), rng.choice([torch.bfloat16, torch.float32])
+    H = 128 * rng.randint(1, 12)
+    F = 128 * rng.randint(1, max(1, min(24, (1 << 26) // (E * H * 128))))
+    Fs, bias = rng.choice([0, 128 * rng.randint(1, 12)]), rng.random() < 0.5
+    print("[decode]", N, H, F, E, K, Fs, bias, dtype, flush=True)
+    t = _inputs(N, H, F, E, K, dtype, Fs, bias, seed=seed)
+    r = _runner(N, t, K, Fs)
+    r.ws.fill_(255)
     y = _forward(r, t)
     torch.cuda.synchronize()
     check(t, K, r, y)
