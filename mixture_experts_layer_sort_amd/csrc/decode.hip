@@ -381,6 +381,19 @@ template <int S> struct Panel<bf16_t, S> {
         for (int m = 0; m < MT; ++m) fma(a[m], b, acc[m][s][i]);
       }
   }
+  // The same for one row tile, rows 4g + r of the sums changing only where
+  // keep[r]: a zero row times an infinite or NaN weight is not zero.
+  __device__ __forceinline__ void multiply_kept(const A2& a, const bool (&keep)[4], f32x4_t (&acc)[S][CW]) const {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < CW; ++i) {
+        f32x4_t t = {0.f, 0.f, 0.f, 0.f};
+        fma(a, column(s, i), t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[s][i][r] += keep[r] ? t[r] : 0.f;
+      }
+  }
 };
 
 template <int S> struct Panel<float, S> {
@@ -421,6 +434,23 @@ template <int S> struct Panel<float, S> {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
             acc[m][s][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m].a[j], w[s][j][i], acc[m][s][i], 0, 0, 0);
+  }
+  __device__ __forceinline__ void multiply_kept(const A2& a, const bool (&keep)[4], f32x4_t (&acc)[S][CW]) const {
+    f32x4_t t[S][CW];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int i = 0; i < CW; ++i)
+          t[s][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[j], w[s][j][i], j == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : t[s][i],
+                                                         0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < CW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[s][i][r] += keep[r] ? t[s][i][r] : 0.f;
   }
 };
 
@@ -882,7 +912,14 @@ __device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __re
       if (row >= 0) a[0].load((sh ? in.sact : in.act) + at, sh ? splane : plane);
       p.load(pw, H);
     }
-    p.template multiply<1>(a, acc);
+    if (q.N == 1 || sh) {  // every row that counts has this expert
+      p.template multiply<1>(a, acc);
+    } else {
+      bool keep[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) keep[r] = slot[u][4 * g + r] >= 0;
+      p.multiply_kept(a[0], keep, acc[0]);
+    }
   }
   join<false, false>(acc, red, [&](int, int s, int row, int col, const f32x4_t* v) {
     if (row < q.N)
@@ -1017,18 +1054,23 @@ struct Plan {
 
 constexpr int64_t kCUs = 256;
 
-// Workgroups that share a strip of `panels` panels when there are about
-// `strips` strips.  Every CU takes its workgroups' panels at the same rate, so the
-// fullest CU sets the time: ceil(strips * p / CUs) / p strips' worth; three
-// workgroups fit a CU at once, and a fourth would wait for their end.  0.6 us a
-// panel for a CU, about 1.2 us of latency for each of a wave's first panels.
-int cut(double strips, int64_t panels) {
+// Workgroups (max_parts at most) that share a strip of `panels` panels when there
+// are about `strips` strips.  A CU reads its workgroups' panels at about 31 bytes a
+// nanosecond (0.5 us for the 16 KiB of a panel), and the CU with most of them sets
+// the time as long as all are resident together (`fit` to a CU).  Besides, 1.2 us
+// of latency for each of a wave's first panels; and nothing covers a workgroup's
+// start and end when it is alone on its CU (2%).  Strips of other widths would
+// even the CUs out better, but a row segment that is not 256 bytes, aligned, reads a
+// third slower.
+int cut(double strips, int64_t panels, int max_parts, double fit) {
   int best = 1;
   double least = 0.0;
-  for (int p = 1; p <= 4 && kWaves * p <= panels && (p == 1 || strips * p <= 3.0 * kCUs); ++p) {
-    const double t = std::ceil(strips * p / double(kCUs)) / p * 0.6 * double(panels) +
-                     1.2 * std::min(4.0, double(panels) / (kWaves * p));
-    if (p == 1 || t < least) {
+  for (int p = 1; p <= max_parts && kWaves * p <= panels; ++p) {
+    const double per_cu = strips * p / double(kCUs);
+    if (p > 1 && per_cu > fit) break;
+    const double turns = std::ceil(per_cu) * (per_cu <= 1.0 ? 1.02 : 1.0);
+    const double t = turns * 0.5 * double(panels) / p + 1.2 * std::min(4.0, double(panels) / (kWaves * p));
+    if (p == 1 || t < 0.99 * least) {
       best = p;
       least = t;
     }
@@ -1050,7 +1092,7 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   const double used = double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N)));
   p.few = d.N <= 16;
   p.joint = q.units * fchunks + schunks >= 200 && NK >= 8 * q.units;
-  q.gu_parts = p.joint ? 1 : cut(2.0 * (used * double(fchunks) + double(schunks)), d.H / 32);
+  q.gu_parts = p.joint ? 1 : cut(2.0 * (used * double(fchunks) + double(schunks)), d.H / 32, 4, p.few ? 3.0 : 2.0);
   p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
   p.route = !p.joint && d.N <= kRouteTok;
   p.logit_parts = int((d.H + kLogitRows - 1) / kLogitRows);
@@ -1061,9 +1103,7 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
     q.dn_parts = int(std::max<int64_t>(1, std::min({int64_t(panels / kWaves), 2 * kCUs / chunks, want})));
   } else {
     // two workgroups fit a CU (row tiles take the registers); a longer shared strip is cut more often
-    q.dn_parts = 1;
-    while (used * double(chunks) * 2 * q.dn_parts <= 2.2 * kCUs && d.F / 32 >= int64_t(2) * q.dn_parts * kWaves)
-      q.dn_parts *= 2;
+    q.dn_parts = cut(used * double(chunks), d.F / 32, 16, 2.0);
     q.sdn_parts = int(Fs == 0 ? 0 : std::min(Fs / (32 * kWaves), q.dn_parts * ((Fs + d.F - 1) / d.F)));
   }
   p.last = d.N == 1 && chunks * q.dn_parts <= 64;

@@ -243,6 +243,28 @@ def test_gates_of_zero_add_nothing_and_weights_stay_unread_elsewhere():
     assert torch.equal(_forward(r, t), good)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [3, 12, 24])
+def test_non_finite_weights_reach_only_the_tokens_that_chose_them(N, dtype):
+    """An expert with infinite and NaN weights: tokens routed elsewhere are as without it."""
+    t = _inputs(N, 256, 256, 8, 2, dtype, Fs=128, seed=13)
+    t["bias"] = torch.zeros(8, device="cuda")
+    t["x"][:] *= 0.5
+    r = _runner(N, t, 2, 128)
+    good = _forward(r, t).clone()
+    bad = int(r.topk[0, 0])
+    hit = (r.topk == bad).any(1)
+    assert hit.any() and not hit.all()
+    for w, v in (("w_gate", float("nan")), ("w_up", float("inf")), ("w_down", float("inf"))):
+        for value in (v, float("nan")):
+            keep = t[w][bad].clone()
+            t[w][bad, 3, 7] = value
+            y = _forward(r, t)
+            assert torch.equal(y[~hit], good[~hit]), w
+            assert not torch.isfinite(y[hit]).all(), w
+            t[w][bad] = keep
+
+
 def test_same_bits_with_a_dirty_workspace_another_stream_and_a_graph():
     t = _inputs(19, 384, 512, 32, 4, torch.bfloat16, Fs=256, bias=True, seed=10)
     r = _runner(32, t, 4, 256)
