@@ -19,6 +19,9 @@
 //    one operand after packing row pairs (4 byte permutes for 8 values).
 //    float32 needs no packing: row j of the eight is one operand of a 16x16x4
 //    instruction.
+//  - All of a panel's loads are issued before its first product: left to itself
+//    the compiler spreads a float32 panel's loads over its products to save
+//    registers (64 tokens of a 16-expert float32 layer: 135 us so, 92 in order).
 //  - The other operand holds up to 16 token rows; rows past the last repeat
 //    row 0 and their results are dropped.
 //  - The waves of a workgroup split the contraction; their float32 sums meet
@@ -205,7 +208,6 @@ __device__ __forceinline__ void route_here(const Route<T>& r, int N, int H, int 
     const T* px = r.x + int64_t(min(c, N - 1)) * H;
     for (int e0 = 0; e0 < E; e0 += 16) {
       f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 2
       for (int h = wave * 32; h < H; h += kWaves * 32) logit_panel(px, r.w_r, h, E, min(e0 + c, E - 1), acc);
       __syncthreads();
       park_logits(acc, red + wave * 256);
@@ -621,6 +623,7 @@ __device__ __forceinline__ void gate_up_rows(const XRows<T>& x, const T* wg, con
 #pragma unroll
       for (int m = 0; m < MT; ++m) a[m].load(px[m] + int64_t(i) * x.panel_step);
       p.load(pw + int64_t(i) * 32 * ld, ld);
+      __builtin_amdgcn_sched_barrier(0);
       p.template multiply<MT>(a, acc);
     }
   join<JOINT, HALVES>(acc, red, [&](int m, int s, int row, int col, const f32x4_t* v) {
@@ -803,6 +806,7 @@ __device__ __forceinline__ void down_rows(const T* __restrict__ act, int64_t pla
 #pragma unroll
       for (int m = 0; m < MT; ++m) a[m].load(pa[m] + int64_t(i) * 32 * (plane / F), plane);
       p.load(pw + int64_t(i) * 32 * H, H);
+      __builtin_amdgcn_sched_barrier(0);
       p.template multiply<MT>(a, acc);
     }
   join<false, HALVES>(acc, red, [&](int m, int s, int row, int col, const f32x4_t* v) {
@@ -904,6 +908,7 @@ __device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __re
       Act act;
       if (row >= 0) act.load((sh ? in.sgu : in.gu) + at, sh ? splane : plane, q.gu_parts);
       p.load(pw, H);
+      __builtin_amdgcn_sched_barrier(0);
       if (row >= 0) {
         act.finish(sh ? 1.f : gate[row], v);
         a[0].set(v);
@@ -911,6 +916,7 @@ __device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __re
     } else {
       if (row >= 0) a[0].load((sh ? in.sact : in.act) + at, sh ? splane : plane);
       p.load(pw, H);
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (q.N == 1 || sh) {  // every row that counts has this expert
       p.template multiply<1>(a, acc);

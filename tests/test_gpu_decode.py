@@ -244,6 +244,34 @@ def test_gates_of_zero_add_nothing_and_weights_stay_unread_elsewhere():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_every_number_of_tokens_on_one_runner(dtype):
+    t = _inputs(64, 256, 384, 12, 3, dtype, Fs=128, bias=True, seed=14)
+    r = _runner(64, t, 3, 128)
+    x = t["x"]
+    for n in list(range(1, 65)) + [1, 40, 2]:
+        t["x"] = x[:n].contiguous()
+        check(t, 3, r, _forward(r, t))
+
+
+def test_two_runners_on_two_streams_at_once():
+    jobs = []
+    for i, (N, E) in enumerate(((1, 16), (12, 16), (50, 8))):
+        t = _inputs(N, 512, 1024, E, 2, torch.bfloat16, seed=20 + i)
+        r = _runner(N, t, 2)
+        jobs.append((t, r, _forward(r, t).clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for t, r, _, s in jobs:
+            r._y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for t, r, _, s in jobs:
+            _forward(r, t, stream=s)
+        torch.cuda.synchronize()
+        for _, r, want, _ in jobs:
+            assert torch.equal(r.y, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("N", [3, 12, 24])
 def test_non_finite_weights_reach_only_the_tokens_that_chose_them(N, dtype):
     """An expert with infinite and NaN weights: tokens routed elsewhere are as without it."""
