@@ -518,8 +518,9 @@ int moe_rms_norm(const moe_dims* d, const void* x, const void* residual, const v
  *   dy, h [N,H] act (h: x when there was no residual); rstd [N] f32 from
  *   moe_rms_norm; dh [N,H] act, the gradient that reaches h beside y (the
  *   residual stream), or NULL; dx [N,H] out, may be dy or dh itself;
- *   dweight [H] f32 out.  ws: MOE_ENTRY_RMS_NORM_BWD (a row of H float32
- *   partial sums per workgroup; any H up to MOE_NORM_MAX_H). */
+ *   dweight [H] f32 out, overlapping no other argument.  ws:
+ *   MOE_ENTRY_RMS_NORM_BWD (a row of H float32 partial sums per workgroup; any
+ *   H up to MOE_NORM_MAX_H). */
 int moe_rms_norm_bwd(const moe_dims* d, const void* dy, const void* h, const void* weight, const float* rstd,
                      const void* dh, void* dx, float* dweight, void* ws, size_t ws_bytes, hipStream_t stream);
 

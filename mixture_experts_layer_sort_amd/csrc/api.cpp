@@ -522,6 +522,10 @@ int moe_rms_norm_bwd(const moe_dims* d, const void* dy, const void* h, const voi
   if ((dx != dy && overlap(dx, b, dy, b)) || (dh != nullptr && dx != dh && overlap(dx, b, dh, b)) ||
       overlap(dx, b, h, b) || overlap(dx, b, weight, wb) || overlap(dx, b, rstd, rb))
     return MOE_EINVAL;
+  const size_t db = size_t(D.H) * 4;
+  if (overlap(dweight, db, dx, b) || overlap(dweight, db, dy, b) || overlap(dweight, db, h, b) ||
+      overlap(dweight, db, weight, wb) || overlap(dweight, db, rstd, rb) || (dh != nullptr && overlap(dweight, db, dh, b)))
+    return MOE_EINVAL;
   if (D.N == 0) return MOE_OK;
   const size_t need = moe_launch::rms_norm_bwd_ws(D);
   if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;

@@ -460,6 +460,7 @@ template <int S> struct Panel<float, S> {
 // Columns of one workgroup: two segments.
 template <typename T>
 constexpr int kCols = 2 * 16 * Panel<T, 1>::CW;
+constexpr int kAlign = 128;  // every dimension but N, E and K is a multiple of it
 
 template <int MT, int S, int CW>
 __device__ __forceinline__ void clear(f32x4_t (&acc)[MT][S][CW]) {
@@ -654,7 +655,7 @@ template <typename T, int MTMAX, bool JOINT>
 __device__ __forceinline__ void gate_up(const XRows<T>& x, const T* wg, const T* wu, int H, int64_t ld, int64_t col0,
                                         const int* rows, int M, int div, int part, int parts,
                                         const GuOut<T, JOINT>& out, float* red) {
-  const bool wide = col0 + kCols<T> <= ld;  // else a last single segment
+  const bool wide = kCols<T> == kAlign || col0 + kCols<T> <= ld;  // else a last single segment
   if constexpr (MTMAX > 2)
     if (M > 32) return gate_up_rows<T, 1, 4, JOINT, true>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
   if constexpr (MTMAX > 1)
@@ -824,7 +825,7 @@ template <typename T, int MTMAX>
 __device__ __forceinline__ void down(const T* __restrict__ act, int64_t plane, const T* wd, int F, int64_t H,
                                      int64_t col0, const int* rows, int M, int part, int parts, float* out,
                                      float* red) {
-  const bool wide = col0 + kCols<T> <= H;
+  const bool wide = kCols<T> == kAlign || col0 + kCols<T> <= H;
   if constexpr (MTMAX > 2)
     if (M > 32) return down_rows<T, 1, 4, true>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
   if (M > 16)
@@ -989,7 +990,7 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down_all(Rows<T, FUSED> in, c
   const int chunks = (q.H + kCols<T> - 1) / kCols<T>;
   const int64_t col0 = int64_t(blockIdx.x % chunks) * kCols<T>;
   const int part = blockIdx.x / chunks;
-  if (col0 + kCols<T> <= q.H)
+  if (kCols<T> == kAlign || col0 + kCols<T> <= q.H)
     down_all<T, 2, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
   else
     down_all<T, 1, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
@@ -1115,9 +1116,12 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
     const int64_t want = std::max(kCUs / chunks, int64_t(panels / (4 * kWaves)));
     q.dn_parts = int(std::max<int64_t>(1, std::min({int64_t(panels / kWaves), 2 * kCUs / chunks, want})));
   } else {
-    // two workgroups fit a CU (row tiles take the registers); a longer shared strip is cut more often
+    // Two workgroups fit a CU (row tiles take the registers).  A longer shared strip is cut
+    // more often, but all of them into no more pieces than CUs (64 tokens, H 2048, F 128,
+    // Fs 32768: 127 us so, 177 without the bound).
     q.dn_parts = cut(used * double(chunks), d.F / 32, 16, 2.0);
-    q.sdn_parts = int(Fs == 0 ? 0 : std::min(Fs / (32 * kWaves), q.dn_parts * ((Fs + d.F - 1) / d.F)));
+    const int64_t longer = q.dn_parts * ((Fs + d.F - 1) / d.F), most = std::max<int64_t>(kCUs / chunks, 1);
+    q.sdn_parts = int(std::min({Fs / (32 * kWaves), longer, most}));
   }
   p.last = d.N == 1 && chunks * q.dn_parts <= 64;
   size_t at = 0;

@@ -124,6 +124,22 @@ def test_norm_backward_refusals(lib):
     assert norm_bwd(D(N=0), ws=None, nb=0, dh=None) == L.MOE_OK
 
 
+def test_norm_backward_refuses_a_dweight_on_other_arguments(lib):
+    for other in (1, 2, 3, 4, 5, 6):
+        assert norm_bwd(D(), dw=at(other)) == L.MOE_EINVAL, other
+    assert norm_bwd(D(), dw=at(1) - 128 * 4 + 16) == L.MOE_EINVAL      # its end on dy
+
+
+def test_decode_workspace_of_a_wide_shared_expert(lib):
+    """Partial sums of the shared expert's down product: at most a piece per CU (256) over the
+    strips of 256 columns, whatever the ratio of the experts' lengths."""
+    N, H, F, Fs = 64, 8192, 128, 65536
+    d, ds = D(N=N, H=H, F=F, E=8, K=2), D(N=N, H=H, F=Fs, E=1, K=1)
+    acts = 2 * 4 * N * Fs * 4 + N * Fs * 4          # sums of gate and up in four pieces at most, activations
+    parts = 256 // (H // 256) * N * H * 4
+    assert L.moe_decode_workspace_bytes(d, ds) <= L.moe_decode_workspace_bytes(d) + acts + parts + 4096
+
+
 def clip(rows, max_norm=1.0, norm=at(100), ws=at(101), nb=L.MOE_GRAD_WS_BYTES, count=None, entry="moe_grad_clip"):
     arr = (L.moe_grad * max(1, len(rows)))(*rows)
     count = len(rows) if count is None else count

@@ -163,6 +163,14 @@ def test_random_sizes(seed):
     check(t, K, r, y)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,H,Fs", [(17, 8192, 8320), (64, 256, 16384), (40, 4224, 2176), (12, 512, 8192)])
+def test_shared_expert_much_longer_than_the_routed_ones(N, H, Fs, dtype):
+    t = _inputs(N, H, 128, 3, 2, dtype, Fs, seed=N)
+    r = _runner(N, t, 2, Fs)
+    check(t, 2, r, _forward(r, t))
+
+
 @pytest.mark.parametrize("N,E,K", [(64, 8, 2), (40, 64, 6), (64, 256, 1)])
 def test_skewed_routing(N, E, K):
     """A bias that sends every token to the same experts (rows of all others empty)."""

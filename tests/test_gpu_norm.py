@@ -187,6 +187,35 @@ def _dw(h, dy):
     return (dy.double() * hd * (hd.square().mean(1, keepdim=True) + EPS).rsqrt()).sum(0)
 
 
+def test_autograd_function_captured_with_its_backward():
+    from mixture_experts_layer_sort_amd import moe_rms_norm
+    x, res, w, dy, dh = _make(40, 512, torch.bfloat16, seed=11)
+    leaves = [t.clone().requires_grad_() for t in (x, res, w)]
+
+    def step():
+        y, h = moe_rms_norm(leaves[0], leaves[2], residual=leaves[1], eps=EPS)
+        return (y.detach(), *torch.autograd.grad([y, h], leaves, [dy, dh]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for i in range(4):
+        with torch.no_grad():
+            leaves[0].copy_(x * (i + 1))
+        want = [t.clone() for t in step()]
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
 def test_gradient_against_differences():
     """Central differences in float64 of the plain formula at the kernel's own h,
     along random directions: f(h + d) - f(h - d) over 2 d, truncation of order d^2."""
