@@ -125,86 +125,92 @@ __global__ __launch_bounds__(kLogitWaves * kWave) void k_decode_logits(const T* 
   }
 }
 
-// Scratch of token_topk.
+// Scratch and results of rank_pairs.
+constexpr int kPairs = 256;  // (token, expert): one a thread
 struct TopK {
-  double l[MOE_MAX_EXPERTS], sel[MOE_MAX_TOPK];
+  double l[kPairs], sel[16 * MOE_MAX_TOPK];
+  int32_t ids[16 * MOE_MAX_TOPK];
+  float gates[16 * MOE_MAX_TOPK];
 };
 
-// Logit of expert e of token n from S partial sums.
-__device__ __forceinline__ double sum_parts(const double* __restrict__ part, int n, int e, int N, int E, int S) {
+// This thread's pair of the tokens from n0 on: its logit from S partial sums.
+__device__ __forceinline__ double sum_parts(const double* __restrict__ part, int n0, int N, int E, int S) {
   double v = 0.0;
   for (int s0 = 0; s0 < S; s0 += 16) {
     double t[16];  // loads of one round trip
 #pragma unroll
-    for (int s = 0; s < 16; ++s) t[s] = s0 + s < S ? part[(int64_t(s0 + s) * N + n) * E + e] : 0.0;
+    for (int s = 0; s < 16; ++s) t[s] = s0 + s < S ? part[(int64_t(s0 + s) * N + n0) * E + threadIdx.x] : 0.0;
 #pragma unroll
     for (int s = 0; s < 16; ++s) v += t[s];
   }
   return v;
 }
 
-// Top-K and gates of one token by 256 threads, thread e < E with expert e's
-// logit v: its place is the number of experts before it in the order (logit
-// desc, id asc); NaN logits come last.  Writes ids and gates of the K places.
-__device__ __forceinline__ void token_topk(double v, const float* __restrict__ bias, int E, int K, TopK* s,
-                                           int32_t* ids, float* gates) {
-  const int e = threadIdx.x;
-  if (e < E) {
+// Top-K and gates of `count` tokens (at most 16, count * E <= kPairs) by 256
+// threads, thread n*E + e with that pair's logit v: the expert's place is the
+// number of experts before it in the order (logit desc, id asc); NaN logits come
+// last.  ids and gates [count][K] to *out, thread p's own p behind it, the others'
+// after a barrier.
+__device__ __forceinline__ void rank_pairs(double v, const float* __restrict__ bias, int count, int E, int K,
+                                           TopK* out) {
+  const int p = threadIdx.x, n = p / E, e = p % E;
+  const bool live = n < count;
+  if (live) {
     if (bias != nullptr) v += double(bias[e]);
     if (v != v) v = -INFINITY;
-    s->l[e] = v;
+    out->l[p] = v;
   }
   __syncthreads();
-  if (e < E) {
+  if (live) {
+    const double* l = out->l + n * E;
     int before = 0;
 #pragma unroll 8
-    for (int i = 0; i < E; ++i) before += s->l[i] > v || (s->l[i] == v && i < e);
+    for (int i = 0; i < E; ++i) before += l[i] > v || (l[i] == v && i < e);
     if (before < K) {
-      ids[before] = e;
-      s->sel[before] = v;
+      out->ids[n * K + before] = e;
+      out->sel[n * K + before] = v;
     }
   }
   __syncthreads();
-  if (e < K) {
+  if (p < count * K) {
+    const double* sel = out->sel + p / K * K;
     float sum = 0.f, mine = 0.f;
     for (int k = 0; k < K; ++k) {
-      const float z = expf(float(s->sel[k] - s->sel[0]));
+      const float z = expf(float(sel[k] - sel[0]));
       sum += z;
-      if (k == e) mine = z;
+      if (k == p % K) mine = z;
     }
-    gates[e] = mine / sum;
+    out->gates[p] = mine / sum;
   }
 }
 
-__global__ __launch_bounds__(256) void k_decode_topk(const double* __restrict__ part, const float* __restrict__ bias,
-                                                     int32_t* __restrict__ topk, float* __restrict__ gates, int N,
-                                                     int E, int K, int S) {
+// A token a workgroup.
+__global__ __launch_bounds__(kPairs) void k_decode_topk(const double* __restrict__ part,
+                                                        const float* __restrict__ bias, int32_t* __restrict__ topk,
+                                                        float* __restrict__ gates, int N, int E, int K, int S) {
   __shared__ TopK s;
-  const int n = blockIdx.x;
-  const double v = int(threadIdx.x) < E ? sum_parts(part, n, threadIdx.x, N, E, S) : 0.0;
-  token_topk(v, bias, E, K, &s, topk + n * K, gates + n * K);
+  const int n = blockIdx.x, t = threadIdx.x;
+  rank_pairs(t < E ? sum_parts(part, n, N, E, S) : 0.0, bias, 1, E, K, &s);
+  if (t < K) {
+    topk[n * K + t] = s.ids[t];
+    gates[n * K + t] = s.gates[t];
+  }
 }
 
-// Routing of one or two tokens by every workgroup of gate/up for itself (from three
-// on a launch of its own is cheaper).
-constexpr int kRouteTok = 2;
+// Routing of all tokens by every workgroup of gate/up for itself.
 template <typename T> struct Route {
   const T *x, *w_r;
   const double* part;  // null: the workgroup forms the logits as well
   const float* bias;
   int S;
 };
-struct Routed {
-  TopK top;
-  int32_t ids[kRouteTok * MOE_MAX_TOPK];
-  float gates[kRouteTok * MOE_MAX_TOPK];
-  double logits[kRouteTok][MOE_MAX_EXPERTS];
-};
 
 // red: 2 KiB per wave.
 template <typename T>
-__device__ __forceinline__ void route_here(const Route<T>& r, int N, int H, int E, int K, Routed* out, double* red) {
+__device__ __forceinline__ void route_here(const Route<T>& r, int N, int H, int E, int K, TopK* out, double* red) {
+  static_assert(kNT == kPairs, "a thread per pair");
   const int t = threadIdx.x, wave = t / kWave, c = lane_id() % 16;
+  double v = 0.0;
   if (r.part == nullptr) {
     const T* px = r.x + int64_t(min(c, N - 1)) * H;
     for (int e0 = 0; e0 < E; e0 += 16) {
@@ -213,21 +219,17 @@ __device__ __forceinline__ void route_here(const Route<T>& r, int N, int H, int 
       __syncthreads();
       park_logits(acc, red + wave * 256);
       __syncthreads();
-      if (t < 16 * N && e0 + t % 16 < E) {
-        double v = 0.0;
+      const int n = t / E, e = t % E - e0;
+      if (n < N && e >= 0 && e < 16) {
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) v += red[i * 256 + t];
-        out->logits[t / 16][e0 + t % 16] = v;
+        for (int i = 0; i < kWaves; ++i) v += red[i * 256 + n * 16 + e];
       }
     }
-    __syncthreads();
+  } else if (t < N * E) {
+    v = sum_parts(r.part, 0, N, E, r.S);
   }
-  for (int n = 0; n < N; ++n) {
-    double v = 0.0;
-    if (t < E) v = r.part == nullptr ? out->logits[n][t] : sum_parts(r.part, n, t, N, E, r.S);
-    token_topk(v, r.bias, E, K, &out->top, out->ids + n * K, out->gates + n * K);
-    __syncthreads();
-  }
+  rank_pairs(v, r.bias, N, E, K, out);
+  __syncthreads();
 }
 
 // ------------------------------------------------------- rows of an expert
@@ -695,7 +697,7 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* 
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
   if constexpr (ROUTE) {
-    __shared__ Routed routed;
+    __shared__ TopK routed;
     route_here(route, q.N, q.H, q.E, q.K, &routed, reinterpret_cast<double*>(red));
     topk = routed.ids;
     if (blockIdx.x == 0 && int(threadIdx.x) < q.N * q.K) {
@@ -1105,11 +1107,15 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   p.joint = q.units * fchunks + schunks >= 200 && NK >= 8 * q.units;
   q.gu_parts = p.joint ? 1 : cut(2.0 * (used * double(fchunks) + double(schunks)), d.H / 32, 4, p.few ? 3.0 : 2.0);
   p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
-  // The logits too are each workgroup's own where the router is a few panels (measured at
-  // one token: 17.5 us against 19.8 with the logits' launch at H 512 and 8 experts, 36.0
-  // against 32.7 at H 2048 and 16 experts; at the bound, 32 panels, both take 24 us).
-  const bool small_router = (d.E + 15) / 16 * (d.H / 32) <= 8 * kWaves;
-  p.route = !p.joint && d.N <= kRouteTok;
+  // Each workgroup of gate/up ranks the pairs (token, expert) for itself while there is one a
+  // thread at most: 1 to 4 us less than with a launch for it (4 tokens, 16 experts: 35.9
+  // against 37.5; 4 tokens, 64 experts: 88 against 90), but with two pairs a thread 123 against
+  // 122 (8 tokens, 64 experts), with four 164 against 160.
+  p.route = p.few && !p.joint && d.N * d.E <= kPairs;
+  // The logits too where the router is a few panels (17.5 us against 19.8 with the logits'
+  // launch at one token, H 512 and 8 experts, 23.4 against 25.1 at three; 37.6 against 35.9 at
+  // four tokens, H 1024 and 16 experts).
+  const bool small_router = (d.E + 15) / 16 * (d.H / 32) <= 4 * kWaves;
   p.logit_parts = p.route && small_router ? 0 : int((d.H + kLogitRows - 1) / kLogitRows);
   if (p.few) {
     const double panels = used * double(d.F / 32) + double(Fs / 32);

@@ -171,6 +171,14 @@ def test_shared_expert_much_longer_than_the_routed_ones(N, H, Fs, dtype):
     check(t, 2, r, _forward(r, t))
 
 
+@pytest.mark.parametrize("H", [128, 640, 1152])
+@pytest.mark.parametrize("N,E,K", [(16, 16, 8), (8, 32, 5), (15, 17, 3), (3, 85, 8), (1, 256, 8), (9, 29, 4), (2, 129, 8)])
+def test_routing_around_one_pair_a_thread(N, E, K, H):
+    t = _inputs(N, H, 128, E, K, torch.bfloat16, 0, True, seed=E)
+    r = _runner(N, t, K)
+    check(t, K, r, _forward(r, t))
+
+
 @pytest.mark.parametrize("N,E,K", [(64, 8, 2), (40, 64, 6), (64, 256, 1)])
 def test_skewed_routing(N, E, K):
     """A bias that sends every token to the same experts (rows of all others empty)."""
