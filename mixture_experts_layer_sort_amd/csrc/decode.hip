@@ -1067,23 +1067,40 @@ struct Plan {
 
 constexpr int64_t kCUs = 256;
 
-// Workgroups (max_parts at most) that share a strip of `panels` panels when there
-// are about `strips` strips.  A CU reads its workgroups' panels at about 31 bytes a
-// nanosecond (0.5 us for the 16 KiB of a panel), and the CU with most of them sets
-// the time as long as all are resident together (`fit` to a CU).  Besides, 1.2 us
-// of latency for each of a wave's first panels; and nothing covers a workgroup's
-// start and end when it is alone on its CU (2%).  Strips of other widths would
-// even the CUs out better, but a row segment that is not 256 bytes, aligned, reads a
-// third slower.
-int cut(double strips, int64_t panels, int max_parts, double fit) {
+// The number of experts that N tokens choose.
+struct Used {
+  double mean;  // if they choose evenly
+  double most;
+};
+
+// Workgroups (max_parts at most) that share a strip of `panels` panels when an
+// expert has `per` strips and the shared one `shared`, by the time that this
+// would take in us:
+//  - A CU reads its workgroups' panels at about 31 bytes a nanosecond (0.5 us for
+//    the 16 KiB of a panel), and the CU with most of them sets the time; all
+//    together read no faster than HBM (0.56 us).  Nothing covers a workgroup's
+//    start and end when it is alone on its CU (2%).
+//  - 1.2 us of latency for each of a wave's first panels, 1 us when workgroups
+//    follow those that a CU holds at a time (`fit`).
+//  - part_cost for writing and adding up one part more.
+// It is the mean over the expected number of experts and a tenth more and less, as
+// the fullest CU's count jumps.  Over 54 sizes the cut so found cost 0.3 % more than
+// the best one of each on average, 4 % at most; the fullest CU alone, without the
+// other terms, 2 % and 15 %.  Strips of other widths would even the CUs out better,
+// but a row segment that is not 256 bytes, aligned, reads a third slower.
+int cut(const Used& used, double per, double shared, int64_t panels, int max_parts, double fit, double part_cost) {
   int best = 1;
   double least = 0.0;
-  for (int p = 1; p <= max_parts && kWaves * p <= panels; ++p) {
-    const double per_cu = strips * p / double(kCUs);
-    if (p > 1 && per_cu > fit) break;
-    const double turns = std::ceil(per_cu) * (per_cu <= 1.0 ? 1.02 : 1.0);
-    const double t = turns * 0.5 * double(panels) / p + 1.2 * std::min(4.0, double(panels) / (kWaves * p));
-    if (p == 1 || t < 0.99 * least) {
+  for (int p = 1; p <= max_parts && (p == 1 || kWaves * p <= panels); ++p) {
+    const int64_t longest = (panels + kWaves * p - 1) / (kWaves * p);  // panels of a workgroup's busiest wave
+    double t = 0.0;
+    for (const double u : {std::max(1.0, 0.9 * used.mean), used.mean, std::min(used.most, 1.1 * used.mean)}) {
+      const double per_cu = (u * per + shared) * p / double(kCUs);
+      const double turns = std::ceil(per_cu) * (per_cu <= 1.0 ? 1.02 : 1.0);
+      t += std::max(0.5 * turns * double(kWaves * longest), 0.56 * per_cu * double(panels) / p) + std::ceil(per_cu / fit);
+    }
+    t = t / 3.0 + 1.2 * double(std::min<int64_t>(4, longest)) + part_cost * (p - 1);
+    if (p == 1 || t < least) {
       best = p;
       least = t;
     }
@@ -1101,11 +1118,15 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   const int64_t NK = d.NK();
   const int64_t fchunks = (d.F + cols - 1) / cols, schunks = (Fs + cols - 1) / cols, chunks = (d.H + cols - 1) / cols;
   q.units = int(std::min(NK, d.E));
-  // experts that N tokens choose if they choose evenly
-  const double used = double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N)));
+  const Used used{double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N))), double(q.units)};
   p.few = d.N <= 16;
   p.joint = q.units * fchunks + schunks >= 200 && NK >= 8 * q.units;
-  q.gu_parts = p.joint ? 1 : cut(2.0 * (used * double(fchunks) + double(schunks)), d.H / 32, 4, p.few ? 3.0 : 2.0);
+  // Up to 16 tokens every strip of the down product reads all parts of its rows' sums; beyond, one
+  // kernel does, once.
+  const double row_elements = 1e-5 * double(NK * d.F + d.N * Fs);
+  q.gu_parts = p.joint ? 1
+                       : cut(used, 2.0 * double(fchunks), 2.0 * double(schunks), d.H / 32, 4, p.few ? 3.0 : 2.0,
+                             p.few ? 3.0 + 3.0 * row_elements : 0.5 + 0.5 * row_elements);
   p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
   // Each workgroup of gate/up ranks the pairs (token, expert) for itself while there is one a
   // thread at most: 1 to 4 us less than with a launch for it (4 tokens, 16 experts: 35.9
@@ -1118,14 +1139,15 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   const bool small_router = (d.E + 15) / 16 * (d.H / 32) <= 4 * kWaves;
   p.logit_parts = p.route && small_router ? 0 : int((d.H + kLogitRows - 1) / kLogitRows);
   if (p.few) {
-    const double panels = used * double(d.F / 32) + double(Fs / 32);
+    const double panels = used.mean * double(d.F / 32) + double(Fs / 32);
     const int64_t want = std::max(kCUs / chunks, int64_t(panels / (4 * kWaves)));
     q.dn_parts = int(std::max<int64_t>(1, std::min({int64_t(panels / kWaves), 2 * kCUs / chunks, want})));
   } else {
     // Two workgroups fit a CU (row tiles take the registers).  A longer shared strip is cut
     // more often, but all of them into no more pieces than CUs (64 tokens, H 2048, F 128,
     // Fs 32768: 127 us so, 177 without the bound).
-    q.dn_parts = cut(used * double(chunks), d.F / 32, 16, 2.0);
+    q.dn_parts = cut(used, double(chunks), double(chunks) * double(Fs) / double(d.F), d.F / 32, 16, 2.0,
+                     0.25 + 7.5e-6 * double(NK * d.H));
     const int64_t longer = q.dn_parts * ((Fs + d.F - 1) / d.F), most = std::max<int64_t>(kCUs / chunks, 1);
     q.sdn_parts = int(std::min({Fs / (32 * kWaves), longer, most}));
   }
