@@ -1088,9 +1088,12 @@ struct Used {
 // the best one of each on average, 4 % at most; the fullest CU alone, without the
 // other terms, 2 % and 15 %.  Strips of other widths would even the CUs out better,
 // but a row segment that is not 256 bytes, aligned, reads a third slower.
-int cut(const Used& used, double per, double shared, int64_t panels, int max_parts, double fit, double part_cost) {
-  int best = 1;
-  double least = 0.0;
+struct Cut {
+  int parts;
+  double us;
+};
+Cut cut(const Used& used, double per, double shared, int64_t panels, int max_parts, double fit, double part_cost) {
+  Cut best = {1, 0.0};
   for (int p = 1; p <= max_parts && (p == 1 || kWaves * p <= panels); ++p) {
     const int64_t longest = (panels + kWaves * p - 1) / (kWaves * p);  // panels of a workgroup's busiest wave
     double t = 0.0;
@@ -1100,10 +1103,7 @@ int cut(const Used& used, double per, double shared, int64_t panels, int max_par
       t += std::max(0.5 * turns * double(kWaves * longest), 0.56 * per_cu * double(panels) / p) + std::ceil(per_cu / fit);
     }
     t = t / 3.0 + 1.2 * double(std::min<int64_t>(4, longest)) + part_cost * (p - 1);
-    if (p == 1 || t < least) {
-      best = p;
-      least = t;
-    }
+    if (p == 1 || t < best.us) best = {p, t};
   }
   return best;
 }
@@ -1120,13 +1120,20 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   q.units = int(std::min(NK, d.E));
   const Used used{double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N))), double(q.units)};
   p.few = d.N <= 16;
-  p.joint = q.units * fchunks + schunks >= 200 && NK >= 8 * q.units;
   // Up to 16 tokens every strip of the down product reads all parts of its rows' sums; beyond, one
   // kernel does, once.
   const double row_elements = 1e-5 * double(NK * d.F + d.N * Fs);
-  q.gu_parts = p.joint ? 1
-                       : cut(used, 2.0 * double(fchunks), 2.0 * double(schunks), d.H / 32, 4, p.few ? 3.0 : 2.0,
-                             p.few ? 3.0 + 3.0 * row_elements : 0.5 + 0.5 * row_elements);
+  const double fit = p.few ? 3.0 : 2.0;
+  const Cut apart = cut(used, 2.0 * double(fchunks), 2.0 * double(schunks), d.H / 32, 4, fit,
+                        p.few ? 3.0 + 3.0 * row_elements : 0.5 + 0.5 * row_elements);
+  // Both matrices in one workgroup spare the sums of G and U their way through memory, and the
+  // workgroups that load them the activations, but leave half as many strips to spread.  20 tokens
+  // of 8 experts (H 4096, F 14336): 448 us so, 455 apart; 64 of them 461 and 496; 16 tokens of 16
+  // experts (H 2048, F 6400): 220 and 227; 64 tokens of 64 experts (H 2048, F 1408): 239 and 232;
+  // with two rows an expert (8 tokens of 8 experts) 422 and 416.
+  const Cut both = cut(used, double(fchunks), double(schunks), d.H / 16, 1, fit, 0.0);
+  p.joint = NK >= 4 * q.units && both.us <= 1.05 * apart.us + 0.9 * row_elements;
+  q.gu_parts = p.joint ? 1 : apart.parts;
   p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
   // Each workgroup of gate/up ranks the pairs (token, expert) for itself while there is one a
   // thread at most: 1 to 4 us less than with a launch for it (4 tokens, 16 experts: 35.9
@@ -1147,7 +1154,7 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
     // more often, but all of them into no more pieces than CUs (64 tokens, H 2048, F 128,
     // Fs 32768: 127 us so, 177 without the bound).
     q.dn_parts = cut(used, double(chunks), double(chunks) * double(Fs) / double(d.F), d.F / 32, 16, 2.0,
-                     0.25 + 7.5e-6 * double(NK * d.H));
+                     0.1 + 7.5e-6 * double(NK * d.H)).parts;
     const int64_t longer = q.dn_parts * ((Fs + d.F - 1) / d.F), most = std::max<int64_t>(kCUs / chunks, 1);
     q.sdn_parts = int(std::min({Fs / (32 * kWaves), longer, most}));
   }
