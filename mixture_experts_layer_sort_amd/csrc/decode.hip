@@ -85,10 +85,11 @@ __device__ __forceinline__ void park_logits(const f64x4_t& acc, double* red) {
   for (int r = 0; r < 4; ++r) red[(4 * r + lane_id() / 16) * 16 + lane_id() % 16] = acc[r];
 }
 
-// Partial logits part[s][n][e] over rows s*512 .. of W_r for 16 experts.  A wave
-// has 32 rows; the waves' sums meet in LDS in wave order.  The first workgroup
-// of each row range also packs x as xp [H/32][N][32], so that the row operand of
-// a panel is one contiguous piece.
+// Partial logits part[s][n][e] over rows s*512 .. of W_r for 16 experts and 16
+// tokens.  A wave has 32 rows; the waves' sums meet in LDS in wave order.  The
+// first workgroup of each row range and token tile also packs x as xp
+// [H/32][N][32], so that the row operand of a panel is one contiguous piece.  The
+// token tiles are workgroups of their own: 64 tokens take 5 us so, 9 in a loop.
 template <typename T>
 __global__ __launch_bounds__(kLogitWaves * kWave) void k_decode_logits(const T* __restrict__ x,
                                                                       const T* __restrict__ w_r,
@@ -96,32 +97,28 @@ __global__ __launch_bounds__(kLogitWaves * kWave) void k_decode_logits(const T* 
                                                                       int N, int H, int E) {
   __shared__ double red[kLogitWaves][256];
   const int wave = threadIdx.x / kWave, g = lane_id() / 16, c = lane_id() % 16;
-  const int e0 = blockIdx.y * 16;
+  const int e0 = blockIdx.y * 16, n0 = blockIdx.z * 16;
   const int h = blockIdx.x * kLogitRows + wave * 32;
-  const bool live = h < H;  // the same in the whole wave: H is a multiple of 128
-  for (int n0 = 0; n0 < N; n0 += 16) {
-    f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
-    const int n = min(n0 + c, N - 1);
-    if (live) {
-      const T* px = x + int64_t(n) * H;
-      logit_panel(px, w_r, h, E, min(e0 + c, E - 1), acc);
-      if (blockIdx.y == 0 && n == n0 + c) {
-        const uint4* from = reinterpret_cast<const uint4*>(px + h + 8 * g);
-        uint4* to = reinterpret_cast<uint4*>(xp + (int64_t(h / 32) * N + n) * 32 + 8 * g);
+  f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
+  const int n = min(n0 + c, N - 1);
+  if (h < H) {  // the same in the whole wave: H is a multiple of 128
+    const T* px = x + int64_t(n) * H;
+    logit_panel(px, w_r, h, E, min(e0 + c, E - 1), acc);
+    if (blockIdx.y == 0 && n == n0 + c) {
+      const uint4* from = reinterpret_cast<const uint4*>(px + h + 8 * g);
+      uint4* to = reinterpret_cast<uint4*>(xp + (int64_t(h / 32) * N + n) * 32 + 8 * g);
 #pragma unroll
-        for (int j = 0; j < 8 * int(sizeof(T)) / 16; ++j) to[j] = from[j];
-      }
+      for (int j = 0; j < 8 * int(sizeof(T)) / 16; ++j) to[j] = from[j];
     }
-    park_logits(acc, red[wave]);
-    __syncthreads();
-    const int tok = n0 + threadIdx.x / 16, ex = e0 + threadIdx.x % 16;
-    if (threadIdx.x < 256 && tok < N && ex < E) {
-      double v = 0.0;
+  }
+  park_logits(acc, red[wave]);
+  __syncthreads();
+  const int tok = n0 + threadIdx.x / 16, ex = e0 + threadIdx.x % 16;
+  if (threadIdx.x < 256 && tok < N && ex < E) {
+    double v = 0.0;
 #pragma unroll
-      for (int i = 0; i < kLogitWaves; ++i) v += red[i][threadIdx.x];
-      part[(int64_t(blockIdx.x) * N + tok) * E + ex] = v;
-    }
-    __syncthreads();
+    for (int i = 0; i < kLogitWaves; ++i) v += red[i][threadIdx.x];
+    part[(int64_t(blockIdx.x) * N + tok) * E + ex] = v;
   }
 }
 
@@ -163,9 +160,16 @@ __device__ __forceinline__ void rank_pairs(double v, const float* __restrict__ b
   __syncthreads();
   if (live) {
     const double* l = out->l + n * E;
+    // one comparison each for the experts below and above all of the wave's own
+    const int first = __builtin_amdgcn_readfirstlane(e), lo = first + kWave <= E ? first : 0;
+    const int hi = first + kWave <= E ? first + kWave : E;
     int before = 0;
 #pragma unroll 8
-    for (int i = 0; i < E; ++i) before += l[i] > v || (l[i] == v && i < e);
+    for (int i = 0; i < lo; ++i) before += l[i] >= v;
+#pragma unroll 8
+    for (int i = lo; i < hi; ++i) before += l[i] > v || (l[i] == v && i < e);
+#pragma unroll 8
+    for (int i = hi; i < E; ++i) before += l[i] > v;
     if (before < K) {
       out->ids[n * K + before] = e;
       out->sel[n * K + before] = v;
@@ -659,7 +663,9 @@ __device__ __forceinline__ void gate_up(const XRows<T>& x, const T* wg, const T*
                                         const GuOut<T, JOINT>& out, float* red) {
   const bool wide = kCols<T> == kAlign || col0 + kCols<T> <= ld;  // else a last single segment
   if constexpr (MTMAX > 2)
-    if (M > 32) return gate_up_rows<T, 1, 4, JOINT, true>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
+    if (M > 32)
+      return M > 48 ? gate_up_rows<T, 1, 4, JOINT, true>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red)
+                    : gate_up_rows<T, 1, 3, JOINT, true>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red);
   if constexpr (MTMAX > 1)
     if (M > 16)
       return wide ? gate_up_rows<T, 2, 2, JOINT, false>(x, wg, wu, H, ld, col0, rows, M, div, part, parts, out, red)
@@ -829,7 +835,9 @@ __device__ __forceinline__ void down(const T* __restrict__ act, int64_t plane, c
                                      float* red) {
   const bool wide = kCols<T> == kAlign || col0 + kCols<T> <= H;
   if constexpr (MTMAX > 2)
-    if (M > 32) return down_rows<T, 1, 4, true>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
+    if (M > 32)
+      return M > 48 ? down_rows<T, 1, 4, true>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red)
+                    : down_rows<T, 1, 3, true>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
   if (M > 16)
     return wide ? down_rows<T, 2, 2, false>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red)
                 : down_rows<T, 1, 2, false>(act, plane, wd, F, H, col0, rows, M, part, parts, out, red);
@@ -1261,7 +1269,7 @@ hipError_t decode_t(const moe_launch::Dims& d, int64_t Fs, const Args<T>& a, hip
   const Shape& q = p.q;
   double* logits = reinterpret_cast<double*>(a.ws + p.logits);
   if (p.logit_parts > 0) {
-    k_decode_logits<T><<<dim3(p.logit_parts, (q.E + 15) / 16), dim3(kLogitWaves * kWave), 0, s>>>(
+    k_decode_logits<T><<<dim3(p.logit_parts, (q.E + 15) / 16, (q.N + 15) / 16), dim3(kLogitWaves * kWave), 0, s>>>(
         a.x, a.w_r, logits, reinterpret_cast<T*>(a.ws + p.xp), q.N, q.H, q.E);
     MOE_LAUNCHED()
   }

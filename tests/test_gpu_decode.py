@@ -171,6 +171,16 @@ def test_shared_expert_much_longer_than_the_routed_ones(N, H, Fs, dtype):
     check(t, 2, r, _forward(r, t))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("F", [256, 6528])               # gate and up apart, and in one workgroup
+@pytest.mark.parametrize("N", [16, 17, 32, 33, 48, 49, 64])
+def test_every_number_of_row_tiles(N, F, dtype):
+    """Every expert has all N rows."""
+    t = _inputs(N, 128, F, 8, 8, dtype, 384, True, seed=N)
+    r = _runner(N, t, 8, 384)
+    check(t, 8, r, _forward(r, t))
+
+
 @pytest.mark.parametrize("H", [128, 640, 1152])
 @pytest.mark.parametrize("N,E,K", [(16, 16, 8), (8, 32, 5), (15, 17, 3), (3, 85, 8), (1, 256, 8), (9, 29, 4), (2, 129, 8)])
 def test_routing_around_one_pair_a_thread(N, E, K, H):
