@@ -1138,9 +1138,10 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   // workgroups that load them the activations, but leave half as many strips to spread.  20 tokens
   // of 8 experts (H 4096, F 14336): 448 us so, 455 apart; 64 of them 461 and 496; 16 tokens of 16
   // experts (H 2048, F 6400): 220 and 227; 64 tokens of 64 experts (H 2048, F 1408): 239 and 232;
-  // with two rows an expert (8 tokens of 8 experts) 422 and 416.
+  // with two rows an expert (8 tokens of 8 experts) 422 and 416; 12 tokens of 10 experts (H 640,
+  // F 7168, K 8) 84 and 78.
   const Cut both = cut(used, double(fchunks), double(schunks), d.H / 16, 1, fit, 0.0);
-  p.joint = NK >= 4 * q.units && both.us <= 1.05 * apart.us + 0.9 * row_elements;
+  p.joint = NK >= 4 * q.units && both.us <= (p.few ? 1.08 * apart.us : 1.05 * apart.us + 0.9 * row_elements);
   q.gu_parts = p.joint ? 1 : apart.parts;
   p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
   // Each workgroup of gate/up ranks the pairs (token, expert) for itself while there is one a

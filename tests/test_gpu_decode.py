@@ -181,6 +181,15 @@ def test_every_number_of_row_tiles(N, F, dtype):
     check(t, 8, r, _forward(r, t))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,E", [(8, 8), (13, 8), (16, 4)])
+def test_few_tokens_of_wide_experts(N, E, dtype):
+    """About as many strips as CUs, all rows in one tile: gate and up in one workgroup."""
+    t = _inputs(N, 512, 4480, E, E, dtype, 384, True, seed=N)
+    r = _runner(N, t, E, 384)
+    check(t, E, r, _forward(r, t))
+
+
 @pytest.mark.parametrize("H", [128, 640, 1152])
 @pytest.mark.parametrize("N,E,K", [(16, 16, 8), (8, 32, 5), (15, 17, 3), (3, 85, 8), (1, 256, 8), (9, 29, 4), (2, 129, 8)])
 def test_routing_around_one_pair_a_thread(N, E, K, H):
