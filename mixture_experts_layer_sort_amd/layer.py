@@ -544,15 +544,10 @@ def moe_rms_norm(x, weight, residual=None, eps: float = 1e-6):
 
 
 def _grad_call(grads, outs):
-    """The checked lists, their device, the result and the address of the scratch behind it."""
+    """The lists, their device, the result and the address of the scratch behind it."""
     grads = list(grads)
     outs = grads if outs is None else list(outs)
-    if len(grads) != len(outs):
-        raise ValueError("as many outputs as gradients are needed")
     dev = grads[0].device if grads else _cuda_device("cuda")
-    for t in grads if outs is grads else grads + outs:
-        if t.device != dev:
-            raise ValueError("all gradients and outputs must be on one device")
     buf = torch.empty((L.MOE_GRAD_WS_BYTES // 4 + 1,), dtype=torch.float32, device=dev)  # scratch, then norm
     return grads, outs, dev, buf[L.MOE_GRAD_WS_BYTES // 4:], buf.data_ptr()
 
