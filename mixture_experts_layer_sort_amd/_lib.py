@@ -147,8 +147,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the same handle as torch.cuda.current_stream().cuda_stream, without building the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # the same handle as torch.cuda.current_stream().cuda_stream, without building the Stream
+        # object (the arguments are device tensors, so torch has initialised the device)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

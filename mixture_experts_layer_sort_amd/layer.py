@@ -361,7 +361,7 @@ _HERE = contextlib.nullcontext()
 
 def _on(dev: torch.device):
     """The launches of a call go to the tensors' device, whatever device is current."""
-    if dev.type != "cuda" or torch.cuda.current_device() == dev.index:
+    if dev.type != "cuda" or torch._C._cuda_getDevice() == dev.index:
         return _HERE
     return torch.cuda.device(dev)
 
@@ -395,6 +395,7 @@ class MoEDecodeRunner:
         self._gates = torch.empty((max_tokens, K), dtype=torch.float32, device=dev)
         self._y = torch.empty((max_tokens, H), dtype=dtype, device=dev)
         self.topk, self.gates, self.y = self._topk, self._gates, self._y
+        self._at = self._topk.data_ptr(), self._gates.data_ptr(), self._y.data_ptr()  # of any first n rows too
 
     def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None, shared=None):
         """Returns y [n, H] of x [n, H], n <= max_tokens; topk and gates [n, K]
@@ -422,8 +423,7 @@ class MoEDecodeRunner:
         d, ds = self._dims[n]
         if n:
             with _on(dev):
-                L.moe_decode(d, x, w_r, bias, w_gate, w_up, w_down, ds, sg, su, sd, self.topk, self.gates, self.y,
-                             self.ws, stream)
+                L.moe_decode(d, x, w_r, bias, w_gate, w_up, w_down, ds, sg, su, sd, *self._at, self.ws, stream)
         return self.y
 
 
@@ -443,6 +443,7 @@ class MoENormRunner:
         self._h = torch.empty((N, H), dtype=dtype, device=dev)
         self._y = torch.empty((N, H), dtype=dtype, device=dev)
         self._rstd = torch.empty((N,), dtype=torch.float32, device=dev)
+        self._at = self._h.data_ptr(), self._y.data_ptr(), self._rstd.data_ptr()  # of any first n rows too
         if backward:
             self._dx = torch.empty((N, H), dtype=dtype, device=dev)
             self.dweight = torch.empty((H,), dtype=torch.float32, device=dev)
@@ -468,7 +469,8 @@ class MoENormRunner:
         self.h = x if h is None else h
         if n:
             with _on(self.device):
-                L.moe_rms_norm(self.d, x, residual, weight, self.eps, h, self.y, self.rstd, stream)
+                h_at, y_at, rstd_at = self._at
+                L.moe_rms_norm(self.d, x, residual, weight, self.eps, None if h is None else h_at, y_at, rstd_at, stream)
         self.inputs = weight
         return self.y
 
