@@ -280,7 +280,7 @@ template <typename T>
 hipError_t norm_bwd_t(const moe_launch::Dims& d, const void* dy, const void* h, const void* weight, const float* rstd,
                       const void* dh, void* dx, float* dw, void* ws, hipStream_t s) {
   const int B = norm_bwd_blocks<T>(d);
-  float* part = static_cast<float*>(ws);
+  float* part = B == 1 ? dw : static_cast<float*>(ws);  // one workgroup's sums are the result
   hipError_t e = by_row(int(d.H / Vec16<T>::n), [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
     auto* const kernel = streams<T>(d) ? k_norm_bwd<T, NT, VPT, true> : k_norm_bwd<T, NT, VPT, false>;
@@ -289,7 +289,7 @@ hipError_t norm_bwd_t(const moe_launch::Dims& d, const void* dy, const void* h, 
         static_cast<const T*>(dh), static_cast<T*>(dx), part, d.N, int(d.H));
     return hipGetLastError();
   });
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || B == 1) return e;
   k_norm_dw<<<dim3(unsigned(d.H / 16)), dim3(1024), 0, s>>>(part, dw, B, int(d.H));
   return hipGetLastError();
 }

@@ -541,7 +541,9 @@ def moe_rms_norm(x, weight, residual=None, eps: float = 1e-6):
     """RMS norm of the rows of x [..., H] with autograd support, the step in
     front of moe_layer: y = x / sqrt(mean(x^2) + eps) * weight.  With a
     residual, h = x + residual is normalised instead and (y, h) is returned, h
-    being the residual stream that the layer's output is added to."""
+    being the residual stream that the layer's output is added to.  In a captured
+    graph take gradients with torch.autograd.grad (or use MoENormRunner): backward()
+    would add to the leaves on the stream of any eager graph of theirs that lives."""
     return MoERMSNormFunction.apply(x, weight, residual, eps)
 
 
