@@ -12,8 +12,8 @@
 //
 // A row stays in registers between its one read and its write, so memory
 // traffic is the inputs and outputs alone and HBM bounds both directions.  A
-// row belongs to one wave while it has at most 256 16-byte vectors (no LDS, no
-// barrier), else to a workgroup.  In the backward a workgroup walks over many
+// row belongs to one wave, or 16 or 32 lanes of one, while it has at most 256
+// 16-byte vectors (no LDS, no barrier), else to a workgroup.  In the backward a workgroup walks over many
 // rows and keeps its share of dweight in registers; the workgroups' partial
 // sums are added in a fixed order by a second kernel, so results do not depend
 // on timing.
@@ -31,10 +31,15 @@ constexpr int kNormBwdBlocks = 768;
 // Workgroups of the forward at most (threads in a grid are counted in 32 bits).
 constexpr int64_t kNormMaxBlocks = 1 << 20;
 
-// Sum over the threads that share a row (NT = 64: a wave), the same in each of
-// them.  s: one float per wave.
+// Sum over the threads that share a row (NT up to 64: lanes of a wave), the same
+// in each of them.  s: one float per wave.
 template <int NT>
 __device__ __forceinline__ float row_sum(float v, float* s) {
+  if constexpr (NT < kWave) {
+#pragma unroll
+    for (int off = NT / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, NT);
+    return v;
+  }
   v = wave_sum(v);
   if constexpr (NT > kWave) {
     __syncthreads();  // s is free again
@@ -78,7 +83,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(const T* x, const 
                                                              int H, float eps) {
   constexpr int V = Vec16<T>::n;
   constexpr int RPB = NT < 256 ? 256 / NT : 1;  // rows per workgroup
-  __shared__ float s[NT / kWave];
+  __shared__ float s[NT > kWave ? NT / kWave : 1];
   const int t = threadIdx.x % NT;
   const int nv = H / V;
   // waves of one workgroup may end at different rows: they share no barrier then
@@ -134,7 +139,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(const T* dy, c
                                                                  float* __restrict__ part, int64_t N, int H) {
   constexpr int V = Vec16<T>::n;
   constexpr int RPB = NT < 256 ? 256 / NT : 1;
-  __shared__ float s[NT / kWave];
+  __shared__ float s[NT > kWave ? NT / kWave : 1];
   const int t = threadIdx.x % NT;
   const int nv = H / V;
   float dw[VPT][V];
@@ -187,7 +192,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(const T* dy, c
   }
   if constexpr (RPB > 1) {
     // the waves' sums, added in wave order
-    __shared__ float sw[VPT * kWave * V];
+    __shared__ float sw[VPT * NT * V];
     for (int q = 0; q < RPB; ++q) {
       if ((int)threadIdx.x / NT == q)
 #pragma unroll
@@ -236,9 +241,13 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
 }
 
 // Threads per row and vectors per thread for a row of nv 16-byte vectors, as
-// F<NT, VPT>().
+// F<NT, VPT>().  A short row has no more lanes than vectors: a training step of
+// 65536 x 128 bf16 rows takes 32 us so, 55 with a wave a row; of 16384 x 256, 20
+// and 23.5.
 template <typename F>
 hipError_t by_row(int nv, F f) {
+  if (nv <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+  if (nv <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
   if (nv <= 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
   if (nv <= 128) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
   if (nv <= 256) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
@@ -272,7 +281,7 @@ hipError_t norm_t(const moe_launch::Dims& d, const void* x, const void* residual
 template <typename T>
 int norm_bwd_blocks(const moe_launch::Dims& d) {
   const int64_t nv = d.H / Vec16<T>::n;
-  const int64_t rpb = nv <= 256 ? 4 : 1;
+  const int64_t rpb = nv <= 16 ? 16 : nv <= 32 ? 8 : nv <= 256 ? 4 : 1;  // as by_row
   return int(std::min<int64_t>(kNormBwdBlocks, (d.N + rpb - 1) / rpb));
 }
 

@@ -88,6 +88,16 @@ def test_norm_matches_float64(N, H, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [2, 15, 16, 17, 1003, 20011])
+@pytest.mark.parametrize("H", [128, 256, 384])
+def test_short_rows_share_a_wave(N, H, dtype):
+    """dweight joins up to 16 rows' sums in a workgroup here instead of 4, but a row's sum of
+    squares has at most 8 terms a thread and 5 steps, so rstd is good to (13 / 2 + 5) u: 15 joins
+    and 12 u stay within the 12 + 34 u that the check allows besides ceil(N / 512)."""
+    test_norm_matches_float64(N, H, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_in_place_and_partial_rows(dtype):
     from mixture_experts_layer_sort_amd import MoENormRunner, _lib as L
     x, res, w, dy, dh = _make(11, 4096, dtype, seed=1)
