@@ -687,8 +687,9 @@ struct Shape {
 
 // G and U sums, a workgroup having one matrix's columns and part of its
 // contraction: gu [part][2][slot][F], sgu [part][2][token][Fs].  ROUTE: the
-// workgroup finds topk and gates itself, the first one writes them.  The first
-// workgroup clears the n_arrived counters of k_decode_down_all.
+// workgroup finds topk and gates itself (one of the shared expert needs none), the
+// first of the routed experts writes them.  The first workgroup clears the
+// n_arrived counters of k_decode_down_all.
 template <typename T, int MTMAX, bool ROUTE>
 __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* __restrict__ wg,
                                                            const T* __restrict__ wu, const T* __restrict__ swg,
@@ -702,17 +703,19 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* 
   const int32_t* topk = topk_out;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
-  if constexpr (ROUTE) {
-    __shared__ TopK routed;
-    route_here(route, q.N, q.H, q.E, q.K, &routed, reinterpret_cast<double*>(red));
-    topk = routed.ids;
-    if (blockIdx.x == 0 && int(threadIdx.x) < q.N * q.K) {
-      topk_out[threadIdx.x] = routed.ids[threadIdx.x];
-      gates[threadIdx.x] = routed.gates[threadIdx.x];
-    }
-  }
   const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
   const int schunks = (q.Fs + kCols<T> - 1) / kCols<T>, shared = 2 * q.gu_parts * schunks;
+  if constexpr (ROUTE) {
+    __shared__ TopK routed;
+    if (int(blockIdx.x) >= shared) {  // the shared expert needs no choice
+      route_here(route, q.N, q.H, q.E, q.K, &routed, reinterpret_cast<double*>(red));
+      topk = routed.ids;
+      if (int(blockIdx.x) == shared && int(threadIdx.x) < q.N * q.K) {
+        topk_out[threadIdx.x] = routed.ids[threadIdx.x];
+        gates[threadIdx.x] = routed.gates[threadIdx.x];
+      }
+    }
+  }
   int b = int(blockIdx.x) - shared;
   if (b >= 0) {
     const int chunk = b % chunks;
