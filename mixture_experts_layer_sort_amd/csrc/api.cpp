@@ -481,9 +481,13 @@ int moe_decode(const moe_dims* d, const void* x, const void* w_r, const float* l
   if (ds != nullptr ? !ptrs_ok(ws_gate, ws_up, ws_down)
                     : (ws_gate != nullptr || ws_up != nullptr || ws_down != nullptr))
     return MOE_EINVAL;
-  if (overlap(x, row_bytes(D), y, row_bytes(D))) return MOE_EINVAL;
+  const size_t need = D.N == 0 ? 0 : moe_launch::decode_ws(D, Fs), nk = size_t(D.N) * size_t(D.K) * 4;
+  const void* const at[] = {x, y, topk_idx, gates, ws};
+  const size_t bytes[] = {row_bytes(D), row_bytes(D), nk, nk, need};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(at[i], bytes[i], at[j], bytes[j])) return MOE_EINVAL;
   if (D.N == 0) return MOE_OK;
-  const size_t need = moe_launch::decode_ws(D, Fs);
   if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;
   return from_hip(moe_launch::decode(D, x, w_r, logit_bias, w_gate, w_up, w_down, Fs, ws_gate, ws_up, ws_down,
                                      topk_idx, gates, y, ws, stream));

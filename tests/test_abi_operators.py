@@ -63,6 +63,18 @@ def test_decode_pointers(lib):
     assert decode(D(N=0), nb=0, ws=None) == L.MOE_OK            # nothing to do
 
 
+def test_decode_outputs_and_workspace_overlap_nothing(lib):
+    need = L.moe_decode_workspace_bytes(D())
+    a = dict(topk=at(30), gates=at(31), y=at(32), x=at(33))
+    for name in a:
+        for other in a:
+            if name < other:
+                assert decode(D(), ws=at(40), **{**a, name: a[other]}) == L.MOE_EINVAL, (name, other)
+    assert decode(D(), ws=at(40), **{**a, "topk": at(40)}) == L.MOE_EINVAL
+    assert decode(D(), ws=at(40), **{**a, "gates": at(40) + need - 16}) == L.MOE_EINVAL
+    assert decode(D(), ws=at(40), **{**a, "y": at(40) - 256}) == L.MOE_EINVAL
+
+
 def test_decode_shared_expert_dims(lib):
     s = (at(10), at(11), at(12))
     good = D(F=384, E=1, K=1)
