@@ -1008,13 +1008,13 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down_all(Rows<T, FUSED> in, c
   else
     down_all<T, 1, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
   if (arrived == nullptr) return;
-  // every thread's part is in memory before the count says so, and the last
-  // workgroup reads the parts only after it has counted all of them
+  // Every thread's part is in memory before the count says so, and the last
+  // workgroup reads the parts only after it has counted all of them.  The fence
+  // stands before the barrier, in every wave: the barrier waits for no store, and
+  // a fence behind it would wait for those of thread 0's wave alone.
+  __threadfence();
   __syncthreads();
-  if (t == 0) {
-    __threadfence();
-    counts[0] = atomicAdd(&arrived[blockIdx.x % chunks], 1) == q.dn_parts - 1;
-  }
+  if (t == 0) counts[0] = atomicAdd(&arrived[blockIdx.x % chunks], 1) == q.dn_parts - 1;
   __syncthreads();
   if (!counts[0]) return;
   __threadfence();
