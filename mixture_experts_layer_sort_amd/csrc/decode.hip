@@ -27,8 +27,8 @@
 //  - The waves of a workgroup split the contraction; their float32 sums meet
 //    in LDS in a fixed order, those of several workgroups in the next kernel.
 // gate/up leaves float32 sums; the down kernel forms gate * silu(G) * U as it
-// loads them, for bf16 as the sum of two bf16 values (hi + lo), so the
-// activation keeps float32 accuracy.  y is rounded once.  Router logits are
+// loads them, for bf16 as the exact sum of three bf16 values of eight significant
+// bits each, so the activation keeps its 24.  y is rounded once.  Router logits are
 // summed in float64, so the choice of experts does not depend on the order of
 // the sum.
 #include <algorithm>
@@ -336,24 +336,37 @@ template <int S> struct Panel<bf16_t, S> {
     words4_t a;
     __device__ __forceinline__ void load(const bf16_t* p) { a = *reinterpret_cast<const words4_t*>(p); }
   };
-  // float32 values as the sum of two bf16 operands; stored, lo lies a plane behind hi
+  // float32 values as the sum of three bf16 operands, the bits of a value cut in
+  // three, so that the sum is exact and a finite value's parts are finite; stored,
+  // each operand lies a plane behind the one before
   struct A2 {
-    words4_t hi, lo;
+    words4_t hi, mid, lo;
     __device__ __forceinline__ void load(const bf16_t* p, int64_t plane) {
       hi = *reinterpret_cast<const words4_t*>(p);
-      lo = *reinterpret_cast<const words4_t*>(p + plane);
+      mid = *reinterpret_cast<const words4_t*>(p + plane);
+      lo = *reinterpret_cast<const words4_t*>(p + 2 * plane);
     }
     __device__ __forceinline__ void store(bf16_t* p, int64_t plane) const {
       *reinterpret_cast<words4_t*>(p) = hi;
-      *reinterpret_cast<words4_t*>(p + plane) = lo;
+      *reinterpret_cast<words4_t*>(p + plane) = mid;
+      *reinterpret_cast<words4_t*>(p + 2 * plane) = lo;
     }
+    // the upper halves of two floats in one word
+    static __device__ __forceinline__ uint32_t upper(const float* r) {
+      return __builtin_amdgcn_perm(__float_as_uint(r[1]), __float_as_uint(r[0]), 0x07060302u);
+    }
+    static __device__ __forceinline__ float rest(float r) { return r - __uint_as_float(__float_as_uint(r) & 0xffff0000u); }
     __device__ __forceinline__ void set(const float* v) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        hi[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-        const float h0 = __uint_as_float(hi[j] << 16), h1 = __uint_as_float(hi[j] & 0xffff0000u);
-        // an infinite or NaN value is all in hi
-        lo[j] = pack_bf16x2(isfinite(h0) ? v[2 * j] - h0 : 0.f, isfinite(h1) ? v[2 * j + 1] - h1 : 0.f);
+        float r[2] = {v[2 * j], v[2 * j + 1]};
+        hi[j] = upper(r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) r[i] = isfinite(r[i]) ? rest(r[i]) : 0.f;  // an infinite or NaN value is all in hi
+        mid[j] = upper(r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) r[i] = rest(r[i]);
+        lo[j] = upper(r);
       }
     }
   };
@@ -377,6 +390,7 @@ template <int S> struct Panel<bf16_t, S> {
   static __device__ __forceinline__ void fma(const A& a, bf16x8_t b, f32x4_t& acc) { fma(a.a, b, acc); }
   static __device__ __forceinline__ void fma(const A2& a, bf16x8_t b, f32x4_t& acc) {
     fma(a.lo, b, acc);
+    fma(a.mid, b, acc);
     fma(a.hi, b, acc);
   }
   template <int MT, typename Op>
@@ -778,7 +792,7 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up_act(XRows<T> x, const
 
 // The activations of all slots, then of the shared expert's tokens, in the form
 // that the down kernels load: act [F/32][slot][32] and sact [Fs/32][token][32],
-// planes of hi and lo for bf16.  A thread has 8 columns.
+// three planes for bf16.  A thread has 8 columns.
 template <typename T>
 __global__ __launch_bounds__(256) void k_decode_act(const float* __restrict__ gu, const float* __restrict__ sgu,
                                                     const float* __restrict__ gates, T* __restrict__ act,
@@ -1182,8 +1196,9 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   p.arrived = take(size_t(chunks) * sizeof(int32_t));
   p.gu = take(p.joint ? 0 : size_t(q.gu_parts) * 2 * NK * d.F * 4);
   p.sgu = take(p.joint ? 0 : size_t(q.gu_parts) * 2 * d.N * Fs * 4);
-  p.act = take(p.fused ? 0 : size_t(NK) * d.F * 4);
-  p.sact = take(p.fused ? 0 : size_t(d.N) * Fs * 4);
+  constexpr size_t act = sizeof(T) == 2 ? 3 * sizeof(T) : sizeof(T);  // bytes of an activation: Panel<T, S>::A2
+  p.act = take(p.fused ? 0 : size_t(NK) * d.F * act);
+  p.sact = take(p.fused ? 0 : size_t(d.N) * Fs * act);
   p.ysp = take(size_t(q.dn_parts) * (p.few ? d.N : NK) * d.H * 4);
   p.sysp = take(p.few ? 0 : size_t(q.sdn_parts) * d.N * d.H * 4);
   p.bytes = at;

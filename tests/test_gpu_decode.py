@@ -402,3 +402,46 @@ def test_decode_reads_offsets_beyond_32_bits():
     assert (r.topk == 2 * E - 1).all()
     o, e = _ffn(t["x"], t["w_gate"][-1], t["w_up"][-1], t["w_down"][-1], 2.0 ** -8)
     assert ((y.double() - o).abs() <= 2.0 ** -8 * o.abs() + 1.01 * e).all()
+
+
+def _cancelling_down(A, g):
+    """W_down [F, H] with three weights a column, chosen so that the sum over the activations A
+    (float64) nearly cancels: about 2^-18 of its terms is left."""
+    F = A.numel()
+    wd = torch.zeros((F, 128), dtype=torch.float64)
+    r = lambda v: v.to(torch.bfloat16).double()  # noqa: E731
+    for h in range(128):
+        f = torch.randperm(F, generator=g)[:3]
+        f = f[torch.argsort(A[f].abs(), descending=True)]
+        a = A[f]
+        w1 = r(-a[0] / a[1])
+        wd[f, h] = torch.stack([torch.ones((), dtype=torch.float64), w1, r(-(a[0] + a[1] * w1) / a[2])])
+    return wd
+
+
+@pytest.mark.parametrize("N,F,E", [(1, 128, 1), (3, 256, 2), (16, 128, 1), (24, 256, 2), (40, 384, 1), (64, 128, 2),
+                                   (16, 6528, 8), (24, 6528, 8), (64, 6656, 8)])
+def test_activations_keep_float32_accuracy_in_bf16(N, F, E):
+    """Tokens with one nonzero value: G and U are single exact products.  All E experts are chosen
+    with gates of 1/E (exact), all but one have a W_down of zero, and that one's columns cancel.
+    So the sum has three terms: with 8 u of an activation's own, 4 u of the sum's, y is good to
+    s |ref| + 12 u |A|.|W_down|.  An activation of two bf16 values (16 bits) misses that for two
+    columns of three, by up to a factor of seven."""
+    g = torch.Generator()
+    g.manual_seed(N + F)
+    t = {k: torch.zeros(s, dtype=torch.bfloat16) for k, s in
+         dict(x=(N, 128), w_r=(128, E), w_gate=(E, 128, F), w_up=(E, 128, F), w_down=(E, F, 128)).items()}
+    t["x"][:, 77] = 1.0
+    e = E // 2
+    t["w_gate"][:, 77], t["w_up"][:, 77] = torch.randn(E, F, generator=g), torch.randn(E, F, generator=g)
+    G, Uu = t["w_gate"][e, 77].double(), t["w_up"][e, 77].double()
+    A = G * torch.sigmoid(G) * Uu / E
+    wd = _cancelling_down(A, g)
+    t["w_down"][e] = wd
+    t = {k: v.cuda() for k, v in t.items()}
+    t.update(bias=None, shared=None)
+    y = _forward(_runner(N, t, E), t).cpu().double()
+    ref, tol = A @ wd, 2.0 ** -8 * (A @ wd).abs() + 1.01 * 12 * U * (A.abs() @ wd.abs())
+    worst = ((y - ref).abs() / tol).max().item()
+    print(f"[decode] worst err/tol {worst:.3f}", flush=True)
+    assert worst <= 1.0
