@@ -702,21 +702,17 @@ struct Shape {
 // G and U sums, a workgroup having one matrix's columns and part of its
 // contraction: gu [part][2][slot][F], sgu [part][2][token][Fs].  ROUTE: the
 // workgroup finds topk and gates itself (one of the shared expert needs none), the
-// first of the routed experts writes them.  The first workgroup clears the
-// n_arrived counters of k_decode_down_all.
+// first of the routed experts writes them.
 template <typename T, int MTMAX, bool ROUTE>
 __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up(XRows<T> x, const T* __restrict__ wg,
                                                            const T* __restrict__ wu, const T* __restrict__ swg,
                                                            const T* __restrict__ swu, int32_t* __restrict__ topk_out,
                                                            float* __restrict__ gates, Route<T> route,
-                                                           int32_t* __restrict__ arrived, int n_arrived,
                                                            float* __restrict__ gu, float* __restrict__ sgu, Shape q) {
   __shared__ Chosen chosen;
   __shared__ int rows[kTok];
   __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
   const int32_t* topk = topk_out;
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
   const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
   const int schunks = (q.Fs + kCols<T> - 1) / kCols<T>, shared = 2 * q.gu_parts * schunks;
   if constexpr (ROUTE) {
@@ -762,13 +758,10 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_gate_up_act(XRows<T> x, const
                                                                const T* __restrict__ swu,
                                                                const int32_t* __restrict__ topk,
                                                                const float* __restrict__ gates,
-                                                               int32_t* __restrict__ arrived, int n_arrived,
                                                                T* __restrict__ act, T* __restrict__ sact, Shape q) {
   __shared__ Chosen chosen;
   __shared__ int rows[kTok];
   __shared__ __attribute__((aligned(16))) float red[kWaves * 16 * kCols<T> / 2];
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < n_arrived; i += kNT) arrived[i] = 0;
   const int chunks = (q.F + kCols<T> - 1) / kCols<T>;
   const int shared = (q.Fs + kCols<T> - 1) / kCols<T>;
   int b = int(blockIdx.x) - shared;
@@ -910,9 +903,10 @@ template <typename T> struct Rows<T, false> {
 // where a token did not choose the panel's expert, so that the sum over the
 // experts is part of the contraction.  All panels of the chosen experts (and of
 // the shared one) are dealt evenly to the waves of dn_parts workgroups; yp
-// [part][token][H].  With `arrived` (one counter per column strip, zero) the
-// strip's last workgroup adds the parts up and writes y, else k_decode_combine
-// does.
+// [part][token][H], added up by a launch of its own: the strip's last workgroup
+// could do it, but the fence that each of its waves needs first costs more (one
+// token, H 512, F 1024, 8 experts: 18.5 us so, 17.7 with the launch; float32 20.7
+// and 18.1).
 template <typename T, int S, bool FUSED>
 __device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __restrict__ wd,
                                          const T* __restrict__ swd, const Shape& q, int64_t col0, const int* expert,
@@ -970,7 +964,6 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down_all(Rows<T, FUSED> in, c
                                                             const T* __restrict__ swd,
                                                             const int32_t* __restrict__ topk,
                                                             const float* __restrict__ gates, float* __restrict__ yp,
-                                                            int32_t* __restrict__ arrived, T* __restrict__ y,
                                                             Shape q) {
   constexpr int SL = 16 * MOE_MAX_TOPK;
   __shared__ int expert[SL];
@@ -1021,30 +1014,6 @@ __global__ __launch_bounds__(kNT, 2) void k_decode_down_all(Rows<T, FUSED> in, c
     down_all<T, 2, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
   else
     down_all<T, 1, FUSED>(in, wd, swd, q, col0, expert, slot, gate, active, part, yp, red);
-  if (arrived == nullptr) return;
-  // Every thread's part is in memory before the count says so, and the last
-  // workgroup reads the parts only after it has counted all of them.  The fence
-  // stands before the barrier, in every wave: the barrier waits for no store, and
-  // a fence behind it would wait for those of thread 0's wave alone.
-  __threadfence();
-  __syncthreads();
-  if (t == 0) counts[0] = atomicAdd(&arrived[blockIdx.x % chunks], 1) == q.dn_parts - 1;
-  __syncthreads();
-  if (!counts[0]) return;
-  __threadfence();
-  const int64_t h = col0 + t;
-  if (t >= kCols<T> || h >= q.H) return;
-  for (int n = 0; n < q.N; ++n) {
-    float v = 0.f;
-    for (int s0 = 0; s0 < q.dn_parts; s0 += 16) {
-      float p[16];
-#pragma unroll
-      for (int s = 0; s < 16; ++s) p[s] = s0 + s < q.dn_parts ? yp[(int64_t(s0 + s) * q.N + n) * q.H + h] : 0.f;
-#pragma unroll
-      for (int s = 0; s < 16; ++s) v += p[s];
-    }
-    y[n * int64_t(q.H) + h] = Elt<T>::from_f32(v);
-  }
 }
 
 // y[n] = sum over the parts of a token's `per` rows (+ the shared expert's
@@ -1085,9 +1054,8 @@ struct Plan {
   bool few;    // at most 16 tokens: k_decode_down_all
   bool joint;  // k_decode_gate_up_act; else k_decode_gate_up, and then
   bool route;  // ... which finds topk itself, and with logit_parts == 0 the logits too
-  bool last;   // the last workgroups of k_decode_down_all write y
   bool fused;  // k_decode_down_all forms the activations itself, else k_decode_act does
-  size_t logits, xp, arrived, gu, sgu, act, sact, ysp, sysp, bytes;
+  size_t logits, xp, gu, sgu, act, sact, ysp, sysp, bytes;
 };
 
 constexpr int64_t kCUs = 256;
@@ -1184,7 +1152,6 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
     const int64_t longer = q.dn_parts * ((Fs + d.F - 1) / d.F), most = std::max<int64_t>(kCUs / chunks, 1);
     q.sdn_parts = int(std::min({Fs / (32 * kWaves), longer, most}));
   }
-  p.last = d.N == 1 && chunks * q.dn_parts <= 64;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -1193,7 +1160,6 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
   };
   p.logits = take(size_t(p.logit_parts) * d.N * d.E * sizeof(double));
   p.xp = take(size_t(d.N) * d.H * sizeof(T));
-  p.arrived = take(size_t(chunks) * sizeof(int32_t));
   p.gu = take(p.joint ? 0 : size_t(q.gu_parts) * 2 * NK * d.F * 4);
   p.sgu = take(p.joint ? 0 : size_t(q.gu_parts) * 2 * d.N * Fs * 4);
   constexpr size_t act = sizeof(T) == 2 ? 3 * sizeof(T) : sizeof(T);  // bytes of an activation: Panel<T, S>::A2
@@ -1233,8 +1199,6 @@ hipError_t decode_experts(const Plan& p, const Args<T>& a, hipStream_t s) {
   T* sact = reinterpret_cast<T*>(a.ws + p.sact);
   float* ysp = reinterpret_cast<float*>(a.ws + p.ysp);
   float* sysp = reinterpret_cast<float*>(a.ws + p.sysp);
-  int32_t* arrived = p.last ? reinterpret_cast<int32_t*>(a.ws + p.arrived) : nullptr;
-  const int n_arrived = p.last ? int(chunks) : 0;
   const T* xp = reinterpret_cast<const T*>(a.ws + p.xp);
   const XRows<T> x = p.logit_parts > 0 ? XRows<T>{xp, 32, 32 * q.N} : XRows<T>{a.x, q.H, 32};
   const Route<T> route{a.x, a.w_r, p.logit_parts > 0 ? reinterpret_cast<const double*>(a.ws + p.logits) : nullptr,
@@ -1242,18 +1206,18 @@ hipError_t decode_experts(const Plan& p, const Args<T>& a, hipStream_t s) {
   const unsigned strips = 2 * (unsigned(q.units) * ((q.F + cols - 1) / cols) + (q.Fs + cols - 1) / cols) * q.gu_parts;
   if (p.joint) {
     k_decode_gate_up_act<T, MTMAX><<<dim3(strips / 2), dim3(kNT), 0, s>>>(x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates,
-                                                                          arrived, n_arrived, act, sact, q);
+                                                                          act, sact, q);
   } else {
     bool done = false;
     if constexpr (MTMAX == 1)
       if (p.route) {
         k_decode_gate_up<T, 1, true><<<dim3(strips), dim3(kNT), 0, s>>>(x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates,
-                                                                        route, arrived, n_arrived, gu, sgu, q);
+                                                                        route, gu, sgu, q);
         done = true;
       }
     if (!done)
       k_decode_gate_up<T, MTMAX, false><<<dim3(strips), dim3(kNT), 0, s>>>(
-          x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates, route, arrived, n_arrived, gu, sgu, q);
+          x, a.wg, a.wu, a.swg, a.swu, a.topk, a.gates, route, gu, sgu, q);
     MOE_LAUNCHED()
     if (!p.fused) {
       const int64_t groups = (int64_t(q.N) * q.K * q.F + int64_t(q.N) * q.Fs) / 8;
@@ -1266,19 +1230,17 @@ hipError_t decode_experts(const Plan& p, const Args<T>& a, hipStream_t s) {
     const dim3 grid(chunks * q.dn_parts);
     if (p.fused)
       k_decode_down_all<T, true><<<grid, dim3(kNT), 0, s>>>(Rows<T, true>{gu, sgu}, a.wd, a.swd, a.topk, a.gates, ysp,
-                                                            arrived, a.y, q);
+                                                            q);
     else
       k_decode_down_all<T, false><<<grid, dim3(kNT), 0, s>>>(Rows<T, false>{act, sact}, a.wd, a.swd, a.topk, a.gates,
-                                                             ysp, arrived, a.y, q);
+                                                             ysp, q);
   } else {
     k_decode_down<T, MTMAX><<<dim3((q.units * q.dn_parts + q.sdn_parts) * chunks), dim3(kNT), 0, s>>>(
         act, sact, a.wd, a.swd, a.topk, ysp, sysp, q);
   }
-  if (!p.last) {
-    MOE_LAUNCHED()
-    k_decode_combine<T><<<dim3(q.H / 64, q.N), dim3(256), 0, s>>>(ysp, sysp, a.y, q.N, q.H, MTMAX == 1 ? 1 : q.K,
-                                                                  q.dn_parts, MTMAX == 1 ? 0 : q.sdn_parts);
-  }
+  MOE_LAUNCHED()
+  k_decode_combine<T><<<dim3(q.H / 64, q.N), dim3(256), 0, s>>>(ysp, sysp, a.y, q.N, q.H, MTMAX == 1 ? 1 : q.K,
+                                                                q.dn_parts, MTMAX == 1 ? 0 : q.sdn_parts);
   return hipGetLastError();
 }
 
