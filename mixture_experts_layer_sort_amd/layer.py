@@ -366,6 +366,14 @@ def _on(dev: torch.device):
     return torch.cuda.device(dev)
 
 
+def _stream_of(dev: torch.device, stream):
+    """torch's own operations go to ``stream`` as the library's calls do: a stream, a raw handle, or
+    None for the device's current one."""
+    if stream is None or dev.type != "cuda":
+        return _HERE
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream)
+
+
 def _expect(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: torch.device):
     if t.shape != shape or t.dtype != dtype or t.device != dev:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -491,7 +499,8 @@ class MoENormRunner:
             with _on(self.device):
                 L.moe_rms_norm_bwd(self.d, dy, self.h, self.inputs, self.rstd, dh, dx, self.dweight, self.ws, stream)
         else:
-            self.dweight.zero_()
+            with _stream_of(self.device, stream):
+                self.dweight.zero_()
         return dx, self.dweight
 
 

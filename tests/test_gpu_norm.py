@@ -353,3 +353,32 @@ def test_serving_step_norm_decode():
             assert torch.equal(a, b)
         check_forward(n2.h, w, n2.y, n2.rstd)
         assert torch.equal(n2.h, (dec.y.float() + n1.h.float()).bfloat16())
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_no_rows_clear_dweight_on_the_given_stream(raw):
+    """A step without rows behind a step with rows, both on a stream that is still busy: its
+    gradient is zero there, also when the handle is passed."""
+    from mixture_experts_layer_sort_amd import MoENormRunner
+    x, _, w, dy, _ = _make(64, 512, torch.float32, seed=12)
+    r = MoENormRunner(64, 512, torch.float32, "cuda", eps=EPS)
+    r.forward(x, w)
+    want = r.backward(dy)[1].clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s = side.cuda_stream if raw else side
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)               # some milliseconds of a waiting kernel
+    r.forward(x, w, stream=s)
+    r.backward(dy, stream=s)
+    with torch.cuda.stream(side):
+        first = r.dweight.clone()
+    r.forward(x[:0], w, stream=s)
+    dx, dw = r.backward(dy[:0], stream=s)
+    side.synchronize()
+    assert dx.shape == (0, 512) and torch.equal(first, want) and (dw == 0).all()
+    if not raw:
+        return
+    r.backward(dy[:0], stream=0)                    # the null stream's handle
+    torch.cuda.synchronize()
+    assert (r.dweight == 0).all()
