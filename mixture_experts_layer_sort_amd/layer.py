@@ -426,12 +426,12 @@ class MoEDecodeRunner:
             _expect("shared w_gate", sg, (H, Fs), dt, dev)
             _expect("shared w_up", su, (H, Fs), dt, dev)
             _expect("shared w_down", sd, (Fs, H), dt, dev)
-        if n != self.y.shape[0]:
-            self.topk, self.gates, self.y = self._topk[:n], self._gates[:n], self._y[:n]
         d, ds = self._dims[n]
         if n:
             with _on(dev):
                 L.moe_decode(d, x, w_r, bias, w_gate, w_up, w_down, ds, sg, su, sd, *self._at, self.ws, stream)
+        if n != self.y.shape[0]:  # not before the call: a refused one changes nothing
+            self.topk, self.gates, self.y = self._topk[:n], self._gates[:n], self._y[:n]
         return self.y
 
 
@@ -469,16 +469,16 @@ class MoENormRunner:
         _expect("weight", weight, (self.H,), self.dtype, self.device)
         if residual is not None:
             _expect("residual", residual, (n, self.H), self.dtype, self.device)
-        if n != self.d.N:
-            self.d = L.dims(n, self.H, 128, 1, 1, L.dtype_code(self.dtype))
-        if n != self.y.shape[0]:
-            self.y, self.rstd = self._y[:n], self._rstd[:n]
-        h = None if residual is None else (self._h if n == self.N else self._h[:n])
-        self.h = x if h is None else h
+        d = self.d if n == self.d.N else L.dims(n, self.H, 128, 1, 1, L.dtype_code(self.dtype))
         if n:
             with _on(self.device):
                 h_at, y_at, rstd_at = self._at
-                L.moe_rms_norm(self.d, x, residual, weight, self.eps, None if h is None else h_at, y_at, rstd_at, stream)
+                L.moe_rms_norm(d, x, residual, weight, self.eps, None if residual is None else h_at, y_at, rstd_at, stream)
+        # not before the call: behind a refused one, backward() is still that of the last forward
+        self.d = d
+        if n != self.y.shape[0]:
+            self.y, self.rstd = self._y[:n], self._rstd[:n]
+        self.h = x if residual is None else self._h if n == self.N else self._h[:n]
         self.inputs = weight
         return self.y
 

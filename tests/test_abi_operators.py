@@ -239,3 +239,20 @@ def test_python_entries_check_their_arguments(lib):
                 dict(grads=[x], max_norm=1.0, out=[torch.zeros(2)]), dict(grads=[x.double()], max_norm=1.0)):
         with pytest.raises(ValueError):
             M.moe_clip_grads(**bad)
+
+
+def test_refused_calls_leave_the_runners_as_they_were(lib):
+    """The host tensors are refused where their addresses are taken, behind the checks of shapes."""
+    import mixture_experts_layer_sort_amd as M
+    n = M.MoENormRunner(4, 128, torch.float32, "cpu")
+    before = n.d, n.h, n.y, n.rstd, n.inputs
+    for residual in (None, torch.zeros(3, 128)):
+        with pytest.raises(ValueError):
+            n.forward(torch.zeros(3, 128), torch.zeros(128), residual=residual)
+        assert all(a is b for a, b in zip(before, (n.d, n.h, n.y, n.rstd, n.inputs)))
+    r = M.MoEDecodeRunner(4, 128, 256, 4, 2, torch.float32, "cpu")
+    before = r.topk, r.gates, r.y
+    wg, wd = torch.zeros(4, 128, 256), torch.zeros(4, 256, 128)
+    with pytest.raises(ValueError):
+        r.forward(torch.zeros(3, 128), torch.zeros(128, 4), wg, wg, wd)
+    assert all(a is b for a, b in zip(before, (r.topk, r.gates, r.y)))

@@ -382,3 +382,18 @@ def test_no_rows_clear_dweight_on_the_given_stream(raw):
     r.backward(dy[:0], stream=0)                    # the null stream's handle
     torch.cuda.synchronize()
     assert (r.dweight == 0).all()
+
+
+def test_backward_behind_a_refused_forward_is_the_last_ones():
+    from mixture_experts_layer_sort_amd import MoEError, MoENormRunner
+    x, res, w, dy, dh = _make(8, 256, torch.bfloat16, seed=13)
+    r = MoENormRunner(8, 256, torch.bfloat16, "cuda", eps=EPS)
+    r.forward(x, w, residual=res)
+    want = [t.clone() for t in r.backward(dy, dh=dh)]
+    odd = torch.zeros(8 * 256 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(8, 256)
+    for bad in (odd, odd[:5], r.y):                 # misaligned; on the output
+        with pytest.raises(MoEError):
+            r.forward(bad, w)
+    assert r.y.shape == (8, 256)
+    for a, b in zip(want, r.backward(dy, dh=dh)):
+        assert torch.equal(a, b)
