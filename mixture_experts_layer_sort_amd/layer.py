@@ -504,6 +504,13 @@ class MoENormRunner:
         return dx, self.dweight
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t as the library takes it, contiguous and aligned to 16 bytes: itself, or a copy (autograd hands
+    on gradients that are views at any element, behind a concatenation for one)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 class MoERMSNormFunction(torch.autograd.Function):
     """(y, h) of x and a residual, or y of x alone, with gradients for x, the
     weight and the residual."""
@@ -514,15 +521,14 @@ class MoERMSNormFunction(torch.autograd.Function):
         _expect("weight", weight, (H,), x.dtype, x.device)
         if residual is not None:
             _expect("residual", residual, x.shape, x.dtype, x.device)
-        x = x.contiguous()
+        x = _dense(x)
         d = L.dims(x.numel() // H if H else 0, H, 128, 1, 1, L.dtype_code(x.dtype))
         y = torch.empty_like(x)
         rstd = torch.empty((d.N,), dtype=torch.float32, device=x.device)
         h = None if residual is None else torch.empty_like(x)
         with _on(x.device):
             if d.N:
-                L.moe_rms_norm(d, x, None if residual is None else residual.contiguous(), weight.contiguous(), eps, h,
-                               y, rstd)
+                L.moe_rms_norm(d, x, None if residual is None else _dense(residual), _dense(weight), eps, h, y, rstd)
         ctx.save_for_backward(x if h is None else h, weight, rstd)
         ctx.d = d
         ctx.set_materialize_grads(False)
@@ -541,8 +547,7 @@ class MoERMSNormFunction(torch.autograd.Function):
         if d.N:
             ws = torch.empty((L.moe_workspace_bytes(d, L.MOE_ENTRY_RMS_NORM_BWD),), dtype=torch.uint8, device=h.device)
             with _on(h.device):
-                L.moe_rms_norm_bwd(d, dy.contiguous(), h, weight.contiguous(), rstd,
-                                   None if dh is None else dh.contiguous(), dx, dw, ws)
+                L.moe_rms_norm_bwd(d, _dense(dy), h, _dense(weight), rstd, None if dh is None else _dense(dh), dx, dw, ws)
         return dx, dw.to(weight.dtype), dx if ctx.needs_input_grad[2] else None, None
 
 

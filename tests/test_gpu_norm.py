@@ -397,3 +397,26 @@ def test_backward_behind_a_refused_forward_is_the_last_ones():
     assert r.y.shape == (8, 256)
     for a, b in zip(want, r.backward(dy, dh=dh)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_autograd_function_takes_views_at_any_element(dtype):
+    """Inputs and gradients that start at odd elements give the same bits as aligned ones."""
+    from mixture_experts_layer_sort_amd import moe_rms_norm
+    x, res, w, dy, dh = _make(6, 256, dtype, seed=14)
+
+    def run(move, through):
+        leaves = [t.clone().requires_grad_() for t in (x, res, w)]
+        y, h = moe_rms_norm(*(move(t) for t in (leaves[0], leaves[2], leaves[1])), eps=EPS)
+        return (y.detach(), h.detach(), *torch.autograd.grad([through(y), through(h)], leaves, [move(dy), move(dh)]))
+
+    def odd(t):                                     # the same values, one element behind the start
+        return torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)
+
+    want = run(lambda t: t, lambda t: t)
+    assert odd(x).is_contiguous() and odd(x).data_ptr() % 16
+    for a, b in zip(want, run(odd, lambda t: t)):
+        assert torch.equal(a, b)
+    # the gradient of the cat's second part starts behind its first
+    for a, b in zip(want, run(lambda t: t, lambda t: torch.cat([t.new_zeros(3), t.flatten()])[3:].view(t.shape))):
+        assert torch.equal(a, b)
