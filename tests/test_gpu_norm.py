@@ -420,3 +420,22 @@ def test_autograd_function_takes_views_at_any_element(dtype):
     # the gradient of the cat's second part starts behind its first
     for a, b in zip(want, run(lambda t: t, lambda t: torch.cat([t.new_zeros(3), t.flatten()])[3:].view(t.shape))):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 12, 1600])
+@pytest.mark.parametrize("used", ["y", "y and h"])
+def test_autograd_function_weight_gradient(dtype, N, used):
+    """The weight's gradient in the weight's type against float64: dweight's own bound, as
+    check_backward has it, and one rounding to the type."""
+    from mixture_experts_layer_sort_amd import moe_rms_norm
+    x, res, w, dy, dh = _make(N, 640, dtype, seed=15 + N)
+    leaves = [t.clone().requires_grad_() for t in (x, res, w)]
+    y, h = moe_rms_norm(leaves[0], leaves[2], residual=leaves[1], eps=EPS)
+    torch.autograd.backward([y] if used == "y" else [y, h], [dy] if used == "y" else [dy, dh])
+    hd, g = h.detach().double(), dy.double()
+    terms = g * hd * (hd.square().mean(1, keepdim=True) + EPS).rsqrt()
+    ref, own = terms.sum(0), (-(-N // 512) + 12 + 34) * U * terms.abs().sum(0)
+    got = leaves[2].grad
+    assert got.dtype == dtype and got.shape == (640,)
+    assert ((got.double() - ref).abs() <= own + _s(dtype) * (ref.abs() + own)).all()
