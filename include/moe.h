@@ -506,7 +506,9 @@ int moe_decode(const moe_dims* d, const void* x, const void* w_r, const float* l
  *   x, residual [N,H] act; residual and h are both set or both NULL; h [N,H]
  *   out, may be x or residual itself; weight [H] act; eps finite and > 0;
  *   y [N,H] out, overlapping no other argument; rstd [N] f32 out or NULL.
- * Squares are summed in float32: rows with |h| above 1.8e19 overflow.
+ * A row's squares are summed in float32: where its 2-norm passes 1.84e19 (the
+ * root of the largest float32; |h| = 1.84e19 / sqrt(H) in all of the row) the sum
+ * is infinite, rstd is 0 and so is y.
  * Errors: MOE_EINVAL for eps, a null, misaligned or overlapping pointer. */
 int moe_rms_norm(const moe_dims* d, const void* x, const void* residual, const void* weight, float eps, void* h,
                  void* y, float* rstd, hipStream_t stream);

@@ -439,3 +439,20 @@ def test_autograd_function_weight_gradient(dtype, N, used):
     got = leaves[2].grad
     assert got.dtype == dtype and got.shape == (640,)
     assert ((got.double() - ref).abs() <= own + _s(dtype) * (ref.abs() + own)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [128, 7168, 32768])
+def test_rows_around_the_largest_sum_of_squares(H, dtype):
+    """Up to a 2-norm of 2^64 (1.84e19) rows are as good as any; behind it rstd and y are 0."""
+    from mixture_experts_layer_sort_amd import MoENormRunner
+    w = (1 + 0.1 * torch.randn(H, device="cuda")).to(dtype)
+    sign = 1 - 2 * (torch.arange(H, device="cuda") % 2)
+    x = torch.stack([(2.0 ** 64 * c / H ** 0.5 * sign).to(dtype) for c in (0.98, 1.02, 1e-9)])
+    x = torch.cat([x, torch.zeros((1, H), dtype=dtype, device="cuda")])
+    x[3, H - 3] = 0.98 * 2.0 ** 64                  # all of it in one value
+    r = MoENormRunner(4, H, dtype, "cuda", eps=EPS, backward=False)
+    y = r.forward(x, w)
+    keep = [0, 2, 3]
+    check_forward(x[keep], w, y[keep], r.rstd[keep])
+    assert r.rstd[1] == 0 and (y[1] == 0).all()
