@@ -523,7 +523,9 @@ int moe_rms_norm(const moe_dims* d, const void* x, const void* residual, const v
  *   residual stream), or NULL; dx [N,H] out, may be dy or dh itself;
  *   dweight [H] f32 out, overlapping no other argument.  ws:
  *   MOE_ENTRY_RMS_NORM_BWD (a row of H float32 partial sums per workgroup; any
- *   H up to MOE_NORM_MAX_H). */
+ *   H up to MOE_NORM_MAX_H), overlapping no other argument.
+ * Errors: MOE_EINVAL for a null, misaligned or overlapping pointer;
+ * MOE_EWORKSPACE. */
 int moe_rms_norm_bwd(const moe_dims* d, const void* dy, const void* h, const void* weight, const float* rstd,
                      const void* dh, void* dx, float* dweight, void* ws, size_t ws_bytes, hipStream_t stream);
 

@@ -530,8 +530,12 @@ int moe_rms_norm_bwd(const moe_dims* d, const void* dy, const void* h, const voi
   if (overlap(dweight, db, dx, b) || overlap(dweight, db, dy, b) || overlap(dweight, db, h, b) ||
       overlap(dweight, db, weight, wb) || overlap(dweight, db, rstd, rb) || (dh != nullptr && overlap(dweight, db, dh, b)))
     return MOE_EINVAL;
+  const size_t need = D.N == 0 ? 0 : moe_launch::rms_norm_bwd_ws(D);
+  if (overlap(ws, need, dweight, db) || overlap(ws, need, dx, b) || overlap(ws, need, dy, b) ||
+      overlap(ws, need, h, b) || overlap(ws, need, weight, wb) || overlap(ws, need, rstd, rb) ||
+      (dh != nullptr && overlap(ws, need, dh, b)))
+    return MOE_EINVAL;
   if (D.N == 0) return MOE_OK;
-  const size_t need = moe_launch::rms_norm_bwd_ws(D);
   if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;
   return from_hip(moe_launch::rms_norm_bwd(D, dy, h, weight, rstd, dh, dx, dweight, ws, stream));
 }

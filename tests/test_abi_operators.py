@@ -256,3 +256,12 @@ def test_refused_calls_leave_the_runners_as_they_were(lib):
     with pytest.raises(ValueError):
         r.forward(torch.zeros(3, 128), torch.zeros(128, 4), wg, wg, wd)
     assert all(a is b for a, b in zip(before, (r.topk, r.gates, r.y)))
+
+
+def test_norm_backward_refuses_a_workspace_on_other_arguments(lib):
+    d = D(N=40)                                                  # ten workgroups' partial sums
+    need = L.moe_workspace_bytes(d, L.MOE_ENTRY_RMS_NORM_BWD)
+    for other in (1, 2, 3, 4, 5, 6, 7):
+        assert norm_bwd(d, ws=at(other)) == L.MOE_EINVAL, other
+        assert norm_bwd(d, ws=at(other) - need + 16) == L.MOE_EINVAL, other      # its end on the argument
+    assert norm_bwd(D(N=0), ws=at(7), nb=0) == L.MOE_OK          # no byte of it is used
