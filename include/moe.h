@@ -551,10 +551,10 @@ typedef struct moe_grad {
  * (never read back by the library), squares summed in float64 in a fixed
  * order.  list: count tensors, HOST memory, read during the call only (a
  * captured graph keeps its own copy).  count = 0 gives 0.  Tensors may overlap
- * or repeat; each occurrence counts.
+ * or repeat; each occurrence counts.  norm, ws and the tensors lie apart.
  * Errors: MOE_EINVAL for count < 0, a null list, n < 0, an unknown dtype (or
- * MOE_EUNSUPPORTED for a longer list or more than 2^44 elements in all), a null
- * or misaligned pointer; MOE_EWORKSPACE. */
+ * MOE_EUNSUPPORTED for a longer list or more than 2^44 elements in all), a null,
+ * misaligned or overlapping pointer; MOE_EWORKSPACE. */
 int moe_grad_norm(const moe_grad* list, int64_t count, float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Clipping by the global norm: norm[0] as moe_grad_norm, then for every tensor

@@ -545,6 +545,11 @@ int moe_grad_norm(const moe_grad* list, int64_t count, float* norm, void* ws, si
   if (st != MOE_OK) return st;
   if (norm == nullptr || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0) return MOE_EINVAL;
   if (ws == nullptr || ws_bytes < MOE_GRAD_WS_BYTES || !aligned16(ws)) return MOE_EWORKSPACE;
+  if (overlap(norm, sizeof(float), ws, MOE_GRAD_WS_BYTES)) return MOE_EINVAL;
+  for (int64_t t = 0; t < count; ++t) {
+    const size_t n = size_t(list[t].n) * (list[t].in_dtype == MOE_BF16 ? 2 : 4);
+    if (overlap(list[t].in, n, norm, sizeof(float)) || overlap(list[t].in, n, ws, MOE_GRAD_WS_BYTES)) return MOE_EINVAL;
+  }
   return from_hip(moe_launch::grad_norm(list, int(count), norm, ws, stream));
 }
 

@@ -265,3 +265,19 @@ def test_norm_backward_refuses_a_workspace_on_other_arguments(lib):
         assert norm_bwd(d, ws=at(other)) == L.MOE_EINVAL, other
         assert norm_bwd(d, ws=at(other) - need + 16) == L.MOE_EINVAL, other      # its end on the argument
     assert norm_bwd(D(N=0), ws=at(7), nb=0) == L.MOE_OK          # no byte of it is used
+
+
+def test_grad_norm_refuses_a_norm_or_workspace_on_its_tensors(lib):
+    ok = (at(1), at(2), 100, F32, F32)
+    for rows, kw in (
+        ([ok, (at(101), None, 100, F32, F32)], {}),                      # a tensor inside the workspace
+        ([(at(101) - 400 + 4, None, 100, F32, F32)], {}),                # its end
+        ([(at(101) + L.MOE_GRAD_WS_BYTES - 2, None, 9, BF16, F32)], {}),  # its start
+        ([ok, (at(100), None, 1, F32, F32)], {}),                        # a tensor on norm
+        ([(at(100) - 8, None, 5, BF16, F32)], {}),
+        ([ok], dict(norm=at(101) + 64)),                                 # norm inside the workspace
+        ([], dict(norm=at(101))),
+    ):
+        assert clip(rows, entry="moe_grad_norm", **kw) == L.MOE_EINVAL, rows
+    # an empty tensor may point anywhere
+    assert clip([(at(101), None, 0, F32, F32)], entry="moe_grad_norm", nb=0) == L.MOE_EWORKSPACE
