@@ -553,8 +553,9 @@ typedef struct moe_grad {
  * captured graph keeps its own copy).  count = 0 gives 0.  Tensors may overlap
  * or repeat; each occurrence counts.  norm, ws and the tensors lie apart.
  * Errors: MOE_EINVAL for count < 0, a null list, n < 0, an unknown dtype (or
- * MOE_EUNSUPPORTED for a longer list or more than 2^44 elements in all), a null,
- * misaligned or overlapping pointer; MOE_EWORKSPACE. */
+ * MOE_EUNSUPPORTED for a longer list, or more than 2^43 elements in all, each
+ * tensor's number rounded up to 4096), a null, misaligned or overlapping pointer;
+ * MOE_EWORKSPACE. */
 int moe_grad_norm(const moe_grad* list, int64_t count, float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Clipping by the global norm: norm[0] as moe_grad_norm, then for every tensor

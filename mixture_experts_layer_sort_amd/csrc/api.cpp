@@ -83,7 +83,9 @@ int check_decode(const moe_dims* d, const moe_dims* ds, Dims* D, int64_t* Fs) {
 int check_grads(const moe_grad* g, int64_t count, bool out) {
   if (count < 0 || (count > 0 && g == nullptr)) return MOE_EINVAL;
   if (count > MOE_GRAD_MAX_TENSORS) return MOE_EUNSUPPORTED;
-  int64_t total = 0;
+  // a launch counts chunks in uint32, and steps by its workgroups (2^20 at most) past the last one
+  const int64_t chunk = moe_launch::grad_chunk(), most = int64_t(1) << 31;
+  int64_t chunks = 0;
   for (int64_t t = 0; t < count; ++t) {
     const moe_grad& q = g[t];
     if (q.n < 0) return MOE_EINVAL;
@@ -93,9 +95,9 @@ int check_grads(const moe_grad* g, int64_t count, bool out) {
     const uintptr_t ie = q.in_dtype == MOE_BF16 ? 1 : 3, oe = q.out_dtype == MOE_BF16 ? 1 : 3;
     if (q.in == nullptr || (reinterpret_cast<uintptr_t>(q.in) & ie) != 0) return MOE_EINVAL;
     if (out && (q.out == nullptr || (reinterpret_cast<uintptr_t>(q.out) & oe) != 0)) return MOE_EINVAL;
-    if (q.n > (int64_t(1) << 44)) return MOE_EUNSUPPORTED;
-    total += q.n + moe_launch::grad_chunk();
-    if (total > (int64_t(1) << 44)) return MOE_EUNSUPPORTED;
+    if (q.n > most * chunk) return MOE_EUNSUPPORTED;
+    chunks += (q.n + chunk - 1) / chunk;
+    if (chunks > most) return MOE_EUNSUPPORTED;
   }
   return MOE_OK;
 }

@@ -237,7 +237,7 @@ hipError_t rms_norm_bwd(const Dims& d, const void* dy, const void* h, const void
                         const void* dh, void* dx, float* dw, void* ws, hipStream_t s);
 
 // Global gradient norm and clipping over a checked list in host memory.
-int64_t grad_chunk();  // elements per chunk; a launch counts its chunks in 31 bits
+int64_t grad_chunk();  // elements per chunk; the list has at most 2^31 chunks
 hipError_t grad_norm(const moe_grad* g, int count, float* norm, void* ws, hipStream_t s);
 hipError_t grad_clip(const moe_grad* g, int count, float max_norm, float* norm, void* ws, hipStream_t s);
 }  // namespace moe_launch

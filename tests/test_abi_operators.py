@@ -281,3 +281,14 @@ def test_grad_norm_refuses_a_norm_or_workspace_on_its_tensors(lib):
         assert clip(rows, entry="moe_grad_norm", **kw) == L.MOE_EINVAL, rows
     # an empty tensor may point anywhere
     assert clip([(at(101), None, 0, F32, F32)], entry="moe_grad_norm", nb=0) == L.MOE_EWORKSPACE
+
+
+@pytest.mark.parametrize("entry", ["moe_grad_norm", "moe_grad_clip"])
+def test_grad_lists_have_at_most_two_to_the_31_chunks(lib, entry):
+    """Chunks of 4096 elements; the refusal of a missing norm comes behind the list's own."""
+    one = 1 << 43
+    for sizes, st in (([one], L.MOE_EINVAL), ([one + 1], L.MOE_EUNSUPPORTED), ([one // 2] * 2, L.MOE_EINVAL),
+                      ([one // 2, one // 2 + 1], L.MOE_EUNSUPPORTED), ([one, 1], L.MOE_EUNSUPPORTED),
+                      ([one - 4096, 0, 1], L.MOE_EINVAL), ([one - 4096, 1, 1], L.MOE_EUNSUPPORTED),
+                      ([(1 << 63) - 1], L.MOE_EUNSUPPORTED)):
+        assert clip([(at(1), at(2), n, BF16, BF16) for n in sizes], entry=entry, norm=None) == st, sizes
