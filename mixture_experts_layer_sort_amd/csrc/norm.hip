@@ -244,8 +244,10 @@ __global__ __launch_bounds__(1024) void k_norm_dw(const float* __restrict__ part
 // F<NT, VPT>().  A short row has no more lanes than vectors: a training step of
 // 65536 x 128 bf16 rows takes 32 us so, 55 with a wave a row; of 16384 x 256, 20
 // and 23.5.
-template <typename F>
+template <typename T, typename F>
 hipError_t by_row(int nv, F f) {
+  constexpr int most = MOE_NORM_MAX_H / Vec16<T>::n;  // 4096 in bf16, 8192 in float32
+  static_assert(most <= 8192, "the last case has all longer rows");
   if (nv <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
   if (nv <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
   if (nv <= 64) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>());
@@ -254,8 +256,9 @@ hipError_t by_row(int nv, F f) {
   if (nv <= 512) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
   if (nv <= 1024) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
   if (nv <= 2048) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
-  if (nv <= 4096) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
-  return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 8>());
+  if constexpr (most > 4096)
+    if (nv > 4096) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 8>());
+  return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 4>());
 }
 
 template <typename T>
@@ -266,7 +269,7 @@ bool streams(const moe_launch::Dims& d) {
 template <typename T>
 hipError_t norm_t(const moe_launch::Dims& d, const void* x, const void* residual, const void* weight, float eps,
                   void* h, void* y, float* rstd, hipStream_t s) {
-  return by_row(int(d.H / Vec16<T>::n), [&](auto nt, auto vpt) {
+  return by_row<T>(int(d.H / Vec16<T>::n), [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
     constexpr int RPB = NT < 256 ? 256 / NT : 1;
     const int64_t blocks = std::min<int64_t>((d.N + RPB - 1) / RPB, kNormMaxBlocks);
@@ -290,7 +293,7 @@ hipError_t norm_bwd_t(const moe_launch::Dims& d, const void* dy, const void* h, 
                       const void* dh, void* dx, float* dw, void* ws, hipStream_t s) {
   const int B = norm_bwd_blocks<T>(d);
   float* part = B == 1 ? dw : static_cast<float*>(ws);  // one workgroup's sums are the result
-  hipError_t e = by_row(int(d.H / Vec16<T>::n), [&](auto nt, auto vpt) {
+  hipError_t e = by_row<T>(int(d.H / Vec16<T>::n), [&](auto nt, auto vpt) {
     constexpr int NT = decltype(nt)::value, VPT = decltype(vpt)::value;
     auto* const kernel = streams<T>(d) ? k_norm_bwd<T, NT, VPT, true> : k_norm_bwd<T, NT, VPT, false>;
     kernel<<<dim3(B), dim3(NT < 256 ? 256 : NT), 0, s>>>(
