@@ -485,8 +485,8 @@ size_t moe_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds);
  *   ds: the shared expert's dims {N, H, Fs, 1, 1, dtype}, with its weights
  *   ws_gate, ws_up [H,Fs] and ws_down [Fs,H]; or NULL, with all three NULL.
  *   topk_idx [N,K] int32 out; gates [N,K] f32 out; y [N,H] out.  ws:
- *   moe_decode_workspace_bytes(d, ds).  The outputs, ws and x do not overlap
- *   (MOE_EINVAL), nor the outputs and ws any other argument. */
+ *   moe_decode_workspace_bytes(d, ds).  The outputs and ws overlap neither
+ *   each other nor any input (MOE_EINVAL). */
 int moe_decode(const moe_dims* d, const void* x, const void* w_r, const float* logit_bias, const void* w_gate,
                const void* w_up, const void* w_down, const moe_dims* ds, const void* ws_gate, const void* ws_up,
                const void* ws_down, int32_t* topk_idx, float* gates, void* y, void* ws, size_t ws_bytes,

@@ -484,10 +484,14 @@ int moe_decode(const moe_dims* d, const void* x, const void* w_r, const float* l
                     : (ws_gate != nullptr || ws_up != nullptr || ws_down != nullptr))
     return MOE_EINVAL;
   const size_t need = D.N == 0 ? 0 : moe_launch::decode_ws(D, Fs), nk = size_t(D.N) * size_t(D.K) * 4;
-  const void* const at[] = {x, y, topk_idx, gates, ws};
-  const size_t bytes[] = {row_bytes(D), row_bytes(D), nk, nk, need};
-  for (int i = 0; i < 5; ++i)
-    for (int j = 0; j < i; ++j)
+  // what is written, then what is read: no written one shares a byte with any before or behind it
+  const size_t es = D.dtype == MOE_BF16 ? 2 : 4, h = size_t(D.H) * es;
+  const size_t wb = D.N == 0 ? 0 : size_t(D.E) * size_t(D.F) * h, sb = D.N == 0 ? 0 : size_t(Fs) * h;
+  const size_t rb = D.N == 0 ? 0 : size_t(D.E) * h, bb = logit_bias == nullptr || D.N == 0 ? 0 : size_t(D.E) * 4;
+  const void* const at[] = {y, topk_idx, gates, ws, x, w_r, logit_bias, w_gate, w_up, w_down, ws_gate, ws_up, ws_down};
+  const size_t bytes[] = {row_bytes(D), nk, nk, need, row_bytes(D), rb, bb, wb, wb, wb, sb, sb, sb};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 13; ++j)
       if (overlap(at[i], bytes[i], at[j], bytes[j])) return MOE_EINVAL;
   if (D.N == 0) return MOE_OK;
   if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;

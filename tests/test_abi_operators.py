@@ -292,3 +292,16 @@ def test_grad_lists_have_at_most_two_to_the_31_chunks(lib, entry):
                       ([one - 4096, 0, 1], L.MOE_EINVAL), ([one - 4096, 1, 1], L.MOE_EUNSUPPORTED),
                       ([(1 << 63) - 1], L.MOE_EUNSUPPORTED)):
         assert clip([(at(1), at(2), n, BF16, BF16) for n in sizes], entry=entry, norm=None) == st, sizes
+
+
+def test_decode_outputs_and_workspace_overlap_no_weights(lib):
+    d, ds, s = D(), D(F=384, E=1, K=1), (at(10), at(11), at(12))
+    need = L.moe_decode_workspace_bytes(d, ds)
+    full, shared = 4 * 128 * 256 * 2, 128 * 384 * 2              # bytes of a weight tensor
+    ends = {2: 128 * 4 * 2, 3: full, 4: full, 5: full, 10: shared, 11: shared, 12: shared, 13: 16}
+    for i, n in ends.items():
+        for where in (at(i), at(i) + n - 16):                    # its start, its last bytes
+            for out in ("y", "topk", "gates", "ws"):
+                assert decode(d, ds, s, bias=at(13), nb=need, **{out: where}) == L.MOE_EINVAL, (i, out)
+        assert decode(d, ds, s, bias=at(13), ws=at(i) - need + 16) == L.MOE_EINVAL, i
+    assert decode(D(N=0), D(N=0, F=384, E=1, K=1), s, y=at(3), bias=at(13), ws=at(4), nb=0) == L.MOE_OK
