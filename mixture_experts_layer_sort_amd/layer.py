@@ -138,6 +138,7 @@ class MoELayerRunner:
                 self.dw_down_s = torch.empty((Fs, H), dtype=f32, device=dev)
         self.inputs = None
         self.shared_w = None
+        self.has_grads = False
 
     def _ws(self, entry: int, d=None):
         n = L.moe_workspace_bytes(self.d if d is None else d, entry)
@@ -273,6 +274,7 @@ class MoELayerRunner:
             L.moe_permute_bwd_add(d, self.dxs, self.inv, self.topk, self.dlogits, w_r, self.aux_alpha is not None,
                                   self.dx_s, self.dx, self.perm_ws, main)
         join(main, side)
+        self.has_grads = True
         out = dict(dx=self.dx, dw_r=self.dw_r, dw_gate=self.dw_gate, dw_up=self.dw_up, dw_down=self.dw_down,
                    dgates=self.dgates, dlogits=self.dlogits)
         if self.shared_w is not None:
@@ -286,6 +288,8 @@ class MoELayerRunner:
         tensor [1].  Runs on the current stream."""
         if not self.with_backward:
             raise RuntimeError("runner was built without backward buffers")
+        if not self.has_grads:
+            raise RuntimeError("clip_grads before backward")
         grads = [self.dw_r, self.dw_gate, self.dw_up, self.dw_down]
         if self.shared_ffn is not None:
             grads += [self.dw_gate_s, self.dw_up_s, self.dw_down_s]
