@@ -478,7 +478,9 @@ size_t moe_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds);
  * stored rounded) and y is rounded once, so the two agree within the element
  * type's rounding but not bit for bit, and may choose differently between
  * experts whose logits differ by less than float32 resolves.  NaN logits rank
- * last.  A call's result depends on N (how sums are cut), not on timing.
+ * last.  A call's result depends on N (how sums are cut), not on timing.  NaN and
+ * infinite values of a token or of an expert's weights reach only the tokens
+ * themselves and those that chose the expert, as infinite or NaN outputs.
  *   d: the layer's dims, 0 <= N <= MOE_DECODE_MAX_TOKENS (MOE_EUNSUPPORTED
  *   above); gemm_tiles is ignored.  x [N,H]; w_r [H,E]; logit_bias [E] f32 or
  *   NULL; w_gate, w_up [E,H,F]; w_down [E,F,H].

@@ -180,6 +180,8 @@ __device__ __forceinline__ void rank_pairs(double v, const float* __restrict__ b
     const double* sel = out->sel + p / K * K;
     float sum = 0.f, mine = 0.f;
     for (int k = 0; k < K; ++k) {
+      // the difference of two float64 logits d, rounded to float32 once: 2^-24 |d| of the gate, about
+      // what expf (1 ulp) and the quotient add; the gate itself is a float32
       const float z = expf(float(sel[k] - sel[0]));
       sum += z;
       if (k == p % K) mine = z;
@@ -1077,9 +1079,9 @@ struct Used {
 //    follow those that a CU holds at a time (`fit`).
 //  - part_cost for writing and adding up one part more.
 // It is the mean over the expected number of experts and a tenth more and less, as
-// the fullest CU's count jumps.  Over 54 sizes the cut so found cost 0.3 % more than
-// the best one of each on average, 4 % at most; the fullest CU alone, without the
-// other terms, 2 % and 15 %.  Strips of other widths would even the CUs out better,
+// the fullest CU's count jumps.  Over 54 sizes the cut so found cost 0.5 % more than
+// the best one of each on average, 5 % at most (profiles/decode_cut_sweep.md); the
+// fullest CU alone, without the other terms, 2 % and 15 %.  Strips of other widths would even the CUs out better,
 // but a row segment that is not 256 bytes, aligned, reads a third slower.
 struct Cut {
   int parts;
