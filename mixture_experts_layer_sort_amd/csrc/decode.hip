@@ -907,8 +907,8 @@ template <typename T> struct Rows<T, false> {
 // the shared one) are dealt evenly to the waves of dn_parts workgroups; yp
 // [part][token][H], added up by a launch of its own: the strip's last workgroup
 // could do it, but the fence that each of its waves needs first costs more (one
-// token, H 512, F 1024, 8 experts: 18.5 us so, 17.7 with the launch; float32 20.7
-// and 18.1).
+// token, H 512, F 1024, 8 experts: 18.5 us so, 17.9 with the launch; float32 20.7
+// and 18.4).
 template <typename T, int S, bool FUSED>
 __device__ __forceinline__ void down_all(const Rows<T, FUSED>& in, const T* __restrict__ wd,
                                          const T* __restrict__ swd, const Shape& q, int64_t col0, const int* expert,
@@ -1123,21 +1123,21 @@ Plan plan_t(const moe_launch::Dims& d, int64_t Fs) {
                         p.few ? 3.0 + 3.0 * row_elements : 0.5 + 0.5 * row_elements);
   // Both matrices in one workgroup spare the sums of G and U their way through memory, and the
   // workgroups that load them the activations, but leave half as many strips to spread.  20 tokens
-  // of 8 experts (H 4096, F 14336): 448 us so, 455 apart; 64 of them 461 and 496; 16 tokens of 16
-  // experts (H 2048, F 6400): 220 and 227; 64 tokens of 64 experts (H 2048, F 1408): 239 and 232;
-  // with two rows an expert (8 tokens of 8 experts) 422 and 416; 12 tokens of 10 experts (H 640,
-  // F 7168, K 8) 84 and 78.
+  // of 8 experts (H 4096, F 14336): 431 us so, 440 apart; 64 of them 483 and 509; 16 tokens of 16
+  // experts (H 2048, F 6400): 222 and 228; 64 tokens of 64 experts (H 2048, F 1408): 209 and 207;
+  // with two rows an expert (8 tokens of 8 experts) 424 and 416; 12 tokens of 10 experts (H 640,
+  // F 7168, K 8) 85 and 78.
   const Cut both = cut(used, double(fchunks), double(schunks), d.H / 16, 1, fit, 0.0);
   p.joint = NK >= 4 * q.units && both.us <= (p.few ? 1.08 * apart.us : 1.05 * apart.us + 0.9 * row_elements);
   q.gu_parts = p.joint ? 1 : apart.parts;
   p.fused = p.few && !p.joint && d.N * q.gu_parts <= 32;
   // Each workgroup of gate/up ranks the pairs (token, expert) for itself while there is one a
-  // thread at most: 1 to 4 us less than with a launch for it (4 tokens, 16 experts: 35.9
-  // against 37.5; 4 tokens, 64 experts: 88 against 90), but with two pairs a thread 123 against
+  // thread at most: 1 to 4 us less than with a launch for it (4 tokens, 16 experts: 27.2
+  // against 28.9; 4 tokens, 64 experts: 76 against 78), but with two pairs a thread 123 against
   // 122 (8 tokens, 64 experts), with four 164 against 160.
   p.route = p.few && !p.joint && d.N * d.E <= kPairs;
-  // The logits too where the router is a few panels (17.5 us against 19.8 with the logits'
-  // launch at one token, H 512 and 8 experts, 23.4 against 25.1 at three; 37.6 against 35.9 at
+  // The logits too where the router is a few panels (18.3 us against 20.3 with the logits'
+  // launch at one token, H 512 and 8 experts, 23.4 against 25.0 at three; 27.4 against 27.1 at
   // four tokens, H 1024 and 16 experts).
   const bool small_router = (d.E + 15) / 16 * (d.H / 32) <= 4 * kWaves;
   p.logit_parts = p.route && small_router ? 0 : int((d.H + kLogitRows - 1) / kLogitRows);
