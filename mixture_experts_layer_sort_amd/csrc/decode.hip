@@ -1080,8 +1080,8 @@ struct Used {
 //  - part_cost for writing and adding up one part more.
 // It is the mean over the expected number of experts and a tenth more and less, as
 // the fullest CU's count jumps.  Over 54 sizes the cut so found cost 0.5 % more than
-// the best one of each on average, 5 % at most (profiles/decode_cut_sweep.md); the
-// fullest CU alone, without the other terms, 2 % and 15 %.  Strips of other widths would even the CUs out better,
+// the best one of each on average, 5 % at most; the fullest CU alone, without the
+// other terms, 2 % and 15 %.  Strips of other widths would even the CUs out better,
 // but a row segment that is not 256 bytes, aligned, reads a third slower.
 struct Cut {
   int parts;
