@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 10
+#define MOE_ABI_VERSION 11
 /* Rows per tile of the grouped-GEMM tile list built by moe_permute_meta. */
 #define MOE_TILE_M 256
 #define MOE_MAX_EXPERTS 256
@@ -570,6 +570,145 @@ int moe_grad_norm(const moe_grad* list, int64_t count, float* norm, void* ws, si
  *   another output (MOE_EINVAL), nor norm and ws. */
 int moe_grad_clip(const moe_grad* list, int64_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
                   hipStream_t stream);
+
+/* --------------------------------------------- 4-bit values (microscaled) */
+/* A tensor in microscaled 4-bit floating point (the OCP Microscaling Formats
+ * specification, MXFP4): blocks of 32 values along the contraction axis share
+ * a power of two,
+ *   s = max(floor(log2(max |v|)) - 2, -127)   (0 in all of a block: -127),
+ *   q = v / 2^s rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a
+ *       sign (ties to the even code, more than 6 to 6),
+ * and q * 2^s stands for v: off by 2^s at most, or by 2 * 2^s where |v| > 6 * 2^s.
+ * A block with an infinite or NaN value becomes NaN as a whole.  A code has
+ * 4 bits (bit 3 the sign, bits 2..0 the magnitude's place in the list above),
+ * two to a byte, the even contraction index in the low half; a scale is the
+ * byte s + 127, 255 for NaN.  Quantising the values that a tensor stands for
+ * gives the same values again.
+ *
+ * Two orders, both with the contraction length k a multiple of 128:
+ *  MOE_MX4_WEIGHTS  count matrices [k, cols], cols a multiple of 128, in the
+ *    order in which the matrix instructions take them:
+ *      codes [count][cols/16][k/128][(k/32)%4][cols%16][16 bytes of 32 k]
+ *      scales [count][cols/16][ceil(k/512)][(k/32)%4][cols%16][(k/128)%4].
+ *    A strip of 16 columns is one piece of memory.
+ *  MOE_MX4_ROWS  count rows of k values (cols = 1):
+ *      codes [count][k/2 bytes]
+ *      scales [count][ceil(k/512)][(k/32)%4][(k/128)%4].
+ * Scales of k that a last group of 512 does not have are 0. */
+typedef enum moe_mx4_order { MOE_MX4_WEIGHTS = 0, MOE_MX4_ROWS = 1 } moe_mx4_order;
+
+/* Device pointers to the codes and scales of one tensor, aligned to 16 bytes. */
+typedef struct moe_mx4 {
+  void* codes;
+  void* scales;
+} moe_mx4;
+
+/* Bytes of the codes and of the scales; (size_t)-1 where moe_mx4_quantize
+ * would refuse the sizes. */
+size_t moe_mx4_code_bytes(int32_t order, int64_t count, int64_t k, int64_t cols);
+size_t moe_mx4_scale_bytes(int32_t order, int64_t count, int64_t k, int64_t cols);
+
+/* v [count, k, cols] (MOE_MX4_WEIGHTS) or [count, k] (MOE_MX4_ROWS), of the
+ * moe_dtype dtype, to codes and scales.  count = 0 enqueues nothing.  Neither
+ * v, the codes nor the scales overlap another of them.
+ * Errors: MOE_EINVAL for an unknown order, count < 0, k or cols <= 0 or not a
+ * multiple of 128 (rows: cols != 1), a null, misaligned or overlapping
+ * pointer; MOE_EUNSUPPORTED for an unknown dtype, k or cols > 2^20, count >=
+ * 2^31 or more than 2^40 values. */
+int moe_mx4_quantize(int32_t order, int64_t count, int64_t k, int64_t cols, int32_t dtype, const void* v,
+                     const moe_mx4* q, hipStream_t stream);
+
+/* The values that codes and scales stand for, to v; exact in both types (but
+ * bfloat16 and float32 values below 2^-126 may come out as 0).  Arguments and
+ * errors as moe_mx4_quantize. */
+int moe_mx4_dequantize(int32_t order, int64_t count, int64_t k, int64_t cols, int32_t dtype, const moe_mx4* q,
+                       void* v, hipStream_t stream);
+
+/* Grouped products of 4-bit rows with 4-bit experts, forward only, products
+ * of codes exact, sums in float32 (the matrix instruction's), one rounding:
+ *   moe_mx4_gate_up: G = xs.W_gate[e], U = xs.W_up[e], act = silu(G) * U with
+ *     xs[i] = x[sorted_flat[i] / K];
+ *   moe_mx4_down:    ys = act.W_down[e].
+ * NaN and infinite values reach only their own row, or the columns of their
+ * expert's rows.
+ *   x: rows [N, H]; act of moe_mx4_down: rows [NK, F]; w_gate, w_up: weights
+ *   [E, H, F]; w_down: weights [E, F, H]; sorted_flat [NK], tiles, num_tiles
+ *   from moe_permute_meta, moe_permute_meta_capacity or moe_route_meta; act
+ *   [NK,F] and ys [NK,H] out, of the type dims->dtype; rows that no tile has
+ *   (dropped ones) are left as they were.  gemm_tiles is ignored.  The output
+ *   overlaps no other argument.
+ * Errors: MOE_EINVAL for a null, misaligned or overlapping pointer. */
+int moe_mx4_gate_up(const moe_dims* d, const moe_mx4* x, const int32_t* sorted_flat, const moe_mx4* w_gate,
+                    const moe_mx4* w_up, const int32_t* tiles, const int32_t* num_tiles, void* act,
+                    hipStream_t stream);
+int moe_mx4_down(const moe_dims* d, const moe_mx4* act, const moe_mx4* w_down, const int32_t* tiles,
+                 const int32_t* num_tiles, void* ys, hipStream_t stream);
+
+/* moe_decode with 4-bit experts (MOE_MX4_WEIGHTS): only the weights are in 4
+ * bits, so a call reads about (chosen experts)*3*H*F*17/32 bytes.  x, W_r and
+ * y have the type dims->dtype; x enters the products with all its bits, the
+ * activations with 16 bits or more (bfloat16 layers) or 24 (float32), every sum is
+ * float32, router logits float64, y is rounded once.  Weights below 2^-126
+ * may count as 0.  Everything else, the shared expert (ds and its weights
+ * [1, H, Fs] and [1, Fs, H]) included, as moe_decode. */
+size_t moe_mx4_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds);
+int moe_mx4_decode(const moe_dims* d, const void* x, const void* w_r, const float* logit_bias, const moe_mx4* w_gate,
+                   const moe_mx4* w_up, const moe_mx4* w_down, const moe_dims* ds, const moe_mx4* ws_gate,
+                   const moe_mx4* ws_up, const moe_mx4* ws_down, int32_t* topk_idx, float* gates, void* y, void* ws,
+                   size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------- balance loss of router logits */
+/* Load-balancing and z loss of given router logits, sequence by sequence, with
+ * padding left out (moe_aux_loss forms its own logits and takes the batch as
+ * one sequence without padding):
+ *   N = B * seq_len tokens; token t counts where mask[t] != 0; n_s of them in
+ *   sequence s, B' sequences with n_s > 0, n tokens in all;
+ *   p_t = softmax(l_t), or sigmoid(l_t) / sum_e sigmoid(l_t,e);
+ *   c_s,e = how often sequence s chose expert e; f_s,e = E c_s,e / (K n_s);
+ *   P_s,e = mean of p_t,e over the sequence's tokens;
+ *   loss = alpha / B' sum_s sum_e f_s,e P_s,e
+ *        + z_coef / n sum_t logsumexp(l_t)^2;
+ *   counts[e] = sum_s c_s,e.
+ * f is a count and carries no gradient.  Without a single counting token the
+ * loss is 0.  Logits of tokens that do not count are not looked at.
+ * Probabilities and their sums over a chunk are float32, the sums over chunks
+ * float64, in a fixed order. */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct moe_balance {
+  int64_t N, E, K, seq_len; /* N a multiple of seq_len; limits of moe_dims */
+  int32_t dtype;            /* of logits and dlogits */
+  int32_t score;            /* moe_score */
+  float alpha, z_coef;      /* finite */
+} moe_balance;
+
+/* Bytes of the state that moe_balance_loss leaves for its backward pass and of
+ * its scratch; (size_t)-1 on invalid sizes. */
+size_t moe_balance_state_bytes(const moe_balance* b);
+size_t moe_balance_workspace_bytes(const moe_balance* b);
+
+/* logits [N,E] of b->dtype; topk_idx [N,K] int32: the chosen experts (values
+ * outside [0,E) count nothing), or NULL: the K experts of largest
+ * logit + logit_bias by (value desc, id asc), NaN last, in float32.
+ * logit_bias [E] f32 or NULL, with topk_idx NULL only; it moves the choice
+ * alone.  mask [N] bytes or NULL (every token counts).
+ *   loss [1] f32 out; counts [E] int32 out; state: moe_balance_state_bytes.
+ * Outputs, state and ws overlap neither each other nor an input.  N == 0
+ * enqueues nothing and leaves the outputs untouched.  Errors: MOE_EINVAL, MOE_EUNSUPPORTED (limits, dtype),
+ * MOE_EWORKSPACE (state or ws). */
+int moe_balance_loss(const moe_balance* b, const void* logits, const int32_t* topk_idx, const float* logit_bias,
+                     const uint8_t* mask, float* loss, int32_t* counts, void* state, size_t state_bytes, void* ws,
+                     size_t ws_bytes, hipStream_t stream);
+
+/* dlogits [N,E] (b->dtype, one rounding) = dloss[0] times the gradient of the
+ * loss: with softmax scores
+ *   alpha / (B' n_s) p_e (f_s,e - sum_i f_s,i p_i) + 2 z_coef / n lse softmax_e,
+ * with sigmoid scores the first term times 1 - sigmoid(l_e); 0 for tokens that
+ * do not count.  dloss [1] f32 on the device, or NULL for 1.  state from
+ * moe_balance_loss with the same b, logits and mask.  dlogits may be logits
+ * itself and overlaps nothing else. */
+int moe_balance_loss_bwd(const moe_balance* b, const void* logits, const uint8_t* mask, const void* state,
+                         const float* dloss, void* dlogits, hipStream_t stream);
 
 /* ------------------------------------------- no-allocation entry point */
 

@@ -29,6 +29,8 @@ MOE_TILE_M = 256
 MOE_DECODE_MAX_TOKENS = 64
 MOE_NORM_MAX_H = 32768
 MOE_GRAD_WS_BYTES, MOE_GRAD_MAX_TENSORS = 8192, 65536
+MOE_MX4_WEIGHTS, MOE_MX4_ROWS = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 # moe_gemm_tiles (moe_dims.gemm_tiles): AUTO, or one bf16 tile family forced on every GEMM stage
 MOE_TILES_AUTO, MOE_TILES_256, MOE_TILES_128X256, MOE_TILES_128 = 0, 1, 2, 3
 
@@ -50,7 +52,18 @@ class moe_grad(ctypes.Structure):
     _fields_ = [("in_", _P), ("out", _P), ("n", _I64), ("in_dtype", _I32), ("out_dtype", _I32)]
 
 
+class moe_mx4(ctypes.Structure):
+    _fields_ = [("codes", _P), ("scales", _P)]
+
+
+class moe_balance(ctypes.Structure):
+    _fields_ = [("N", _I64), ("E", _I64), ("K", _I64), ("seq_len", _I64), ("dtype", _I32), ("score", _I32),
+                ("alpha", _F), ("z_coef", _F)]
+
+
 _DP = ctypes.POINTER(moe_dims)
+_MP = ctypes.POINTER(moe_mx4)
+_BP = ctypes.POINTER(moe_balance)
 _GP = ctypes.POINTER(moe_grad)
 
 SIGNATURES = {
@@ -91,6 +104,18 @@ SIGNATURES = {
     "moe_rms_norm_bwd": (ctypes.c_int, [_DP] + [_P] * 8 + [_SZ, _P]),
     "moe_grad_norm": (ctypes.c_int, [_GP, _I64, _P, _P, _SZ, _P]),
     "moe_grad_clip": (ctypes.c_int, [_GP, _I64, _F, _P, _P, _SZ, _P]),
+    "moe_mx4_code_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
+    "moe_mx4_scale_bytes": (_SZ, [_I32, _I64, _I64, _I64]),
+    "moe_mx4_quantize": (ctypes.c_int, [_I32, _I64, _I64, _I64, _I32, _P, _MP, _P]),
+    "moe_mx4_dequantize": (ctypes.c_int, [_I32, _I64, _I64, _I64, _I32, _MP, _P, _P]),
+    "moe_mx4_gate_up": (ctypes.c_int, [_DP, _MP, _P, _MP, _MP, _P, _P, _P, _P]),
+    "moe_mx4_down": (ctypes.c_int, [_DP, _MP, _MP, _P, _P, _P, _P]),
+    "moe_mx4_decode_workspace_bytes": (_SZ, [_DP, _DP]),
+    "moe_mx4_decode": (ctypes.c_int, [_DP, _P, _P, _P, _MP, _MP, _MP, _DP, _MP, _MP, _MP, _P, _P, _P, _P, _SZ, _P]),
+    "moe_balance_state_bytes": (_SZ, [_BP]),
+    "moe_balance_workspace_bytes": (_SZ, [_BP]),
+    "moe_balance_loss": (ctypes.c_int, [_BP] + [_P] * 7 + [_SZ, _P, _SZ, _P]),
+    "moe_balance_loss_bwd": (ctypes.c_int, [_BP] + [_P] * 6),
 }
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -405,3 +430,68 @@ def moe_grad_clip(grads, outs, max_norm, norm, ws, stream=None, ws_bytes=None):
     """outs None: in place.  ws: a tensor, or an address and ws_bytes."""
     _call("moe_grad_clip", grad_list(grads, outs), len(grads), float(max_norm), _ptr(norm), _ptr(ws),
           _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
+
+
+# 4-bit tensors are given as moe_mx4 structures (mx4), which hold addresses only: the caller keeps
+# the tensors.
+def mx4(codes, scales) -> moe_mx4:
+    return moe_mx4(_ptr(codes), _ptr(scales))
+
+
+def _ref(q):
+    return None if q is None else ctypes.byref(q)
+
+
+def moe_mx4_code_bytes(order: int, count: int, k: int, cols: int) -> int:
+    return lib().moe_mx4_code_bytes(order, count, k, cols)
+
+
+def moe_mx4_scale_bytes(order: int, count: int, k: int, cols: int) -> int:
+    return lib().moe_mx4_scale_bytes(order, count, k, cols)
+
+
+def moe_mx4_quantize(order, count, k, cols, dtype, v, q, stream=None):
+    _call("moe_mx4_quantize", order, count, k, cols, dtype, _ptr(v), _ref(q), _stream(stream))
+
+
+def moe_mx4_dequantize(order, count, k, cols, dtype, q, v, stream=None):
+    _call("moe_mx4_dequantize", order, count, k, cols, dtype, _ref(q), _ptr(v), _stream(stream))
+
+
+def moe_mx4_gate_up(d, x, sorted_flat, w_gate, w_up, tiles, num_tiles, act, stream=None):
+    _call("moe_mx4_gate_up", ctypes.byref(d), _ref(x), _ptr(sorted_flat), _ref(w_gate), _ref(w_up), _ptr(tiles),
+          _ptr(num_tiles), _ptr(act), _stream(stream))
+
+
+def moe_mx4_down(d, act, w_down, tiles, num_tiles, ys, stream=None):
+    _call("moe_mx4_down", ctypes.byref(d), _ref(act), _ref(w_down), _ptr(tiles), _ptr(num_tiles), _ptr(ys),
+          _stream(stream))
+
+
+def moe_mx4_decode_workspace_bytes(d: moe_dims, ds: Optional[moe_dims] = None) -> int:
+    return lib().moe_mx4_decode_workspace_bytes(ctypes.byref(d), _dims_ref(ds))
+
+
+def moe_mx4_decode(d, x, w_r, logit_bias, w_gate, w_up, w_down, ds, ws_gate, ws_up, ws_down, topk_idx, gates, y, ws,
+                   stream=None):
+    _call("moe_mx4_decode", ctypes.byref(d), _ptr(x), _ptr(w_r), _ptr(logit_bias), _ref(w_gate), _ref(w_up),
+          _ref(w_down), _dims_ref(ds), _ref(ws_gate), _ref(ws_up), _ref(ws_down), _ptr(topk_idx), _ptr(gates),
+          _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def moe_balance_state_bytes(b: moe_balance) -> int:
+    return lib().moe_balance_state_bytes(ctypes.byref(b))
+
+
+def moe_balance_workspace_bytes(b: moe_balance) -> int:
+    return lib().moe_balance_workspace_bytes(ctypes.byref(b))
+
+
+def moe_balance_loss(b, logits, topk_idx, logit_bias, mask, loss, counts, state, ws, stream=None):
+    _call("moe_balance_loss", ctypes.byref(b), _ptr(logits), _ptr(topk_idx), _ptr(logit_bias), _ptr(mask),
+          _ptr(loss), _ptr(counts), _ptr(state), _nbytes(state), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def moe_balance_loss_bwd(b, logits, mask, state, dloss, dlogits, stream=None):
+    _call("moe_balance_loss_bwd", ctypes.byref(b), _ptr(logits), _ptr(mask), _ptr(state), _ptr(dloss),
+          _ptr(dlogits), _stream(stream))

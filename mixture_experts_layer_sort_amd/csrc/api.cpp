@@ -79,6 +79,57 @@ int check_decode(const moe_dims* d, const moe_dims* ds, Dims* D, int64_t* Fs) {
   return D->N > MOE_DECODE_MAX_TOKENS ? MOE_EUNSUPPORTED : MOE_OK;
 }
 
+// Sizes of a 4-bit tensor; its bytes.
+struct Mx4Sizes {
+  size_t codes, scales, values;  // values: how many
+};
+int check_mx4_sizes(int32_t order, int64_t count, int64_t k, int64_t cols, Mx4Sizes* out) {
+  if (order != MOE_MX4_WEIGHTS && order != MOE_MX4_ROWS) return MOE_EINVAL;
+  if (count < 0 || k <= 0 || cols <= 0 || k % 128 != 0) return MOE_EINVAL;
+  if (order == MOE_MX4_ROWS ? cols != 1 : cols % 128 != 0) return MOE_EINVAL;
+  const int64_t side = int64_t(1) << 20;
+  if (k > side || cols > side || count >= int64_t(1) << 31) return MOE_EUNSUPPORTED;
+  if (count > (int64_t(1) << 40) / k / cols) return MOE_EUNSUPPORTED;
+  const size_t n = size_t(count) * size_t(k) * size_t(cols);
+  *out = Mx4Sizes{n / 2, size_t(count) * size_t(cols) * size_t((k + 511) / 512) * 16, n};
+  return MOE_OK;
+}
+
+bool mx4_ok(const moe_mx4* q) { return q != nullptr && ptrs_ok(q->codes, q->scales); }
+moe_launch::Mx4 mx4_of(const moe_mx4* q) {
+  return q == nullptr ? moe_launch::Mx4{nullptr, nullptr} : moe_launch::Mx4{q->codes, q->scales};
+}
+
+// Codes and scales [count][k][cols] of a tensor, as spans.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+void add_mx4(Span* s, int* n, const moe_mx4* q, int64_t count, int64_t k, int64_t cols) {
+  s[(*n)++] = Span{q->codes, size_t(count) * size_t(k) * size_t(cols) / 2};
+  s[(*n)++] = Span{q->scales, size_t(count) * size_t(cols) * size_t((k + 511) / 512) * 16};
+}
+// Whether one of the first `written` spans shares a byte with any other one.
+bool spans_overlap(const Span* s, int n, int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(s[i].at, s[i].bytes, s[j].at, s[j].bytes)) return true;
+  return false;
+}
+
+// A balance loss's sizes and options.
+int check_balance(const moe_balance* b) {
+  if (b == nullptr) return MOE_EINVAL;
+  if (b->dtype != MOE_F32 && b->dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+  if (b->score != MOE_SCORE_SOFTMAX && b->score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+  if (b->N < 0 || b->E <= 0 || b->K <= 0 || b->seq_len <= 0 || b->N % b->seq_len != 0) return MOE_EINVAL;
+  if (!std::isfinite(b->alpha) || !std::isfinite(b->z_coef)) return MOE_EINVAL;
+  if (b->E > MOE_MAX_EXPERTS || b->K > MOE_MAX_TOPK || b->K > b->E) return MOE_EUNSUPPORTED;
+  const int64_t lim = int64_t(1) << 31;
+  if (b->N >= lim || b->seq_len >= lim - 4096 || b->N * b->K >= lim || b->N * b->E >= lim) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
 // A list of gradients (out: the outputs count too).
 int check_grads(const moe_grad* g, int64_t count, bool out) {
   if (count < 0 || (count > 0 && g == nullptr)) return MOE_EINVAL;
@@ -569,6 +620,175 @@ int moe_grad_clip(const moe_grad* list, int64_t count, float max_norm, float* no
   st = check_grad_overlaps(list, count, norm, ws);
   if (st != MOE_OK) return st;
   return from_hip(moe_launch::grad_clip(list, int(count), max_norm, norm, ws, stream));
+}
+
+size_t moe_mx4_code_bytes(int32_t order, int64_t count, int64_t k, int64_t cols) {
+  Mx4Sizes z;
+  return check_mx4_sizes(order, count, k, cols, &z) == MOE_OK ? z.codes : size_t(-1);
+}
+
+size_t moe_mx4_scale_bytes(int32_t order, int64_t count, int64_t k, int64_t cols) {
+  Mx4Sizes z;
+  return check_mx4_sizes(order, count, k, cols, &z) == MOE_OK ? z.scales : size_t(-1);
+}
+
+int moe_mx4_quantize(int32_t order, int64_t count, int64_t k, int64_t cols, int32_t dtype, const void* v,
+                     const moe_mx4* q, hipStream_t stream) {
+  Mx4Sizes z;
+  const int st = check_mx4_sizes(order, count, k, cols, &z);
+  if (st != MOE_OK) return st;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+  if (!ptrs_ok(v) || !mx4_ok(q)) return MOE_EINVAL;
+  const Span s[] = {{q->codes, z.codes}, {q->scales, z.scales}, {v, z.values * (dtype == MOE_BF16 ? 2 : 4)}};
+  if (spans_overlap(s, 3, 2)) return MOE_EINVAL;
+  if (count == 0) return MOE_OK;
+  return from_hip(moe_launch::mx4_quantize(order == MOE_MX4_ROWS, count, k, cols, dtype, v, q->codes, q->scales, stream));
+}
+
+int moe_mx4_dequantize(int32_t order, int64_t count, int64_t k, int64_t cols, int32_t dtype, const moe_mx4* q,
+                       void* v, hipStream_t stream) {
+  Mx4Sizes z;
+  const int st = check_mx4_sizes(order, count, k, cols, &z);
+  if (st != MOE_OK) return st;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+  if (!ptrs_ok(v) || !mx4_ok(q)) return MOE_EINVAL;
+  const Span s[] = {{v, z.values * (dtype == MOE_BF16 ? 2 : 4)}, {q->codes, z.codes}, {q->scales, z.scales}};
+  if (spans_overlap(s, 3, 1) || overlap(q->codes, z.codes, q->scales, z.scales)) return MOE_EINVAL;
+  if (count == 0) return MOE_OK;
+  return from_hip(moe_launch::mx4_dequantize(order == MOE_MX4_ROWS, count, k, cols, dtype, mx4_of(q), v, stream));
+}
+
+int moe_mx4_gate_up(const moe_dims* d, const moe_mx4* x, const int32_t* sorted_flat, const moe_mx4* w_gate,
+                    const moe_mx4* w_up, const int32_t* tiles, const int32_t* num_tiles, void* act,
+                    hipStream_t stream) {
+  MOE_CHECK_DIMS(d, D);
+  if (!mx4_ok(x) || !mx4_ok(w_gate) || !mx4_ok(w_up) || !ptrs_ok(sorted_flat, tiles, num_tiles, act)) return MOE_EINVAL;
+  Span s[10] = {{act, size_t(D.NK()) * size_t(D.F) * (D.dtype == MOE_BF16 ? 2 : 4)},
+                {sorted_flat, size_t(D.NK()) * 4},
+                {tiles, size_t(moe_launch::max_tiles(D)) * 12},
+                {num_tiles, 4}};
+  int n = 4;
+  add_mx4(s, &n, x, D.N, D.H, 1);
+  add_mx4(s, &n, w_gate, D.E, D.H, D.F);
+  add_mx4(s, &n, w_up, D.E, D.H, D.F);
+  if (D.N == 0) return MOE_OK;
+  if (spans_overlap(s, n, 1)) return MOE_EINVAL;
+  return from_hip(moe_launch::mx4_gate_up(D, mx4_of(x), sorted_flat, mx4_of(w_gate), mx4_of(w_up), tiles, num_tiles,
+                                          act, stream));
+}
+
+int moe_mx4_down(const moe_dims* d, const moe_mx4* act, const moe_mx4* w_down, const int32_t* tiles,
+                 const int32_t* num_tiles, void* ys, hipStream_t stream) {
+  MOE_CHECK_DIMS(d, D);
+  if (!mx4_ok(act) || !mx4_ok(w_down) || !ptrs_ok(tiles, num_tiles, ys)) return MOE_EINVAL;
+  Span s[7] = {{ys, size_t(D.NK()) * size_t(D.H) * (D.dtype == MOE_BF16 ? 2 : 4)},
+               {tiles, size_t(moe_launch::max_tiles(D)) * 12},
+               {num_tiles, 4}};
+  int n = 3;
+  add_mx4(s, &n, act, D.NK(), D.F, 1);
+  add_mx4(s, &n, w_down, D.E, D.F, D.H);
+  if (D.N == 0) return MOE_OK;
+  if (spans_overlap(s, n, 1)) return MOE_EINVAL;
+  return from_hip(moe_launch::mx4_down(D, mx4_of(act), mx4_of(w_down), tiles, num_tiles, ys, stream));
+}
+
+size_t moe_mx4_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds) {
+  Dims D;
+  int64_t Fs;
+  if (check_decode(d, ds, &D, &Fs) != MOE_OK) return size_t(-1);
+  return D.N == 0 ? 0 : moe_launch::mx4_decode_ws(D, Fs);
+}
+
+int moe_mx4_decode(const moe_dims* d, const void* x, const void* w_r, const float* logit_bias, const moe_mx4* w_gate,
+                   const moe_mx4* w_up, const moe_mx4* w_down, const moe_dims* ds, const moe_mx4* ws_gate,
+                   const moe_mx4* ws_up, const moe_mx4* ws_down, int32_t* topk_idx, float* gates, void* y, void* ws,
+                   size_t ws_bytes, hipStream_t stream) {
+  Dims D;
+  int64_t Fs;
+  const int st = check_decode(d, ds, &D, &Fs);
+  if (st != MOE_OK) return st;
+  if (!ptrs_ok(x, w_r, topk_idx, gates, y) || !mx4_ok(w_gate) || !mx4_ok(w_up) || !mx4_ok(w_down)) return MOE_EINVAL;
+  if (logit_bias != nullptr && !aligned16(logit_bias)) return MOE_EINVAL;
+  if (ds != nullptr ? !(mx4_ok(ws_gate) && mx4_ok(ws_up) && mx4_ok(ws_down))
+                    : (ws_gate != nullptr || ws_up != nullptr || ws_down != nullptr))
+    return MOE_EINVAL;
+  if (D.N == 0) return MOE_OK;
+  const size_t need = moe_launch::mx4_decode_ws(D, Fs), nk = size_t(D.NK()) * 4;
+  Span s[19] = {{y, row_bytes(D)},
+                {topk_idx, nk},
+                {gates, nk},
+                {ws, need},
+                {x, row_bytes(D)},
+                {w_r, size_t(D.E) * size_t(D.H) * (D.dtype == MOE_BF16 ? 2 : 4)},
+                {logit_bias, logit_bias == nullptr ? 0 : size_t(D.E) * 4}};
+  int n = 7;
+  add_mx4(s, &n, w_gate, D.E, D.H, D.F);
+  add_mx4(s, &n, w_up, D.E, D.H, D.F);
+  add_mx4(s, &n, w_down, D.E, D.F, D.H);
+  if (ds != nullptr) {
+    add_mx4(s, &n, ws_gate, 1, D.H, Fs);
+    add_mx4(s, &n, ws_up, 1, D.H, Fs);
+    add_mx4(s, &n, ws_down, 1, Fs, D.H);
+  }
+  if (spans_overlap(s, n, 4)) return MOE_EINVAL;
+  if (ws == nullptr || ws_bytes < need || !aligned16(ws)) return MOE_EWORKSPACE;
+  return from_hip(moe_launch::mx4_decode(D, x, w_r, logit_bias, mx4_of(w_gate), mx4_of(w_up), mx4_of(w_down), Fs,
+                                         mx4_of(ws_gate), mx4_of(ws_up), mx4_of(ws_down), topk_idx, gates, y, ws,
+                                         stream));
+}
+
+size_t moe_balance_state_bytes(const moe_balance* b) {
+  if (check_balance(b) != MOE_OK) return size_t(-1);
+  return b->N == 0 ? 0 : moe_launch::balance_state(*b);
+}
+
+size_t moe_balance_workspace_bytes(const moe_balance* b) {
+  if (check_balance(b) != MOE_OK) return size_t(-1);
+  return b->N == 0 ? 0 : moe_launch::balance_ws(*b);
+}
+
+int moe_balance_loss(const moe_balance* b, const void* logits, const int32_t* topk_idx, const float* logit_bias,
+                     const uint8_t* mask, float* loss, int32_t* counts, void* state, size_t state_bytes, void* ws,
+                     size_t ws_bytes, hipStream_t stream) {
+  const int st = check_balance(b);
+  if (st != MOE_OK) return st;
+  if (!ptrs_ok(logits, loss, counts)) return MOE_EINVAL;
+  if (topk_idx != nullptr && (logit_bias != nullptr || !aligned16(topk_idx))) return MOE_EINVAL;
+  if (logit_bias != nullptr && !aligned16(logit_bias)) return MOE_EINVAL;
+  if (mask != nullptr && !aligned16(mask)) return MOE_EINVAL;
+  if (b->N == 0) return MOE_OK;
+  const size_t sb = moe_launch::balance_state(*b), wb = moe_launch::balance_ws(*b);
+  const size_t row = size_t(b->E) * (b->dtype == MOE_BF16 ? 2 : 4);
+  const Span s[] = {{loss, 4},
+                    {counts, size_t(b->E) * 4},
+                    {state, sb},
+                    {ws, wb},
+                    {logits, size_t(b->N) * row},
+                    {topk_idx, topk_idx == nullptr ? 0 : size_t(b->N) * size_t(b->K) * 4},
+                    {logit_bias, logit_bias == nullptr ? 0 : size_t(b->E) * 4},
+                    {mask, mask == nullptr ? 0 : size_t(b->N)}};
+  if (spans_overlap(s, 8, 4)) return MOE_EINVAL;
+  if (state == nullptr || state_bytes < sb || !aligned16(state)) return MOE_EWORKSPACE;
+  if (ws == nullptr || ws_bytes < wb || !aligned16(ws)) return MOE_EWORKSPACE;
+  return from_hip(moe_launch::balance_loss(*b, logits, topk_idx, logit_bias, mask, loss, counts, state, ws, stream));
+}
+
+int moe_balance_loss_bwd(const moe_balance* b, const void* logits, const uint8_t* mask, const void* state,
+                         const float* dloss, void* dlogits, hipStream_t stream) {
+  const int st = check_balance(b);
+  if (st != MOE_OK) return st;
+  if (!ptrs_ok(logits, state, dlogits)) return MOE_EINVAL;
+  if (mask != nullptr && !aligned16(mask)) return MOE_EINVAL;
+  if (dloss != nullptr && (reinterpret_cast<uintptr_t>(dloss) & 3u) != 0) return MOE_EINVAL;
+  if (b->N == 0) return MOE_OK;
+  const size_t n = size_t(b->N) * size_t(b->E) * (b->dtype == MOE_BF16 ? 2 : 4);
+  const Span s[] = {{dlogits, n},
+                    {logits, dlogits == logits ? 0 : n},
+                    {mask, mask == nullptr ? 0 : size_t(b->N)},
+                    {state, moe_launch::balance_state(*b)},
+                    {dloss, dloss == nullptr ? size_t(0) : size_t(4)}};
+  if (spans_overlap(s, 5, 1)) return MOE_EINVAL;
+  return from_hip(moe_launch::balance_loss_bwd(*b, logits, mask, state, dloss, dlogits, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,556 @@
+// Balance and z loss of router logits, per sequence, padding left out, and the
+// gradient of the logits (moe_balance in moe.h).
+//
+//   p_t = softmax(l_t) or sigmoid(l_t) / sum sigmoid(l_t),   lse_t = log sum exp(l_t),
+//   f_s,e = E c_s,e / (K n_s),  P_s,e = mean_t p_t,e,
+//   loss = alpha / B' sum_s f_s.P_s + z / n sum_t lse_t^2,
+//   dl_t,e = alpha / (B' n_s) p_e (f_s,e - f_s.p_t) [1 - sigmoid(l_e)] + 2 z / n lse_t softmax_e.
+//
+// Sixteen lanes have a token, so that every sum over its experts stays within a
+// row of lanes (DPP moves, no LDS).  The logits are read twice: f, which the
+// gradient needs, is known only after all of a sequence's tokens.  Probabilities
+// are formed again in the backward pass, which costs less than 4 bytes of them
+// written and read for each logit.  Chunks of a sequence leave partial sums; the
+// next launch adds them up in float64 in their order.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "common.h"
+
+namespace {
+using namespace moe;
+
+constexpr int kLanes = 16;       // of a token
+constexpr int kRows = 256 / kLanes;  // tokens a workgroup has under way
+constexpr int64_t kMostChunks = 512;
+
+// Over the sixteen lanes of a token, all of them getting the result: each step
+// takes the value of a lane with the lowest 1, 2, 3, 4 bits of its number mirrored.
+#define MOE_DPP(v, ctrl) __builtin_amdgcn_update_dpp(0, v, ctrl, 0xf, 0xf, true)
+template <typename F>
+__device__ __forceinline__ float over_lanes(float v, F f) {
+  v = f(v, __int_as_float(MOE_DPP(__float_as_int(v), 0xb1)));   // quad_perm 1 0 3 2
+  v = f(v, __int_as_float(MOE_DPP(__float_as_int(v), 0x4e)));   // quad_perm 2 3 0 1
+  v = f(v, __int_as_float(MOE_DPP(__float_as_int(v), 0x141)));  // row_half_mirror
+  return f(v, __int_as_float(MOE_DPP(__float_as_int(v), 0x140)));  // row_mirror
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+  return over_lanes(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float lanes_max(float v) {
+  return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// A token's NV * 16 >= E values over its lanes: VEC, four neighbours at a time
+// (E a multiple of 4), else every sixteenth.
+template <int NV, bool VEC> struct Place {
+  static __device__ __forceinline__ int expert(int sub, int v) {
+    return VEC ? v / 4 * 64 + sub * 4 + v % 4 : v * kLanes + sub;
+  }
+};
+
+template <typename T, int NV, bool VEC>
+__device__ __forceinline__ void load_row(const T* __restrict__ p, int sub, int E, float (&l)[NV]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int v = 0; v < NV; v += 4) {
+      const int e = Place<NV, VEC>::expert(sub, v);
+      if (e < E) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p + e);
+          l[v] = q.x; l[v + 1] = q.y; l[v + 2] = q.z; l[v + 3] = q.w;
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(p + e);
+          l[v] = __uint_as_float(q.x << 16);
+          l[v + 1] = __uint_as_float(q.x & 0xffff0000u);
+          l[v + 2] = __uint_as_float(q.y << 16);
+          l[v + 3] = __uint_as_float(q.y & 0xffff0000u);
+        }
+      } else {
+        l[v] = l[v + 1] = l[v + 2] = l[v + 3] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = Place<NV, VEC>::expert(sub, v);
+      l[v] = e < E ? Elt<T>::load(p + e) : -INFINITY;
+    }
+  }
+}
+
+// Probabilities of one token: soft the softmax, p the score's, rest 1 - sigmoid
+// (sigmoid scores), lse its log-sum-exp.  Places past E hold -inf: 0 in all.
+template <int NV> struct Token {
+  float soft[NV], p[NV], rest[NV], lse;
+  __device__ __forceinline__ void set(const float (&l)[NV], bool sigmoid) {
+    float top = l[0];
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      top = fmaxf(top, l[v]);
+      nan = nan || l[v] != l[v];
+    }
+    top = lanes_max(top);
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      soft[v] = expf(l[v] - top);
+      sum += soft[v];
+    }
+    if (nan) sum = __uint_as_float(0x7fc00000u);
+    sum = lanes_sum(sum);
+    lse = top + logf(sum);
+    const float inv = 1.f / sum;
+    if (sigmoid) {
+      // Where all logits are negative every sigmoid may be tiny: there all of them
+      // over exp(top), whose largest is 1 / (1 + exp(top)).
+      const float down = expf(top);
+      float all = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const float t = expf(-fabsf(l[v])), r = 1.f / (1.f + t);
+        const float s = top > 0.f ? (l[v] >= 0.f ? r : t * r) : soft[v] / (1.f + soft[v] * down);
+        rest[v] = l[v] >= 0.f ? t * r : r;
+        p[v] = s;
+        all += s;
+      }
+      all = lanes_sum(all);
+      const float a = 1.f / all;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) p[v] *= a;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      soft[v] *= inv;
+      if (!sigmoid) p[v] = soft[v];
+    }
+  }
+};
+
+// Order of the choice: larger values first, NaN last, equal values (0 and -0 too)
+// by their expert, as one number that is larger the earlier.
+__device__ __forceinline__ uint64_t choice_key(float v, int e) {
+  uint32_t u = __float_as_uint(v + 0.f);
+  u = u & 0x80000000u ? ~u : u | 0x80000000u;
+  if (v != v) u = 0;
+  return uint64_t(u) << 8 | uint64_t(255 - e);
+}
+
+// The K experts of largest value, each counted by the lane that holds it.
+template <int NV, bool VEC>
+__device__ __forceinline__ void choose(const float (&l)[NV], const float* __restrict__ bias, int sub, int E, int K,
+                                       int* count) {
+  uint64_t key[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int e = Place<NV, VEC>::expert(sub, v);
+    // 0 is below every expert's key: NaN and the last expert of 256 give 0 too, so 1 is added
+    key[v] = e < E ? choice_key(bias != nullptr ? l[v] + bias[e] : l[v], e) + 1 : 0;
+  }
+  for (int k = 0; k < K; ++k) {
+    uint64_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < NV; ++v) best = key[v] > best ? key[v] : best;
+    uint32_t hi = uint32_t(best >> 32), lo = uint32_t(best);
+#define MOE_STEP(ctrl)                                                                       \
+  {                                                                                          \
+    const uint32_t h = uint32_t(MOE_DPP(int(hi), ctrl)), o = uint32_t(MOE_DPP(int(lo), ctrl)); \
+    const bool more = h > hi || (h == hi && o > lo);                                         \
+    hi = more ? h : hi;                                                                      \
+    lo = more ? o : lo;                                                                      \
+  }
+    MOE_STEP(0xb1)
+    MOE_STEP(0x4e)
+    MOE_STEP(0x141)
+    MOE_STEP(0x140)
+#undef MOE_STEP
+    best = uint64_t(hi) << 32 | lo;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (key[v] == best) {
+        key[v] = 0;
+        atomicAdd(count + Place<NV, VEC>::expert(sub, v), 1);
+      }
+  }
+}
+
+// One chunk's sums: P [E], counts [E], the sum of lse^2, the number of tokens.
+__host__ __device__ constexpr int64_t part_words(int64_t E) { return 2 * E + 2; }
+
+template <typename T, int NV, bool VEC>
+__global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ logits, const int32_t* __restrict__ topk,
+                                                       const float* __restrict__ bias,
+                                                       const uint8_t* __restrict__ mask, float* __restrict__ parts,
+                                                       int E, int K, int seq_len, int chunk, int chunks, bool sigmoid) {
+  __shared__ float sp[kRows][NV * kLanes];
+  __shared__ float sz[kRows];
+  __shared__ int count[NV * kLanes], tokens;
+  const int t = threadIdx.x, sub = t % kLanes, q = t / kLanes;
+  for (int i = t; i < NV * kLanes; i += 256) count[i] = 0;
+  if (t == 0) tokens = 0;
+  __syncthreads();
+  const int first = int(blockIdx.x % chunks) * chunk, last = min(first + chunk, seq_len);
+  const int64_t row0 = int64_t(blockIdx.x / chunks) * seq_len;
+  float p[NV], z = 0.f, l[NV], next[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) p[v] = 0.f;
+  int mine = 0;
+  bool live = false, ahead;
+  auto fetch = [&](int r, float (&to)[NV]) {
+    const int64_t n = row0 + r;
+    const bool is = r < last && (mask == nullptr || mask[n] != 0);
+    if (is) load_row<T, NV, VEC>(logits + n * E, sub, E, to);
+    return is;
+  };
+  live = fetch(first + q, l);
+  for (int r = first + q; r < last; r += kRows) {
+    ahead = fetch(r + kRows, next);  // the next token's logits on their way
+    if (live) {
+      Token<NV> a;
+      a.set(l, sigmoid);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) p[v] += a.p[v];
+      z += a.lse * a.lse;
+      ++mine;
+      if (topk == nullptr) {
+        choose<NV, VEC>(l, bias, sub, E, K, count);
+      } else if (sub < K) {
+        const int e = topk[(row0 + r) * K + sub];
+        if (e >= 0 && e < E) atomicAdd(count + e, 1);
+      }
+    }
+    live = ahead;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) l[v] = next[v];
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) sp[q][Place<NV, VEC>::expert(sub, v)] = p[v];
+  if (sub == 0) {
+    sz[q] = z;
+    atomicAdd(&tokens, mine);
+  }
+  __syncthreads();
+  float* out = parts + int64_t(blockIdx.x) * part_words(E);
+  for (int e = t; e < E; e += 256) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s += sp[i][e];
+    out[e] = s;
+    reinterpret_cast<int*>(out)[E + e] = count[e];
+  }
+  if (t == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s += sz[i];
+    out[2 * E] = s;
+    reinterpret_cast<int*>(out)[2 * E + 1] = tokens;
+  }
+}
+
+// What the backward pass needs: words 0 and 1 the sequences and tokens that count,
+// then of every sequence f [E] and its tokens.
+constexpr int kStateHead = 4;
+__host__ __device__ constexpr int64_t state_words(int64_t B, int64_t E) { return kStateHead + B * (E + 1); }
+
+// Of every sequence, for the sums over them.
+struct SeqSum {
+  double loss, z;  // f.P, sum of lse^2
+  int64_t tokens;
+};
+
+// alpha / B' sum f.P + z / n sum lse^2, from the sums over the sequences.
+__device__ __forceinline__ float total_loss(double fp, double z, int64_t seqs, int64_t tokens, float alpha,
+                                            float z_coef) {
+  if (tokens == 0) return 0.f;
+  const double balance = double(alpha) * fp / double(seqs);
+  return float(z_coef == 0.f ? balance : balance + double(z_coef) * z / double(tokens));  // no 0 * infinity
+}
+
+// A sequence a workgroup: its chunks added up by 1024 threads, (expert, slice of
+// the chunks), eight loads under way; f, its loss, and with one sequence the rest.
+__global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ parts, float* __restrict__ state,
+                                                      SeqSum* __restrict__ sums, int32_t* __restrict__ seq_counts,
+                                                      float* __restrict__ loss, int E, int lanes, int K, int chunks,
+                                                      int B, float alpha, float z_coef) {
+  __shared__ double sp[1024];
+  __shared__ int sc[1024];
+  __shared__ double sz[16];
+  __shared__ int64_t sn[16];
+  const int t = threadIdx.x, s = blockIdx.x, e = t % lanes, slice = t / lanes, slices = 1024 / lanes;
+  const float* in = parts + int64_t(s) * chunks * part_words(E);
+  const int64_t step = part_words(E);
+  double p = 0.0;
+  int c = 0;
+  if (e < E)
+    for (int i0 = slice; i0 < chunks; i0 += 8 * slices) {
+      float a[8];
+      int b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * slices;
+        a[j] = i < chunks ? in[i * step + e] : 0.f;
+        b[j] = i < chunks ? reinterpret_cast<const int*>(in)[i * step + E + e] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p += double(a[j]);
+        c += b[j];
+      }
+    }
+  double z = 0.0;
+  int64_t n = 0;
+  for (int i = t; i < chunks; i += 1024) {
+    z += double(in[i * step + 2 * E]);
+    n += reinterpret_cast<const int*>(in)[i * step + 2 * E + 1];
+  }
+  auto over_block = [&](double& dv, int64_t& iv) {  // sums over all threads, in a fixed order
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      dv += __shfl_xor(dv, off, kWave);
+      iv += __shfl_xor(iv, off, kWave);
+    }
+    __syncthreads();
+    if (lane_id() == 0) {
+      sz[t / kWave] = dv;
+      sn[t / kWave] = iv;
+    }
+    __syncthreads();
+    dv = 0.0;
+    iv = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      dv += sz[i];
+      iv += sn[i];
+    }
+  };
+  over_block(z, n);
+  sp[t] = p;
+  sc[t] = c;
+  __syncthreads();
+  double fp = 0.0;
+  if (t < E) {
+    p = 0.0;
+    c = 0;
+    for (int i = 0; i < slices; ++i) {
+      p += sp[i * lanes + t];
+      c += sc[i * lanes + t];
+    }
+    const double f = n == 0 ? 0.0 : double(E) * double(c) / (double(K) * double(n));
+    state[kStateHead + int64_t(s) * (E + 1) + t] = float(f);
+    seq_counts[int64_t(s) * E + t] = c;  // the counts themselves where there is one sequence
+    fp = n == 0 ? 0.0 : f * p / double(n);
+  }
+  int64_t none = 0;
+  over_block(fp, none);
+  if (t == 0) {
+    reinterpret_cast<int32_t*>(state)[kStateHead + int64_t(s) * (E + 1) + E] = int32_t(n);
+    if (B == 1) {
+      reinterpret_cast<int32_t*>(state)[0] = n > 0;
+      reinterpret_cast<int32_t*>(state)[1] = int32_t(n);
+      loss[0] = total_loss(fp, z, 1, n, alpha, z_coef);
+    } else {
+      sums[s] = SeqSum{fp, z, n};
+    }
+  }
+}
+
+// Over several sequences: workgroup 0 the loss, the others 16 experts' counts each.
+__global__ __launch_bounds__(256) void k_balance_total(const SeqSum* __restrict__ sums,
+                                                       const int32_t* __restrict__ seq_counts,
+                                                       float* __restrict__ state, int32_t* __restrict__ counts,
+                                                       float* __restrict__ loss, int E, int B, float alpha,
+                                                       float z_coef) {
+  const int t = threadIdx.x;
+  if (blockIdx.x == 0) {
+    __shared__ double sf[256], sz[256];
+    __shared__ int64_t sn[256], ss[256];
+    double f = 0.0, z = 0.0;
+    int64_t n = 0, seqs = 0;
+    for (int i = t; i < B; i += 256) {
+      const SeqSum q = sums[i];
+      f += q.loss;
+      z += q.z;
+      n += q.tokens;
+      seqs += q.tokens > 0;
+    }
+    sf[t] = f; sz[t] = z; sn[t] = n; ss[t] = seqs;
+    for (int off = 128; off > 0; off >>= 1) {
+      __syncthreads();
+      if (t < off) {
+        sf[t] += sf[t + off]; sz[t] += sz[t + off]; sn[t] += sn[t + off]; ss[t] += ss[t + off];
+      }
+    }
+    if (t == 0) {
+      reinterpret_cast<int32_t*>(state)[0] = int32_t(ss[0]);
+      reinterpret_cast<int32_t*>(state)[1] = int32_t(sn[0]);
+      loss[0] = total_loss(sf[0], sz[0], ss[0], sn[0], alpha, z_coef);
+    }
+    return;
+  }
+  __shared__ int sc[256];
+  const int e = (int(blockIdx.x) - 1) * 16 + t % 16;
+  int c = 0;
+  if (e < E)
+    for (int s = t / 16; s < B; s += 16) c += seq_counts[int64_t(s) * E + e];
+  sc[t] = c;
+  __syncthreads();
+  if (t < 16 && e < E) {
+    c = 0;
+    for (int i = 0; i < 16; ++i) c += sc[16 * i + t];
+    counts[e] = c;
+  }
+}
+
+template <typename T, int NV, bool VEC>
+__global__ __launch_bounds__(256) void k_balance_bwd(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
+                                                     const float* __restrict__ state, const float* __restrict__ dloss,
+                                                     T* __restrict__ dlogits, int64_t N, int E, int seq_len,
+                                                     float alpha, float z_coef, bool sigmoid) {
+  const int sub = threadIdx.x % kLanes;
+  const int64_t n = int64_t(blockIdx.x) * kRows + threadIdx.x / kLanes;
+  if (n >= N) return;  // all lanes of a token
+  const int32_t* head = reinterpret_cast<const int32_t*>(state);
+  float d[NV];
+  if (mask == nullptr || mask[n] != 0) {
+    float l[NV];
+    load_row<T, NV, VEC>(logits + n * E, sub, E, l);
+    const float* seq = state + kStateHead + n / seq_len * (E + 1);
+    float f[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = Place<NV, VEC>::expert(sub, v);
+      f[v] = e < E ? seq[e] : 0.f;
+    }
+    const float up = dloss == nullptr ? 1.f : dloss[0];
+    const float c = up * alpha / (float(head[0]) * float(reinterpret_cast<const int32_t*>(seq)[E]));
+    Token<NV> a;
+    a.set(l, sigmoid);
+    float fp = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) fp += f[v] * a.p[v];
+    fp = lanes_sum(fp);
+    const float zc = up * 2.f * z_coef / float(head[1]) * a.lse;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float b = c * a.p[v] * (f[v] - fp);
+      if (sigmoid) b *= a.rest[v];
+      d[v] = z_coef == 0.f ? b : b + zc * a.soft[v];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) d[v] = 0.f;
+  }
+  T* p = dlogits + n * E;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int v = 0; v < NV; v += 4) {
+      const int e = Place<NV, VEC>::expert(sub, v);
+      if (e < E) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(p + e) = make_float4(d[v], d[v + 1], d[v + 2], d[v + 3]);
+        else
+          *reinterpret_cast<uint2*>(p + e) = make_uint2(pack_bf16x2(d[v], d[v + 1]), pack_bf16x2(d[v + 2], d[v + 3]));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = Place<NV, VEC>::expert(sub, v);
+      if (e < E) p[e] = Elt<T>::from_f32(d[v]);
+    }
+  }
+}
+
+// Tokens of a chunk: a sequence in as many as keep their number near kMostChunks in
+// all, a whole number of a workgroup's turns each.
+int64_t chunk_of(const moe_balance& b) {
+  const int64_t per = (b.N + kMostChunks - 1) / kMostChunks;
+  return std::min<int64_t>((per + kRows - 1) / kRows * kRows, (b.seq_len + kRows - 1) / kRows * kRows);
+}
+int64_t chunks_of(const moe_balance& b) { return (b.seq_len + chunk_of(b) - 1) / chunk_of(b); }
+
+size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
+size_t parts_bytes(const moe_balance& b) {
+  return pad(size_t(b.N / b.seq_len * chunks_of(b)) * part_words(b.E) * 4);
+}
+
+// NV and VEC of a launch.
+template <typename T, typename F>
+hipError_t by_experts(int64_t E, F f) {
+  if (E % 4 == 0 && E > 32)
+    return E <= 64 ? f(std::integral_constant<int, 4>(), std::true_type())
+           : E <= 128 ? f(std::integral_constant<int, 8>(), std::true_type())
+                      : f(std::integral_constant<int, 16>(), std::true_type());
+  return E <= 16    ? f(std::integral_constant<int, 1>(), std::false_type())
+         : E <= 32  ? f(std::integral_constant<int, 2>(), std::false_type())
+         : E <= 64  ? f(std::integral_constant<int, 4>(), std::false_type())
+         : E <= 128 ? f(std::integral_constant<int, 8>(), std::false_type())
+                    : f(std::integral_constant<int, 16>(), std::false_type());
+}
+
+template <typename T>
+hipError_t loss_t(const moe_balance& b, const T* logits, const int32_t* topk, const float* bias, const uint8_t* mask,
+                  float* loss, int32_t* counts, float* state, char* ws, hipStream_t s) {
+  const int64_t B = b.N / b.seq_len, chunk = chunk_of(b), chunks = chunks_of(b);
+  float* parts = reinterpret_cast<float*>(ws);
+  SeqSum* sums = reinterpret_cast<SeqSum*>(ws + parts_bytes(b));
+  int32_t* seq_counts = B == 1 ? counts : reinterpret_cast<int32_t*>(ws + parts_bytes(b) + pad(size_t(B) * sizeof(SeqSum)));
+  const hipError_t st = by_experts<T>(b.E, [&](auto nv, auto vec) {
+    k_balance_parts<T, nv.value, vec.value><<<dim3(unsigned(B * chunks)), dim3(256), 0, s>>>(
+        logits, topk, bias, mask, parts, int(b.E), int(b.K), int(b.seq_len), int(chunk), int(chunks),
+        b.score == MOE_SCORE_SIGMOID);
+    return hipGetLastError();
+  });
+  if (st != hipSuccess) return st;
+  int lanes = 1;
+  while (lanes < b.E) lanes *= 2;
+  k_balance_seq<<<dim3(unsigned(B)), dim3(1024), 0, s>>>(parts, state, sums, seq_counts, loss, int(b.E), lanes,
+                                                         int(b.K), int(chunks), int(B), b.alpha, b.z_coef);
+  if (B > 1)
+    k_balance_total<<<dim3(unsigned(1 + (b.E + 15) / 16)), dim3(256), 0, s>>>(sums, seq_counts, state, counts, loss,
+                                                                             int(b.E), int(B), b.alpha, b.z_coef);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t bwd_t(const moe_balance& b, const T* logits, const uint8_t* mask, const float* state, const float* dloss,
+                 T* dlogits, hipStream_t s) {
+  return by_experts<T>(b.E, [&](auto nv, auto vec) {
+    k_balance_bwd<T, nv.value, vec.value><<<dim3(unsigned((b.N + kRows - 1) / kRows)), dim3(256), 0, s>>>(
+        logits, mask, state, dloss, dlogits, b.N, int(b.E), int(b.seq_len), b.alpha, b.z_coef,
+        b.score == MOE_SCORE_SIGMOID);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+namespace moe_launch {
+
+size_t balance_state(const moe_balance& b) { return size_t(state_words(b.N / b.seq_len, b.E)) * 4; }
+
+size_t balance_ws(const moe_balance& b) {
+  const size_t B = size_t(b.N / b.seq_len);
+  return parts_bytes(b) + (B == 1 ? 0 : pad(B * sizeof(SeqSum)) + pad(B * b.E * 4));
+}
+
+hipError_t balance_loss(const moe_balance& b, const void* logits, const int32_t* topk, const float* bias,
+                        const uint8_t* mask, float* loss, int32_t* counts, void* state, void* ws, hipStream_t s) {
+  char* w = static_cast<char*>(ws);
+  float* st = static_cast<float*>(state);
+  return b.dtype == MOE_BF16
+             ? loss_t(b, static_cast<const bf16_t*>(logits), topk, bias, mask, loss, counts, st, w, s)
+             : loss_t(b, static_cast<const float*>(logits), topk, bias, mask, loss, counts, st, w, s);
+}
+
+hipError_t balance_loss_bwd(const moe_balance& b, const void* logits, const uint8_t* mask, const void* state,
+                            const float* dloss, void* dlogits, hipStream_t s) {
+  const float* st = static_cast<const float*>(state);
+  return b.dtype == MOE_BF16
+             ? bwd_t(b, static_cast<const bf16_t*>(logits), mask, st, dloss, static_cast<bf16_t*>(dlogits), s)
+             : bwd_t(b, static_cast<const float*>(logits), mask, st, dloss, static_cast<float*>(dlogits), s);
+}
+
+}  // namespace moe_launch

@@ -229,6 +229,34 @@ hipError_t decode(const Dims& d, const void* x, const void* w_r, const float* bi
                   const void* wd, int64_t Fs, const void* swg, const void* swu, const void* swd, int32_t* topk,
                   float* gates, void* y, void* ws, hipStream_t s);
 
+// A tensor in 4 bits: weights [count][k][cols], or rows [count][k] (cols = 1).
+struct Mx4 {
+  const void* codes;
+  const void* scales;
+};
+hipError_t mx4_quantize(bool rows, int64_t count, int64_t k, int64_t cols, int dtype, const void* v, void* codes,
+                        void* scales, hipStream_t s);
+hipError_t mx4_dequantize(bool rows, int64_t count, int64_t k, int64_t cols, int dtype, const Mx4& q, void* v,
+                          hipStream_t s);
+// Grouped products of 4-bit rows; wu null: the plain product (down).
+hipError_t mx4_gate_up(const Dims& d, const Mx4& x, const int32_t* sorted_flat, const Mx4& wg, const Mx4& wu,
+                       const int32_t* tiles, const int32_t* num_tiles, void* act, hipStream_t s);
+hipError_t mx4_down(const Dims& d, const Mx4& act, const Mx4& wd, const int32_t* tiles, const int32_t* num_tiles,
+                    void* ys, hipStream_t s);
+// The layer for few tokens with 4-bit experts; Fs = 0: no shared expert.
+size_t mx4_decode_ws(const Dims& d, int64_t Fs);
+hipError_t mx4_decode(const Dims& d, const void* x, const void* w_r, const float* bias, const Mx4& wg, const Mx4& wu,
+                      const Mx4& wd, int64_t Fs, const Mx4& swg, const Mx4& swu, const Mx4& swd, int32_t* topk,
+                      float* gates, void* y, void* ws, hipStream_t s);
+
+// Balance and z loss of given logits, over a checked moe_balance.
+size_t balance_state(const moe_balance& b);
+size_t balance_ws(const moe_balance& b);
+hipError_t balance_loss(const moe_balance& b, const void* logits, const int32_t* topk, const float* bias,
+                        const uint8_t* mask, float* loss, int32_t* counts, void* state, void* ws, hipStream_t s);
+hipError_t balance_loss_bwd(const moe_balance& b, const void* logits, const uint8_t* mask, const void* state,
+                            const float* dloss, void* dlogits, hipStream_t s);
+
 // Residual addition and RMS norm; residual and h null: h is x.
 hipError_t rms_norm(const Dims& d, const void* x, const void* residual, const void* weight, float eps, void* h,
                     void* y, float* rstd, hipStream_t s);

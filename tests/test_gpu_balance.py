@@ -1,0 +1,335 @@
+"""Balance and z loss of router logits (moe_balance_loss) against plain float64.
+
+Tolerances.  u = 2^-24.  expf, logf and the quotients are good to a few u; a float32 sum of m
+positive terms is off by at most m u of it.  With R = max|l| + 10 over finite l:
+  a softmax probability is exp(l - max) / sum: the difference rounded once (R u), so (R + E + 16) u
+  of it; a normalised sigmoid alike;
+  P_s,e adds up a chunk's tokens in float32: (chunk + 16) u more, chunk <= N / 512 + 16;
+  lse: R u + (E + 8) u absolutely, at most (R + E + 8) u, and its square 2 |lse| times that.
+The loss adds alpha times the first and z times the second, and is rounded once.  A gradient
+    c p_e (f_e - f.p) [1 - sigmoid] + zc lse softmax_e
+is off by c p_e (max f (E + 4) u + (|f_e| + |f.p|) (R + E + 24) u) + zc softmax_e (|lse| + 1) (R + E + 24) u, then
+rounded to its type.  Counts are whole numbers."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def logits_of(N, E, dtype, seed=0, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    l = torch.randn((N, E), generator=g, device="cuda") * scale + 0.5 * torch.randn((1, E), generator=g, device="cuda")
+    return l.to(dtype)
+
+
+def order(l, bias, K):
+    """K experts by (value desc, id asc), NaN last, float32 values."""
+    v = l.float() if bias is None else l.float() + bias
+    key = torch.where(torch.isnan(v), torch.full_like(v, -float("inf")), v)
+    rank = torch.sort(torch.isnan(v).int() * 2, dim=1, stable=True)  # NaN behind -inf
+    ids = rank[1]
+    key = torch.gather(key, 1, ids)
+    i = torch.sort(key, dim=1, descending=True, stable=True)[1]
+    return torch.gather(ids, 1, i)[:, :K]
+
+
+def reference(l, topk, mask, T, alpha, z, score):
+    """loss, its bound, counts, gradient and its bound before the rounding, float64."""
+    N, E = l.shape
+    K = topk.shape[1]
+    keep = torch.ones(N, dtype=torch.bool, device=l.device) if mask is None else mask.reshape(N).bool()
+    x = torch.where(keep[:, None], l.double(), torch.zeros_like(l, dtype=torch.float64))
+    ok = (topk >= 0) & (topk < E) & keep[:, None]
+    hits = torch.zeros((N, E), dtype=torch.float64, device=l.device)
+    hits.scatter_add_(1, torch.where(ok, topk, torch.zeros_like(topk)).long(), ok.double())
+    soft, lse = torch.softmax(x, 1), torch.logsumexp(x, 1)
+    sig = torch.sigmoid(x)
+    if score == "softmax":
+        p, rest = soft, torch.ones_like(soft)
+    else:
+        p, rest = torch.exp(torch.nn.functional.logsigmoid(x)), 1 - sig
+        p = p / p.sum(1, keepdim=True)
+    kd = keep.double()[:, None]
+    n = kd.reshape(-1, T).sum(1)
+    seqs, total = int((n > 0).sum()), float(n.sum())
+    nz = n.clamp(min=1)[:, None]
+    f = (hits.reshape(-1, T, E).sum(1)) * E / (K * nz)
+    P = (p * kd).reshape(-1, T, E).sum(1) / nz
+    R = float(x[torch.isfinite(x)].abs().max()) + 10 if x.numel() else 10.0  # exp(-inf) is exactly 0
+    rel = (R + E + 24) * U
+    balance = float((f * P).sum()) * alpha / max(1, seqs)
+    zed = float((lse ** 2 * kd[:, 0]).sum()) * z / max(1.0, total)
+    bound = abs(balance) * (rel + (N / 512 + 64) * U) + abs(z) / max(1.0, total) * float(
+        (2 * lse.abs() * rel * (1 + lse.abs()) + lse ** 2 * (N / 512 + 64) * U).sum())
+    fr = f.repeat_interleave(T, 0)
+    c = (alpha / max(1, seqs) / nz[:, 0]).repeat_interleave(T)[:, None]
+    fp = (fr * p).sum(1, keepdim=True)
+    zc = 2 * z / max(1.0, total)
+    d = (c * p * (fr - fp) * rest + zc * lse[:, None] * soft) * kd
+    ed = abs(c) * p * rest * (fr.amax(1, keepdim=True) * (E + 4) * U + (fr + fp) * rel) + abs(zc) * soft * (
+        lse.abs()[:, None] + 1) * rel
+    return balance + zed, bound + U * abs(balance + zed), hits.sum(0).long(), d, ed * kd
+
+
+def check(l, K, T, alpha, z, score, topk=None, mask=None, bias=None, loss=None, counts=None, d=None):
+    ids = topk if topk is not None else order(l, bias, K)
+    want, tol, hits, dw, ed = reference(l, ids, mask, T, alpha, z, score)
+    assert torch.equal(counts.long(), hits)
+    assert abs(float(loss) - want) <= 1.01 * tol, (float(loss), want, tol)
+    s = 2.0 ** -8 if l.dtype == torch.bfloat16 else U
+    err, lim = (d.double() - dw).abs(), s * dw.abs() + 1.01 * ed + 1e-40
+    assert bool((err <= lim).all()), float((err / lim).max())
+
+
+CASES = [(1, 1, 1, 1), (1, 203, 8, 2), (3, 67, 12, 3), (1, 1, 256, 8), (5, 64, 7, 7), (1, 5000, 64, 6), (4, 513, 60, 4),
+         (2, 300, 33, 5), (8, 16, 128, 8), (3, 130, 100, 2), (1, 700, 255, 8), (2, 1025, 256, 8), (300, 1, 16, 2),
+         (77, 3, 250, 1), (1, 40000, 4, 2)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,E,K", CASES)
+def test_runner(B, T, E, K, dtype, score):
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    N = B * T
+    l = logits_of(N, E, dtype, seed=N + E)
+    r = MoEBalanceRunner(N, E, K, dtype, seq_len=T, alpha=0.02, z_coef=0.005, score=score)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    mask = torch.rand(N, generator=g, device="cuda") < 0.7
+    given = torch.stack([torch.randperm(E, generator=g, device="cuda")[:K] for _ in range(min(N, 50))])
+    given = given.repeat((N + len(given) - 1) // len(given), 1)[:N].to(torch.int32).contiguous()
+    bias = torch.randn(E, generator=g, device="cuda")
+    for kw in (dict(), dict(mask=mask), dict(topk=given), dict(topk=given, mask=mask), dict(bias=bias, mask=mask)):
+        loss = r.forward(l, **kw).clone()
+        d = r.backward().clone()
+        check(l, K, T, 0.02, 0.005, score, loss=loss, counts=r.counts, d=d, **kw)
+        again = r.forward(l, **kw)
+        assert torch.equal(again, loss) and torch.equal(r.backward(), d)  # bit for bit
+
+
+def test_ties_infinities_and_nan():
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    N, E, K = 64, 40, 5
+    l = torch.round(logits_of(N, E, torch.float32, seed=2))     # many equal logits, 0 and -0 among them
+    l[0] = 0.0
+    l[1] = -0.0
+    l[2, ::2] = -float("inf")
+    r = MoEBalanceRunner(N, E, K, torch.float32, alpha=0.1, z_coef=0.01)
+    loss = r.forward(l)
+    check(l, K, N, 0.1, 0.01, "softmax", loss=loss, counts=r.counts, d=r.backward())
+    assert float(r.dlogits[2, ::2].abs().max()) == 0.0
+    # NaN in a token that counts: its gradients and the loss; the others' gradients stay
+    clean = r.dlogits.clone()
+    ids = order(l, None, K).to(torch.int32).contiguous()
+    l[7, 3] = float("nan")
+    loss = r.forward(l, topk=ids)
+    d = r.backward()
+    others = torch.arange(N, device="cuda") != 7
+    assert bool(torch.isnan(loss).all()) and bool(torch.isnan(d[7]).all()) and torch.equal(d[others], clean[others])
+    # in padding it is not looked at
+    mask = others
+    loss = r.forward(l, topk=ids, mask=mask)
+    check(torch.where(mask[:, None], l, torch.zeros_like(l)), K, N, 0.1, 0.01, "softmax", topk=ids, mask=mask, loss=loss,
+          counts=r.counts, d=r.backward())
+    # NaN logits are chosen last
+    l = logits_of(N, E, torch.float32, seed=3)
+    l[:, :E - K] = float("nan")
+    r.forward(l)
+    assert r.counts.tolist() == [0] * (E - K) + [N] * K
+    l[:] = float("nan")
+    r.forward(l)
+    assert r.counts.tolist() == [N] * K + [0] * (E - K)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("shift", [-300.0, -80.0, 60.0, 300.0])
+def test_large_logits(score, shift):
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    N, E, K = 200, 24, 2
+    l = logits_of(N, E, torch.float32, seed=5, scale=3.0) + shift
+    r = MoEBalanceRunner(N, E, K, torch.float32, alpha=0.1, z_coef=1e-4, score=score)
+    loss = r.forward(l)
+    check(l, K, N, 0.1, 1e-4, score, loss=loss, counts=r.counts, d=r.backward())
+
+
+def test_sequences_without_tokens_and_ids_outside():
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    B, T, E, K = 6, 50, 16, 4
+    l = logits_of(B * T, E, torch.bfloat16)
+    r = MoEBalanceRunner(B * T, E, K, torch.bfloat16, seq_len=T, alpha=0.3, z_coef=0.01)
+    mask = torch.ones((B, T), dtype=torch.uint8, device="cuda")
+    mask[1] = 0
+    mask[4] = 0
+    mask[2, 1:] = 0
+    ids = order(l, None, K).to(torch.int32)
+    ids[::3, 2] = -1
+    ids[::5, 0] = E
+    ids[::7, 1] = 2 ** 31 - 1
+    ids = ids.contiguous()
+    loss = r.forward(l, topk=ids, mask=mask)
+    check(l, K, T, 0.3, 0.01, "softmax", topk=ids, mask=mask, loss=loss, counts=r.counts, d=r.backward())
+    mask.zero_()
+    loss = r.forward(l, topk=ids, mask=mask)
+    assert float(loss) == 0.0 and int(r.counts.abs().max()) == 0 and float(r.backward().abs().max()) == 0.0
+    one = MoEBalanceRunner(T, E, K, torch.bfloat16, alpha=0.3, z_coef=0.01)
+    loss = one.forward(l[:T].contiguous(), mask=mask[0].contiguous())
+    assert float(loss) == 0.0 and float(one.backward().abs().max()) == 0.0
+
+
+def test_agrees_with_the_layers_own_loss():
+    """One sequence, softmax scores, no padding: moe_aux_loss on the same logits."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner, MoELayerRunner
+    N, H, F, E, K = 500, 128, 128, 8, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    x = torch.randn((N, H), generator=g, device="cuda")
+    w = [torch.randn(s, generator=g, device="cuda") * 0.1 for s in ((H, E), (E, H, F), (E, H, F), (E, F, H))]
+    layer = MoELayerRunner(N, H, F, E, K, torch.float32, aux_alpha=0.05)
+    layer.forward(x, *w)
+    r = MoEBalanceRunner(N, E, K, torch.float32, alpha=0.05)
+    loss = r.forward((x.double() @ w[0].double()).float(), topk=layer.topk)
+    assert torch.equal(r.counts, layer.counts)
+    assert abs(float(loss) - float(layer.aux_loss)) <= 1e-6 * float(loss)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_autograd(score):
+    from mixture_experts_layer_sort_amd import moe_balance_loss
+    B, T, E, K = 4, 30, 10, 3
+    l = logits_of(B * T, E, torch.float32, seed=9).reshape(B, T, E)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    mask = torch.rand((B, T), generator=g, device="cuda") < 0.8
+    leaf = l.clone().requires_grad_()
+    loss, counts = moe_balance_loss(leaf, K, mask=mask, seq_len=T, alpha=0.2, z_coef=0.03, score=score)
+    assert loss.requires_grad and not counts.requires_grad and counts.dtype == torch.int32
+    (3.0 * loss).sum().backward()
+    flat = l.reshape(B * T, E)
+    check(flat, K, T, 0.2, 0.03, score, mask=mask, loss=loss.detach(), counts=counts, d=leaf.grad.reshape(B * T, E) / 3.0)
+    # against differences of the float64 loss, the choice of experts held
+    ids = order(flat, None, K)
+    h = 1e-6
+    for n, e in ((0, 0), (17, 4), (B * T - 1, 9), (50, 7)):
+        up, dn = flat.double().clone(), flat.double().clone()
+        up[n, e] += h
+        dn[n, e] -= h
+        diff = (reference(up, ids, mask, T, 0.2, 0.03, score)[0] - reference(dn, ids, mask, T, 0.2, 0.03, score)[0]) / (2 * h)
+        # the third derivative's h^2 and the loss's rounding over h, both below 1e-9; the gradient's own 1e-6 of its size
+        assert abs(float(leaf.grad.reshape(-1, E)[n, e]) / 3.0 - diff) <= 1e-8 + 1e-5 * abs(diff)
+    # views at any element, a double use, and a loss that nothing depends on
+    wide = torch.randn((B * T, E + 1), device="cuda", requires_grad=True)
+    a, _ = moe_balance_loss(wide[:, 1:], K, alpha=0.1)
+    b, _ = moe_balance_loss(wide[:, 1:], K, alpha=0.1, z_coef=0.1)
+    (a + b).backward()
+    assert wide.grad.shape == wide.shape and float(wide.grad[:, 0].abs().max()) == 0.0
+    assert bool(torch.isfinite(wide.grad).all()) and float(wide.grad.abs().max()) > 0.0
+    empty = torch.zeros((0, E), device="cuda", requires_grad=True)
+    loss, counts = moe_balance_loss(empty, K)
+    loss.backward()
+    assert float(loss) == 0.0 and int(counts.sum()) == 0 and empty.grad.shape == (0, E)
+
+
+def test_training_step_with_the_layer():
+    """The loss next to the layer in one training step, as a user writes it: gradients reach x and W_r along
+    both paths, the sum of the two taken apart."""
+    from mixture_experts_layer_sort_amd import moe_balance_loss, moe_layer
+    N, H, F, E, K = 96, 128, 128, 8, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    x = torch.randn((N, H), generator=g, device="cuda")
+    w = [torch.randn(s, generator=g, device="cuda") * 0.1 for s in ((H, E), (E, H, F), (E, H, F), (E, F, H))]
+
+    def grads(task, balance):
+        leaves = [t.clone().requires_grad_() for t in (x, *w)]
+        total = 0.0
+        if task:
+            total = total + moe_layer(*leaves, K).square().mean()
+        if balance:
+            total = total + moe_balance_loss(leaves[0] @ leaves[1], K, seq_len=N // 2, alpha=0.5, z_coef=0.1)[0].sum()
+        return torch.autograd.grad(total, leaves, allow_unused=True)
+
+    whole, one, two = grads(True, True), grads(True, False), grads(False, True)
+    for i in range(5):
+        want = one[i] if two[i] is None else one[i] + two[i]
+        assert torch.allclose(whole[i], want, rtol=1e-6, atol=1e-9)
+    assert float(two[0].abs().max()) > 0 and float(two[1].abs().max()) > 0 and two[2] is None
+
+
+def test_refusals_change_nothing():
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner, MoEError, moe_balance_loss
+    N, E, K = 32, 8, 2
+    l = logits_of(N, E, torch.float32)
+    r = MoEBalanceRunner(N, E, K, torch.float32)
+    with pytest.raises(RuntimeError):
+        r.backward()
+    loss = float(r.forward(l))
+    ids = torch.zeros((N, K), dtype=torch.int32, device="cuda")
+    bias = torch.zeros(E, device="cuda")
+    for args in (dict(logits=l[:16]), dict(logits=l.bfloat16()), dict(logits=l, topk=ids.long()),
+                 dict(logits=l, topk=ids[:, :1]), dict(logits=l, topk=ids, bias=bias), dict(logits=l, bias=bias[:4]),
+                 dict(logits=l, mask=torch.ones(N, device="cuda")), dict(logits=l, mask=ids[:16, 0] > 0)):
+        with pytest.raises(ValueError):
+            r.forward(**args)
+    with pytest.raises(ValueError):
+        r.backward(torch.ones(2, device="cuda"))
+    with pytest.raises(ValueError):
+        MoEBalanceRunner(N, E, K, torch.float32, score="relu")
+    for kw in (dict(seq_len=5), dict(alpha=float("nan"))):
+        with pytest.raises(MoEError):
+            MoEBalanceRunner(N, E, K, torch.float32, **kw)
+        with pytest.raises(MoEError):
+            moe_balance_loss(l, K, **kw)
+    with pytest.raises(ValueError):
+        moe_balance_loss(l, K, topk=ids, bias=bias)
+    assert float(r.loss) == loss
+    none = MoEBalanceRunner(0, E, K, torch.float32)
+    assert float(none.forward(l[:0])) == 0.0 and none.backward().shape == (0, E)
+    up = torch.full((1,), -2.5, device="cuda")
+    d = r.backward().clone()
+    assert torch.allclose(r.backward(up), -2.5 * d, rtol=1e-6, atol=0)
+
+
+def test_on_another_stream_and_captured():
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner, moe_balance_loss
+    B, T, E, K = 4, 300, 64, 6
+    l = logits_of(B * T, E, torch.bfloat16)
+    r = MoEBalanceRunner(B * T, E, K, torch.bfloat16, seq_len=T, z_coef=0.01)
+    want = r.forward(l).clone(), r.counts.clone(), r.backward().clone()
+    side = torch.cuda.Stream()
+    for t in (r.loss, r.counts, r.dlogits):
+        t.zero_()
+    torch.cuda.synchronize()
+    r.forward(l, stream=side)
+    r.backward(stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((r.loss, r.counts, r.dlogits), want))
+    graph, leaf = torch.cuda.CUDAGraph(), l.clone().requires_grad_()
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        torch.autograd.grad(moe_balance_loss(leaf, K, seq_len=T, z_coef=0.01)[0], leaf)
+    torch.cuda.current_stream().wait_stream(warm)
+    with torch.cuda.graph(graph):
+        r.forward(l)
+        r.backward()
+        out = moe_balance_loss(leaf, K, seq_len=T, z_coef=0.01)
+        grad, = torch.autograd.grad(out[0], leaf)
+    for i in range(4):
+        new = logits_of(B * T, E, torch.bfloat16, seed=20 + i)
+        l.copy_(new)
+        leaf.data.copy_(new)
+        fresh = MoEBalanceRunner(B * T, E, K, torch.bfloat16, seq_len=T, z_coef=0.01)
+        want = fresh.forward(new).clone(), fresh.counts.clone(), fresh.backward().clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((r.loss, r.counts, r.dlogits), want))
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and torch.equal(grad, want[2])
