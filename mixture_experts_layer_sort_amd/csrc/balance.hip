@@ -23,7 +23,7 @@ using namespace moe;
 
 constexpr int kLanes = 16;       // of a token
 constexpr int kRows = 256 / kLanes;  // tokens a workgroup has under way
-constexpr int64_t kMostChunks = 512;
+constexpr int64_t kMostChunks = 1024;
 
 // Over the sixteen lanes of a token, all of them getting the result: each step
 // takes the value of a lane with the lowest 1, 2, 3, 4 bits of its number mirrored.
@@ -80,44 +80,61 @@ __device__ __forceinline__ void load_row(const T* __restrict__ p, int sub, int E
   }
 }
 
+__device__ __forceinline__ int lanes_sum(int v) {
+  v += MOE_DPP(v, 0xb1);
+  v += MOE_DPP(v, 0x4e);
+  v += MOE_DPP(v, 0x141);
+  return v + MOE_DPP(v, 0x140);
+}
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, uint32_t(MOE_DPP(int(v), 0xb1)));
+  v = max(v, uint32_t(MOE_DPP(int(v), 0x4e)));
+  v = max(v, uint32_t(MOE_DPP(int(v), 0x141)));
+  return max(v, uint32_t(MOE_DPP(int(v), 0x140)));
+}
+
 // Probabilities of one token: soft the softmax, p the score's, rest 1 - sigmoid
-// (sigmoid scores), lse its log-sum-exp.  Places past E hold -inf: 0 in all.
+// (sigmoid scores), lse its log-sum-exp.  Places past E hold -inf: 0 in all.  The
+// hardware's exponential of x / ln 2 is off by about |x| 2^-24 of itself, its
+// reciprocal by one unit in the last place: about a third of the time of the exact
+// functions, which bound the kernel.
 template <int NV> struct Token {
   float soft[NV], p[NV], rest[NV], lse;
   __device__ __forceinline__ void set(const float (&l)[NV], bool sigmoid) {
-    float top = l[0];
-    bool nan = false;
+    float top = l[0];  // of those that are numbers; a NaN reaches the sum
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      top = fmaxf(top, l[v]);
-      nan = nan || l[v] != l[v];
-    }
+    for (int v = 1; v < NV; ++v) top = fmaxf(top, l[v]);
     top = lanes_max(top);
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      soft[v] = expf(l[v] - top);
+      soft[v] = __expf(l[v] - top);
       sum += soft[v];
     }
-    if (nan) sum = __uint_as_float(0x7fc00000u);
     sum = lanes_sum(sum);
     lse = top + logf(sum);
-    const float inv = 1.f / sum;
+    const float inv = __builtin_amdgcn_rcpf(sum);
     if (sigmoid) {
       // Where all logits are negative every sigmoid may be tiny: there all of them
       // over exp(top), whose largest is 1 / (1 + exp(top)).
-      const float down = expf(top);
       float all = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const float t = expf(-fabsf(l[v])), r = 1.f / (1.f + t);
-        const float s = top > 0.f ? (l[v] >= 0.f ? r : t * r) : soft[v] / (1.f + soft[v] * down);
+        const float t = __expf(-fabsf(l[v])), r = __builtin_amdgcn_rcpf(1.f + t);
         rest[v] = l[v] >= 0.f ? t * r : r;
-        p[v] = s;
-        all += s;
+        p[v] = l[v] >= 0.f ? r : t * r;
+        all += p[v];
       }
-      all = lanes_sum(all);
-      const float a = 1.f / all;
+      if (top <= 0.f) {
+        const float down = __expf(top);
+        all = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          p[v] = soft[v] * __builtin_amdgcn_rcpf(1.f + soft[v] * down);
+          all += p[v];
+        }
+      }
+      const float a = __builtin_amdgcn_rcpf(lanes_sum(all));
 #pragma unroll
       for (int v = 0; v < NV; ++v) p[v] *= a;
     }
@@ -129,49 +146,80 @@ template <int NV> struct Token {
   }
 };
 
-// Order of the choice: larger values first, NaN last, equal values (0 and -0 too)
-// by their expert, as one number that is larger the earlier.
-__device__ __forceinline__ uint64_t choice_key(float v, int e) {
-  uint32_t u = __float_as_uint(v + 0.f);
-  u = u & 0x80000000u ? ~u : u | 0x80000000u;
-  if (v != v) u = 0;
-  return uint64_t(u) << 8 | uint64_t(255 - e);
+// Order of the choice: larger values first, NaN last, 0 and -0 equal; 0 is below all.
+__device__ __forceinline__ uint32_t choice_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  const uint32_t key = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return v != v ? 1u : max(key, 2u);
 }
 
-// The K experts of largest value, each counted by the lane that holds it.
-template <int NV, bool VEC>
+// The largest key under `below` of a token: the smallest distance to it, which wraps
+// around to a large one from `below` upwards.
+template <int NV>
+__device__ __forceinline__ uint32_t next_below(const uint32_t (&key)[NV], uint32_t below) {
+  uint32_t d = ~0u;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) d = min(d, below - 1u - key[v]);
+  return below - 1u - ~lanes_max(~d);
+}
+
+// The K experts of largest value, each counted by the lane that holds it.  Only the
+// set matters, so the K-th largest value is found by going down from one value to
+// the next; everything above it is chosen, and of its equals the first ones by their
+// expert.  RARE: equals are rare (float32 logits), so they are looked for at the end
+// only (131072 tokens of 256 experts: a third of the time of counting at each step).
+template <int NV, bool VEC, bool RARE>
 __device__ __forceinline__ void choose(const float (&l)[NV], const float* __restrict__ bias, int sub, int E, int K,
-                                       int* count) {
-  uint64_t key[NV];
+                                       int (&count)[NV]) {
+  uint32_t key[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int e = Place<NV, VEC>::expert(sub, v);
-    // 0 is below every expert's key: NaN and the last expert of 256 give 0 too, so 1 is added
-    key[v] = e < E ? choice_key(bias != nullptr ? l[v] + bias[e] : l[v], e) + 1 : 0;
+    key[v] = e < E ? choice_key(bias != nullptr ? l[v] + bias[e] : l[v]) : 0u;
   }
-  for (int k = 0; k < K; ++k) {
-    uint64_t best = key[0];
+  uint32_t last = ~0u;
+  int left = K, equal = 0;  // still to choose; how many equals the last value has
+  if constexpr (RARE) {
+    for (int k = 0; k < K; ++k) last = next_below(key, last);
+    int got = 0;
 #pragma unroll
-    for (int v = 1; v < NV; ++v) best = key[v] > best ? key[v] : best;
-    uint32_t hi = uint32_t(best >> 32), lo = uint32_t(best);
-#define MOE_STEP(ctrl)                                                                       \
-  {                                                                                          \
-    const uint32_t h = uint32_t(MOE_DPP(int(hi), ctrl)), o = uint32_t(MOE_DPP(int(lo), ctrl)); \
-    const bool more = h > hi || (h == hi && o > lo);                                         \
-    hi = more ? h : hi;                                                                      \
-    lo = more ? o : lo;                                                                      \
+    for (int v = 0; v < NV; ++v) got += key[v] >= last;
+    // no equals among the first K (fewer distinct values than K end at 0, which all keys reach)
+    if (lanes_sum(got) == K) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) count[v] += key[v] >= last;
+      return;
+    }
+    last = ~0u;
   }
-    MOE_STEP(0xb1)
-    MOE_STEP(0x4e)
-    MOE_STEP(0x141)
-    MOE_STEP(0x140)
-#undef MOE_STEP
-    best = uint64_t(hi) << 32 | lo;
+  while (left > 0) {
+    last = next_below(key, last);
+    equal = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) equal += key[v] == last;
+    equal = lanes_sum(equal);
+    left -= equal;
+  }
+  if (left == 0) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) count[v] += key[v] >= last;
+    return;
+  }
+  // of the equals of the last value, -left too many: the first take - by their expert
+  int take = equal + left;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) count[v] += key[v] > last;
+  for (int k = 0; k < take; ++k) {
+    int first = MOE_MAX_EXPERTS;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (key[v] == best) {
+      first = key[v] == last ? min(first, Place<NV, VEC>::expert(sub, v)) : first;
+    first = MOE_MAX_EXPERTS - int(lanes_max(uint32_t(MOE_MAX_EXPERTS - first)));
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (key[v] == last && Place<NV, VEC>::expert(sub, v) == first) {
         key[v] = 0;
-        atomicAdd(count + Place<NV, VEC>::expert(sub, v), 1);
+        ++count[v];
       }
   }
 }
@@ -194,8 +242,12 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
   const int first = int(blockIdx.x % chunks) * chunk, last = min(first + chunk, seq_len);
   const int64_t row0 = int64_t(blockIdx.x / chunks) * seq_len;
   float p[NV], z = 0.f, l[NV], next[NV];
+  int chosen[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) p[v] = 0.f;
+  for (int v = 0; v < NV; ++v) {
+    p[v] = 0.f;
+    chosen[v] = 0;
+  }
   int mine = 0;
   bool live = false, ahead;
   auto fetch = [&](int r, float (&to)[NV]) {
@@ -215,7 +267,7 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
       z += a.lse * a.lse;
       ++mine;
       if (topk == nullptr) {
-        choose<NV, VEC>(l, bias, sub, E, K, count);
+        choose<NV, VEC, sizeof(T) == 4>(l, bias, sub, E, K, chosen);
       } else if (sub < K) {
         const int e = topk[(row0 + r) * K + sub];
         if (e >= 0 && e < E) atomicAdd(count + e, 1);
@@ -226,7 +278,10 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
     for (int v = 0; v < NV; ++v) l[v] = next[v];
   }
 #pragma unroll
-  for (int v = 0; v < NV; ++v) sp[q][Place<NV, VEC>::expert(sub, v)] = p[v];
+  for (int v = 0; v < NV; ++v) {
+    sp[q][Place<NV, VEC>::expert(sub, v)] = p[v];
+    if (chosen[v] > 0) atomicAdd(count + Place<NV, VEC>::expert(sub, v), chosen[v]);
+  }
   if (sub == 0) {
     sz[q] = z;
     atomicAdd(&tokens, mine);
@@ -268,8 +323,8 @@ __device__ __forceinline__ float total_loss(double fp, double z, int64_t seqs, i
   return float(z_coef == 0.f ? balance : balance + double(z_coef) * z / double(tokens));  // no 0 * infinity
 }
 
-// A sequence a workgroup: its chunks added up by 1024 threads, (expert, slice of
-// the chunks), eight loads under way; f, its loss, and with one sequence the rest.
+// A sequence a workgroup of 256 or 1024 threads: its chunks added up by (expert, slice
+// of the chunks), eight loads under way; f, its loss, and with one sequence the rest.
 __global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ parts, float* __restrict__ state,
                                                       SeqSum* __restrict__ sums, int32_t* __restrict__ seq_counts,
                                                       float* __restrict__ loss, int E, int lanes, int K, int chunks,
@@ -278,13 +333,13 @@ __global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ 
   __shared__ int sc[1024];
   __shared__ double sz[16];
   __shared__ int64_t sn[16];
-  const int t = threadIdx.x, s = blockIdx.x, e = t % lanes, slice = t / lanes, slices = 1024 / lanes;
+  const int t = threadIdx.x, nt = blockDim.x, s = blockIdx.x, e = t % lanes, slices = nt / lanes;
   const float* in = parts + int64_t(s) * chunks * part_words(E);
   const int64_t step = part_words(E);
   double p = 0.0;
   int c = 0;
   if (e < E)
-    for (int i0 = slice; i0 < chunks; i0 += 8 * slices) {
+    for (int i0 = t / lanes; i0 < chunks; i0 += 8 * slices) {
       float a[8];
       int b[8];
 #pragma unroll
@@ -301,7 +356,7 @@ __global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ 
     }
   double z = 0.0;
   int64_t n = 0;
-  for (int i = t; i < chunks; i += 1024) {
+  for (int i = t; i < chunks; i += nt) {
     z += double(in[i * step + 2 * E]);
     n += reinterpret_cast<const int*>(in)[i * step + 2 * E + 1];
   }
@@ -311,7 +366,6 @@ __global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ 
       dv += __shfl_xor(dv, off, kWave);
       iv += __shfl_xor(iv, off, kWave);
     }
-    __syncthreads();
     if (lane_id() == 0) {
       sz[t / kWave] = dv;
       sn[t / kWave] = iv;
@@ -319,30 +373,31 @@ __global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ 
     __syncthreads();
     dv = 0.0;
     iv = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < nt / kWave; ++i) {
       dv += sz[i];
       iv += sn[i];
     }
   };
-  over_block(z, n);
   sp[t] = p;
   sc[t] = c;
-  __syncthreads();
+  over_block(z, n);
+  for (int off = nt / 2; off >= lanes; off >>= 1) {
+    if (t < off) {
+      sp[t] += sp[t + off];
+      sc[t] += sc[t + off];
+    }
+    __syncthreads();
+  }
   double fp = 0.0;
   if (t < E) {
-    p = 0.0;
-    c = 0;
-    for (int i = 0; i < slices; ++i) {
-      p += sp[i * lanes + t];
-      c += sc[i * lanes + t];
-    }
+    c = sc[t];
     const double f = n == 0 ? 0.0 : double(E) * double(c) / (double(K) * double(n));
     state[kStateHead + int64_t(s) * (E + 1) + t] = float(f);
     seq_counts[int64_t(s) * E + t] = c;  // the counts themselves where there is one sequence
-    fp = n == 0 ? 0.0 : f * p / double(n);
+    fp = n == 0 ? 0.0 : f * sp[t] / double(n);
   }
   int64_t none = 0;
+  __syncthreads();
   over_block(fp, none);
   if (t == 0) {
     reinterpret_cast<int32_t*>(state)[kStateHead + int64_t(s) * (E + 1) + E] = int32_t(n);
@@ -463,10 +518,12 @@ __global__ __launch_bounds__(256) void k_balance_bwd(const T* __restrict__ logit
   }
 }
 
-// Tokens of a chunk: a sequence in as many as keep their number near kMostChunks in
-// all, a whole number of a workgroup's turns each.
+// Tokens of a chunk, a whole number of a workgroup's turns: one for each CU, then up to four
+// turns, then kMostChunks chunks.  The next launch reads each chunk's sums (4 sequences of 4096
+// tokens, 64 experts: chunks of one turn take 4.5 us and the next launch 10.9, of four turns 5.9
+// and 6.2; 203 tokens of 8 experts: 3.3 and 3.7, 4.5 and 3.7).
 int64_t chunk_of(const moe_balance& b) {
-  const int64_t per = (b.N + kMostChunks - 1) / kMostChunks;
+  const int64_t per = std::max(std::min<int64_t>(4 * kRows, b.N / 256), (b.N + kMostChunks - 1) / kMostChunks);
   return std::min<int64_t>((per + kRows - 1) / kRows * kRows, (b.seq_len + kRows - 1) / kRows * kRows);
 }
 int64_t chunks_of(const moe_balance& b) { return (b.seq_len + chunk_of(b) - 1) / chunk_of(b); }
@@ -506,7 +563,8 @@ hipError_t loss_t(const moe_balance& b, const T* logits, const int32_t* topk, co
   if (st != hipSuccess) return st;
   int lanes = 1;
   while (lanes < b.E) lanes *= 2;
-  k_balance_seq<<<dim3(unsigned(B)), dim3(1024), 0, s>>>(parts, state, sums, seq_counts, loss, int(b.E), lanes,
+  const unsigned threads = lanes * chunks > 2048 ? 1024 : 256;  // lanes is 256 at most
+  k_balance_seq<<<dim3(unsigned(B)), dim3(threads), 0, s>>>(parts, state, sums, seq_counts, loss, int(b.E), lanes,
                                                          int(b.K), int(chunks), int(B), b.alpha, b.z_coef);
   if (B > 1)
     k_balance_total<<<dim3(unsigned(1 + (b.E + 15) / 16)), dim3(256), 0, s>>>(sums, seq_counts, state, counts, loss,
