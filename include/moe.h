@@ -637,7 +637,8 @@ int moe_mx4_dequantize(int32_t order, int64_t count, int64_t k, int64_t cols, in
  *   [NK,F] and ys [NK,H] out, of the type dims->dtype; rows that no tile has
  *   (dropped ones) are left as they were.  gemm_tiles is ignored.  The output
  *   overlaps no other argument.
- * Errors: MOE_EINVAL for a null, misaligned or overlapping pointer. */
+ * Errors: MOE_EINVAL for a null, misaligned or overlapping pointer;
+ * MOE_EUNSUPPORTED for N*H >= 2^33 (moe_mx4_gate_up). */
 int moe_mx4_gate_up(const moe_dims* d, const moe_mx4* x, const int32_t* sorted_flat, const moe_mx4* w_gate,
                     const moe_mx4* w_up, const int32_t* tiles, const int32_t* num_tiles, void* act,
                     hipStream_t stream);

@@ -473,10 +473,11 @@ def moe_mx4_decode_workspace_bytes(d: moe_dims, ds: Optional[moe_dims] = None) -
 
 
 def moe_mx4_decode(d, x, w_r, logit_bias, w_gate, w_up, w_down, ds, ws_gate, ws_up, ws_down, topk_idx, gates, y, ws,
-                   stream=None):
+                   stream=None, ws_bytes=None):
+    """ws: a tensor, or an address and ws_bytes."""
     _call("moe_mx4_decode", ctypes.byref(d), _ptr(x), _ptr(w_r), _ptr(logit_bias), _ref(w_gate), _ref(w_up),
           _ref(w_down), _dims_ref(ds), _ref(ws_gate), _ref(ws_up), _ref(ws_down), _ptr(topk_idx), _ptr(gates),
-          _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream))
+          _ptr(y), _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes, _stream(stream))
 
 
 def moe_balance_state_bytes(b: moe_balance) -> int:
@@ -487,9 +488,11 @@ def moe_balance_workspace_bytes(b: moe_balance) -> int:
     return lib().moe_balance_workspace_bytes(ctypes.byref(b))
 
 
-def moe_balance_loss(b, logits, topk_idx, logit_bias, mask, loss, counts, state, ws, stream=None):
+def moe_balance_loss(b, logits, topk_idx, logit_bias, mask, loss, counts, state, ws, stream=None, sizes=None):
+    """state and ws: tensors, or addresses and their sizes in bytes."""
+    sb, wb = (_nbytes(state), _nbytes(ws)) if sizes is None else sizes
     _call("moe_balance_loss", ctypes.byref(b), _ptr(logits), _ptr(topk_idx), _ptr(logit_bias), _ptr(mask),
-          _ptr(loss), _ptr(counts), _ptr(state), _nbytes(state), _ptr(ws), _nbytes(ws), _stream(stream))
+          _ptr(loss), _ptr(counts), _ptr(state), sb, _ptr(ws), wb, _stream(stream))
 
 
 def moe_balance_loss_bwd(b, logits, mask, state, dloss, dlogits, stream=None):

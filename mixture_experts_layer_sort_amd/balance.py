@@ -61,6 +61,8 @@ class MoEBalanceRunner:
         self.loss = torch.zeros((1,), dtype=torch.float32, device=dev)
         self.counts = torch.zeros((E,), dtype=torch.int32, device=dev)
         self.dlogits = torch.empty((N, E), dtype=dtype, device=dev)
+        self._at = self.loss.data_ptr(), self.counts.data_ptr(), self.state.data_ptr(), self.ws.data_ptr()
+        self._sizes, self._d_at = (state, ws), self.dlogits.data_ptr()
         self.inputs = None
 
     def forward(self, logits, topk=None, mask=None, bias=None, stream=None):
@@ -74,11 +76,12 @@ class MoEBalanceRunner:
             _expect("bias", bias, (self.E,), torch.float32, dev)
             if topk is not None:
                 raise ValueError("a bias moves the choice of experts: it goes without topk")
-        with _stream_of(dev, stream):
-            mask = _mask(mask, self.N, dev)
+        if mask is not None:
+            with _stream_of(dev, stream):
+                mask = _mask(mask, self.N, dev)
         if self.N:
             with _on(dev):
-                L.moe_balance_loss(self.b, logits, topk, bias, mask, self.loss, self.counts, self.state, self.ws, stream)
+                L.moe_balance_loss(self.b, logits, topk, bias, mask, *self._at, stream, self._sizes)
         self.inputs = logits, mask
         return self.loss
 
@@ -91,7 +94,7 @@ class MoEBalanceRunner:
         logits, mask = self.inputs
         if self.N:
             with _on(self.device):
-                L.moe_balance_loss_bwd(self.b, logits, mask, self.state, dloss, self.dlogits, stream)
+                L.moe_balance_loss_bwd(self.b, logits, mask, self._at[2], dloss, self._d_at, stream)
         return self.dlogits
 
 

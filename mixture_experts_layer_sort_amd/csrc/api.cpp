@@ -663,6 +663,8 @@ int moe_mx4_gate_up(const moe_dims* d, const moe_mx4* x, const int32_t* sorted_f
                     hipStream_t stream) {
   MOE_CHECK_DIMS(d, D);
   if (!mx4_ok(x) || !mx4_ok(w_gate) || !mx4_ok(w_up) || !ptrs_ok(sorted_flat, tiles, num_tiles, act)) return MOE_EINVAL;
+  // the rows' codes are addressed by 32 bits from the first token's on
+  if (D.N * D.H >= int64_t(1) << 33) return MOE_EUNSUPPORTED;
   Span s[10] = {{act, size_t(D.NK()) * size_t(D.F) * (D.dtype == MOE_BF16 ? 2 : 4)},
                 {sorted_flat, size_t(D.NK()) * 4},
                 {tiles, size_t(moe_launch::max_tiles(D)) * 12},

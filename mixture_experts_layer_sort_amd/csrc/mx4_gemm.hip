@@ -1,20 +1,25 @@
 // Grouped products over many tokens with rows and experts in 4 bits
-// (moe_mx4_gate_up, moe_mx4_down in moe.h) on the scaled 16x16x128 matrix
+// (moe_mx4_gate_up, moe_mx4_down in moe.h) on the scaled 32x32x64 matrix
 // instruction: products of codes are exact, each block of 32 is scaled by both its
-// powers of two, sums are float32.
+// powers of two, sums are float32.  (The 16x16x128 form takes as long for half the
+// work: 4.9 against 8.3 PFLOP/s in a loop of nothing else.)
 //
-// A workgroup has 16*RG rows of one list tile and 16 strips of 16 columns, each of
-// its four waves all the rows and four strips (of gate/up: two strips of both
-// matrices, so that the activation is formed in registers).  Per step, 512 values
-// of the contraction:
-//  - rows: moved by the LDS DMA in the order in which the instruction takes them
-//    (a lane's 16 bytes from anywhere, so the gather costs nothing; the LDS reads
-//    are contiguous over the lanes), one step ahead, two buffers;
+// A workgroup has 128 rows of one list tile and 16 strips of 16 columns, each of its
+// four waves all the rows and four strips (of gate/up: two strips of both matrices, so
+// that the activation is formed in registers); two workgroups share a CU, so that one
+// of them multiplies while the other waits for its first loads or stores its results.
+// Per step, 256 values of the contraction:
+//  - rows: moved by the LDS DMA one step ahead, two buffers; a wave's request takes
+//    8 rows of 128 bytes, whole cache lines (the gather costs nothing).  Requests of 64
+//    bytes of 16 rows, half a line each, and rows through registers took 2220 us where
+//    this takes 1910 to 1980: gate/up of 16384 tokens, H 4096, F 14336, E 8, K 2;
 //  - weights: each strip is read by one wave only, so they go straight to
-//    registers, a step ahead as well; a load is 1 KiB of contiguous memory;
+//    registers: behind its last product a tile's registers take the same tile of the
+//    next step;
 //  - scales: a word for four tiles of the contraction; the instruction picks the
 //    byte.
-// Weights are the row operand: a lane ends with four neighbouring columns of a row.
+// Weights are the row operand: a lane ends with groups of four neighbouring columns
+// of a row.
 #include <algorithm>
 
 #include "mma_lds.h"
@@ -29,184 +34,291 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kGWaves = 4;
 constexpr int kGNT = kGWaves * kWave;
-constexpr int kStrips = 4;  // of a wave
-constexpr int kStep = 4;    // tiles of a step: a word of scales
+constexpr int kPairs = 2;  // pairs of strips of a wave
 
-template <int RG> struct Stage {
-  static constexpr int A = RG * kStep * 1024;  // [row group][tile][lane][16 bytes]
-  static constexpr int S = RG * 16 * 16;       // [row][16 bytes]
-  static constexpr int BYTES = A + S;
-};
+constexpr int kStep = 2;  // tiles of a step
 
-__device__ __forceinline__ void dma_bytes(const void* g, char* lds_wave) {
-  __builtin_amdgcn_global_load_lds(static_cast<const char*>(g), (LDS_AS void*)lds_wave, 16, 0, 0);
+constexpr int kRows = 128, kGroups = kRows / 32;
+// Of a step, in LDS: the rows, [row][(k/32)%8 ^ row%8][16 bytes] so that 8 rows' blocks lie in all banks, and
+// their scales, [row][16 bytes].
+constexpr int kRowBytes = kRows * 128, kStageBytes = kRowBytes + kRows * 16;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
+}
+// 16 bytes a lane from off to LDS.
+__device__ __forceinline__ void dma_bytes(__amdgpu_buffer_rsrc_t r, uint32_t off, char* lds_wave) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LDS_AS void*)lds_wave, 16, int(off), 0, 0, 0);
+}
+__device__ __forceinline__ i32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// A wave's weights of one step.
+// A wave's weights of one step: lane (h, c) = (lane / 32, lane % 32) holds of pair p the
+// 32 values from 32 (2 * half + h) on of each tile, of column c of the pair.
 struct Weights {
-  i32x4_t b[kStep][kStrips];
-  int s[kStrips];
+  i32x4_t b[kStep][2][kPairs];
+  int s[2][kPairs];
 };
 
-// acc[row group][strip] += weights . rows over one step of `tiles` tiles.
-template <int RG>
-__device__ __forceinline__ void step(const char* __restrict__ rows, const Weights& w, int tiles,
-                                     f32x4_t (&acc)[RG][kStrips]) {
-  const int lane = lane_id(), g = lane / 16, c = lane % 16;
-  int s[RG];
+// acc[row group][pair] += weights . rows over one step, the scales of its first tile
+// `shift` bits up in their words; tiles past the last one have zero weights.  Two row
+// groups at a time; the next two are read while the products of these run (left to
+// itself the compiler reads them right before their use).  behind(n) after batch n of
+// products: memory requests that go out there one or two at a time, as a row of them
+// holds up the wave, and its products.
+constexpr int kBatch = 2, kBatches = 2 * kGroups / kBatch;  // of a tile
+template <typename Behind>
+__device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, int shift,
+                                     f32x16_t (&acc)[kGroups][kPairs], Behind behind) {
+  const int lane = lane_id(), h = lane / 32;
+  const char* mine = rows + lane % 32 * 128;
+  const int first = (h ^ lane % 8) * 16;
+  int s[2][kGroups];
 #pragma unroll
-  for (int r = 0; r < RG; ++r)
-    s[r] = *reinterpret_cast<const int*>(rows + Stage<RG>::A + (r * 16 + c) * 16 + g * 4);
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int r = 0; r < kGroups; ++r)
+      s[f][r] = *reinterpret_cast<const int*>(rows + kRowBytes + (r * 32 + lane % 32) * 16 + (2 * f + h) * 4);
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+#pragma unroll
+    for (int r = 0; r < kGroups; ++r) s[f][r] >>= shift;
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) w.s[f][p] >>= shift;
+  }
+  i32x4_t a[2][kBatch];
+  auto read = [&](int n, i32x4_t (&to)[kBatch]) {  // of all tiles' halves' row groups
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int at = n * kBatch + k, r = at % kGroups, f = at / kGroups % 2, kt = at / (2 * kGroups);
+      to[k] = *reinterpret_cast<const i32x4_t*>(mine + (first ^ (kt * 64 + f * 32)) + r * 4096);
+    }
+  };
+  read(0, a[0]);
   auto tile = [&](auto kt) {
     constexpr int KT = decltype(kt)::value;
 #pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      const i32x4_t a = *reinterpret_cast<const i32x4_t*>(rows + (r * kStep + KT) * 1024 + lane * 16);
-      const i32x8_t x = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+    for (int b = 0; b < kBatches; ++b) {
+      const int n = KT * kBatches + b;
+      if (n + 1 < kStep * kBatches) read(n + 1, a[(n + 1) % 2]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < kStrips; ++i) {
-        const i32x4_t b = w.b[KT][i];
-        acc[r][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8_t{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, x,
-                                                                     acc[r][i], 4, 4, KT, w.s[i], KT, s[r]);
+      for (int k = 0; k < kBatch; ++k) {
+        const int r = (b * kBatch + k) % kGroups, f = (b * kBatch + k) / kGroups;
+        const i32x4_t v = a[n % 2][k];
+        const i32x8_t x = {v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+          const i32x4_t q = w.b[KT][f][p];
+          acc[r][p] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              i32x8_t{q[0], q[1], q[2], q[3], 0, 0, 0, 0}, x, acc[r][p], 4, 4, KT, w.s[f][p], KT, s[f][r]);
+          // in this order: without a side effect products sink to the end of the step, and the
+          // operands of all of them stay in registers until there
+          asm volatile("" : "+v"(acc[r][p]));
+        }
       }
+      __builtin_amdgcn_sched_barrier(0);
+      behind(n);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   tile(std::integral_constant<int, 0>());
-  if (tiles > 1) tile(std::integral_constant<int, 1>());
-  if (tiles > 2) tile(std::integral_constant<int, 2>());
-  if (tiles > 3) tile(std::integral_constant<int, 3>());
+  tile(std::integral_constant<int, 1>());
 }
 
-// The DMA of one step into `to`, then the step before it from `from`: distinct
-// buffers, so that reads of one do not wait for the other.
-template <int RG, typename Fetch>
-__device__ __forceinline__ void fetch_and_step(char* __restrict__ to, const char* __restrict__ from, bool more,
-                                               Fetch fetch, Weights& next, const Weights& w, int tiles,
-                                               f32x4_t (&acc)[RG][kStrips]) {
-  if (more) fetch(to, next);
-  step<RG>(from, w, tiles, acc);
+// One step from `from`, with the requests for the next one, whose rows go to `to`:
+// distinct buffers, so that reads of one do not wait for the other.
+template <typename Request>
+__device__ __forceinline__ void step_and_next(char* __restrict__ to, const char* __restrict__ from, Request request,
+                                              Weights& w, int shift, f32x16_t (&acc)[kGroups][kPairs]) {
+  step(from, w, shift, acc, [&](int n) { request(n, to); });
 }
 
 struct Rows {
   const char *codes, *scales;
-  const int32_t* sorted_flat;  // null: rows as they lie
-  int K;                       // row i is row sorted_flat[i] / K
+  const int32_t* sorted_flat;  // gate/up: row i is row sorted_flat[i] / K
+  int K;
 };
 
+// A lane's 32x32 results, four groups of columns 8q + 4h .. + 3 of row lane % 32, as 16
+// neighbouring columns from 16h on: the halves of the wave exchange two groups each.
+__device__ __forceinline__ void gather_columns(const f32x16_t& v, float (&out)[16]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[4 * q + k]), __float_as_uint(v[4 * q + 8 + k]),
+                                                      false, false);
+      out[8 * q + k] = __uint_as_float(x[0]);
+      out[8 * q + 4 + k] = __uint_as_float(x[1]);
+    }
+}
+
 // G and U of a workgroup's columns (GATE_UP) or one product.
-template <typename T, int RG, bool GATE_UP>
-__global__ __launch_bounds__(kGNT, 1) void k_mx4_product(Rows x, const char* __restrict__ codes0,
+template <typename T, bool GATE_UP>
+__global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __restrict__ codes0,
                                                          const char* __restrict__ scales0,
                                                          const char* __restrict__ codes1,
                                                          const char* __restrict__ scales1,
                                                          const int32_t* __restrict__ tiles,
-                                                         const int32_t* __restrict__ num_tiles, T* __restrict__ out,
-                                                         int L, int C) {
+                                                         const int32_t* __restrict__ num_tiles,
+                                                         T* __restrict__ out, int L, int C) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  typedef Stage<RG> St;
-  constexpr int SUB = 16 / RG, BN = (GATE_UP ? 2 : 4) * 16 * kGWaves;  // columns
-  const int ncols = (C + BN - 1) / BN, nrows = *num_tiles * SUB;
-  const int b = xcd_window_block<32>(blockIdx.x, nrows * ncols);
-  if (b < 0) return;
+  constexpr int SUB = MOE_TILE_M / kRows;
+  constexpr int BN = (GATE_UP ? 1 : 2) * 32 * kGWaves;  // columns
+  const int ncols = (C + BN - 1) / BN, nrows = *num_tiles * SUB, all = nrows * ncols;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
+  const int kts = L / kMxTile, steps = (kts + kStep - 1) / kStep, groups = mx_groups(L);
+  const int64_t strips = C / 16;
+
   // eight row tiles by turns, then the next columns
+  const int b = xcd_window_block<32>(blockIdx.x, all);
+  if (b < 0) return;
   const int group = b / (8 * ncols), in = b % (8 * ncols), high = min(8, nrows - group * 8);
   const int rt = group * 8 + in % high, ct = in / high;
-  const int t = rt / SUB, e = tiles[3 * t], row0 = tiles[3 * t + 1] + rt % SUB * 16 * RG;
-  const int M = min(16 * RG, tiles[3 * t + 2] - rt % SUB * 16 * RG);
+  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  const int e = uniform(tiles[3 * (rt / SUB)]), row0 = uniform(tiles[3 * (rt / SUB) + 1]) + rt % SUB * kRows;
+  const int M = min(kRows, uniform(tiles[3 * (rt / SUB) + 2]) - rt % SUB * kRows);
   if (M <= 0) return;
-  const int wave = threadIdx.x / kWave, lane = lane_id(), g = lane / 16, c = lane % 16;
-  const int kts = L / kMxTile, steps = mx_groups(L);
 
-  // rows past the last repeat it; their results are dropped
-  auto source = [&](int r) -> int64_t {
-    const int i = row0 + min(r, M - 1);
-    return x.sorted_flat != nullptr ? x.sorted_flat[i] / x.K : i;
-  };
-  const char* px[RG / kGWaves];
+  // the wave's strips, two a pair; a pair past the last column repeats the last one, its results
+  // are dropped (C is a multiple of 32)
+  __amdgpu_buffer_rsrc_t pw[kPairs], pws[kPairs];
 #pragma unroll
-  for (int j = 0; j < RG / kGWaves; ++j)
-    px[j] = x.codes + source((wave * (RG / kGWaves) + j) * 16 + c) * (L / 2) + g * 16;
-  // scales of 64 rows an instruction
-  const char* ps = x.scales + source((wave * kWave + lane) % (16 * RG)) * steps * 16;
-
-  // the wave's strips; those past the last column repeat it, their results are dropped
-  const int64_t strips = C / 16;
-  const char *pw[kStrips], *pws[kStrips];
-#pragma unroll
-  for (int i = 0; i < kStrips; ++i) {
-    const int64_t s = GATE_UP ? ct * (BN / 16) + wave * 2 + i % 2
-                              : min(int64_t(ct) * (BN / 16) + wave * kStrips + i, strips - 1);
-    pw[i] = (GATE_UP && i >= 2 ? codes1 : codes0) + (mx_strip_codes(e * strips + s, L) + lane) * 16;
-    pws[i] = (GATE_UP && i >= 2 ? scales1 : scales0) + (mx_strip_scales(e * strips + s, L) + lane) * 4;
+  for (int p = 0; p < kPairs; ++p) {
+    const int64_t s = e * strips + min(int64_t(ct) * (BN / 16) + (GATE_UP ? wave * 2 : wave * 4 + 2 * p), strips - 2);
+    pw[p] = resource((GATE_UP && p > 0 ? codes1 : codes0) + mx_strip_codes(s, L) * 16, 2 * kts * 1024);
+    pws[p] = resource((GATE_UP && p > 0 ? scales1 : scales0) + mx_strip_scales(s, L) * 4, 2 * groups * kWave * 4);
   }
-
-  int q = 0;  // the step that fetch() is for
-  auto fetch = [&](char* to, Weights& w) {
-    const int n = min(kStep, kts - q * kStep);
+  // a lane's place behind the first strip of a pair
+  const uint32_t lane_code = lane % 32 / 16 * uint32_t(kts * 1024) + lane / 32 * 256 + lane % 16 * 16;
+  const uint32_t lane_scale = lane % 32 / 16 * uint32_t(groups * 256) + lane / 32 * 64 + lane % 16 * 4;
+  auto fetch_scales = [&](int q, int (&to)[2][kPairs]) {
 #pragma unroll
-    for (int i = 0; i < kStrips; ++i) w.s[i] = *reinterpret_cast<const int*>(pws[i] + int64_t(q) * kWave * 4);
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
-    for (int kt = 0; kt < kStep; ++kt)
-      if (kt < n) {
-#pragma unroll
-        for (int i = 0; i < kStrips; ++i)
-          w.b[kt][i] = *reinterpret_cast<const i32x4_t*>(pw[i] + (int64_t(q) * kStep + kt) * 1024);
-#pragma unroll
-        for (int j = 0; j < RG / kGWaves; ++j)
-          dma_bytes(px[j] + (q * kStep + kt) * 64, to + ((wave * (RG / kGWaves) + j) * kStep + kt) * 1024);
-      }
-    if (wave * kWave < 16 * RG) dma_bytes(ps + q * 16, to + St::A + wave * 1024);
-    ++q;
+      for (int p = 0; p < kPairs; ++p)
+        to[f][p] = __builtin_amdgcn_raw_buffer_load_b32(pws[p], lane_scale + q * kStep / 4 * (kWave * 4) + f * 128, 0, 0);
+  };
+  // Load j (half, pair) of tile k of step q.  Past the last tile it is asked for past the end of the
+  // strips, which gives 0 without a branch around the load (its registers would be doubled).
+  constexpr int PARTS = 2 * kPairs, LOADS = kStep * PARTS;  // of a tile's, of a step's weights
+  auto fetch_tile = [&](int q, int k, int j, Weights& w) {
+    const int kt = q * kStep + k;
+    const uint32_t at = lane_code + (kt < kts ? uint32_t(kt) * 1024u : 1u << 31);
+    w.b[k][j / kPairs][j % kPairs] = load16(pw[j % kPairs], at + j / kPairs * 512);
   };
 
-  f32x4_t acc[RG][kStrips];
+  // Rows past the last repeat it; their results are dropped.  32-bit offsets: of all tokens for gathered
+  // rows, else of the piece's.
+  auto source = [&](int r) -> uint32_t {
+    const int i = min(r, M - 1);
+    return GATE_UP ? uint32_t(x.sorted_flat[row0 + i]) / uint32_t(x.K) : i;
+  };
+  const char* codes = x.codes + (GATE_UP ? 0 : int64_t(row0) * (L / 2));
+  const char* scales = x.scales + (GATE_UP ? 0 : int64_t(row0) * groups * 16);
+  // a request takes 8 rows, lane (r, b) the block of row r whose place in LDS is b; the last one scales of 64
+  // rows (of waves 0 and 1)
+  constexpr int REQUESTS = kRows / 8 / kGWaves, MOVED = REQUESTS + 1;
+  const uint32_t block = (lane % 8 ^ lane / 8) * 16;
+  uint32_t px[MOVED];
 #pragma unroll
-  for (int r = 0; r < RG; ++r)
+  for (int j = 0; j < REQUESTS; ++j) px[j] = source((wave * REQUESTS + j) * 8 + lane / 8) * uint32_t(L / 2) + block;
+  px[REQUESTS] = source(wave * kWave + lane) * uint32_t(groups * 16);
+  // Request n of step q's rows.  An odd last tile is brought twice; past the last step nothing is (zeros).
+  auto fetch_rows = [&](int q, int n, char* to) {
+    const int live = uniform(q < steps ? -1 : 0);
+    if (n < REQUESTS) {
+      dma_bytes(resource(codes + q * 128, live), px[n] - (2 * q + 1 < kts ? 0 : block & 64), to + (wave * REQUESTS + n) * 1024);
+    } else if (wave * kWave < kRows) {
+      dma_bytes(resource(scales + q * kStep / 4 * 16, live), px[REQUESTS], to + kRowBytes + wave * 1024);
+    }
+  };
+
+  Weights w;
 #pragma unroll
-    for (int i = 0; i < kStrips; ++i) acc[r][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  Weights w, next;
-  fetch(lds, w);
+  for (int k = 0; k < MOVED; ++k) fetch_rows(0, k, lds);
+  fetch_scales(0, w.s);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int k = 0; k < LOADS; ++k) fetch_tile(0, k / PARTS, k % PARTS, w);
+  f32x16_t acc[kGroups][kPairs];
+#pragma unroll
+  for (int r = 0; r < kGroups; ++r)
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[r][p][k] = 0.f;
+#pragma clang loop unroll(disable)
   for (int i = 0; i < steps; ++i) {
-    wait_vm<0>();
+    wait_vm<LOADS>();  // the rows are here; the weights behind them may still be on their way
     lds_barrier();
-    fetch_and_step<RG>(lds + (i + 1) % 2 * St::BYTES, lds + i % 2 * St::BYTES, i + 1 < steps, fetch, next, w,
-                       min(kStep, kts - i * kStep), acc);
-    w = next;
+    int s[2][kPairs];
+    // Behind the batches of the first tile the next step's rows are asked for, behind those of the second
+    // the weights of the first.  Past the last step too, where they bring nothing: with as many requests on
+    // every path, the compiler's waits need not take the fewest.
+    constexpr int EACH = (PARTS + kBatches - 1) / kBatches, TWO = (MOVED + kBatches - 1) / kBatches;
+    auto request = [&](int n, char* to) {
+      const int b = n % kBatches;
+      if (n == 0) fetch_scales(i + 1, s);
+      if (n < kBatches) {
+#pragma unroll
+        for (int k = TWO * b; k < TWO * b + TWO; ++k)
+          if (k < MOVED) fetch_rows(i + 1, k, to);
+      } else {
+#pragma unroll
+        for (int k = EACH * b; k < EACH * b + EACH; ++k)
+          if (k < PARTS) fetch_tile(i + 1, 0, k, w);
+      }
+      if (n + 1 == 2 * kBatches) {
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) fetch_tile(i + 1, 1, k, w);
+      }
+    };
+    step_and_next(lds + (i + 1) % 2 * kStageBytes, lds + i % 2 * kStageBytes, request, w, i % 2 * 16, acc);
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) w.s[f][p] = s[f][p];
   }
 
-  constexpr int PAIRS = GATE_UP ? 2 : kStrips;
+  // 32-bit offsets from the piece's first row
+  const uint32_t mine = (lane % 32 * uint32_t(C) + lane / 32 * 16) * uint32_t(sizeof(T));
 #pragma unroll
-  for (int r = 0; r < RG; ++r) {
-    const int row = r * 16 + c;
-    if (row >= M) continue;
+  for (int r = 0; r < kGroups; ++r) {
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-      const int col = (ct * (BN / 16) + wave * PAIRS + i) * 16 + 4 * g;
-      if (!GATE_UP && col >= C) continue;
-      f32x4_t v = acc[r][i];
+    for (int p = 0; p < (GATE_UP ? 1 : kPairs); ++p) {
+      const int col = ct * BN + (GATE_UP ? wave * 32 : wave * 64 + 32 * p);
+      f32x16_t v = acc[r][p];
       if constexpr (GATE_UP) {
-        // the hardware's reciprocal is good to 1 ulp
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = v[k] * __builtin_amdgcn_rcpf(1.0f + expf(-v[k])) * acc[r][i + 2][k];
+        for (int k = 0; k < 16; ++k) v[k] = silu_f32(v[k]) * acc[r][1][k];
       }
-      T* to = out + int64_t(row0 + row) * C + col;
-      if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<f32x4_t*>(to) = v;
-      else
-        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      float o[16];
+      gather_columns(v, o);
+      char* to = reinterpret_cast<char*>(out + int64_t(row0 + r * 32) * C + col);
+      if (r * 32 + lane % 32 < M && col < C) {
+#pragma unroll
+        for (int k = 0; k < 16; k += Vec16<T>::n)
+          Vec16<T>::store(reinterpret_cast<T*>(to + mine + k * sizeof(T)), o + k);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one group's registers at a time
     }
   }
+  wait_vm<0>();  // the LDS is given back only when nothing more goes there
 }
 
-template <typename T, int RG, bool GATE_UP>
+template <typename T, bool GATE_UP>
 hipError_t product(const moe_launch::Dims& d, const Rows& x, const moe_launch::Mx4& w0, const moe_launch::Mx4& w1,
                    const int32_t* tiles, const int32_t* num_tiles, T* out, int L, int C, hipStream_t s) {
-  constexpr int bytes = 2 * Stage<RG>::BYTES, BN = (GATE_UP ? 2 : 4) * 16 * kGWaves;
-  const hipError_t e = allow_lds<k_mx4_product<T, RG, GATE_UP>>(bytes);
+  constexpr int bytes = 2 * kStageBytes, BN = (GATE_UP ? 1 : 2) * 32 * kGWaves;
+  const hipError_t e = allow_lds<k_mx4_product<T, GATE_UP>>(bytes);
   if (e != hipSuccess) return e;
-  const int64_t blocks = moe_launch::max_tiles(d) * (16 / RG) * ((C + BN - 1) / BN);
-  if (blocks > (int64_t(1) << 31) - 256) return hipErrorInvalidValue;
-  k_mx4_product<T, RG, GATE_UP><<<dim3(unsigned((blocks + 255) / 256 * 256)), dim3(kGNT), bytes, s>>>(
+  const int64_t pieces = moe_launch::max_tiles(d) * (MOE_TILE_M / kRows) * ((C + BN - 1) / BN);
+  if (pieces > (int64_t(1) << 31) - 512) return hipErrorInvalidValue;
+  const unsigned grid = unsigned((pieces + 255) / 256 * 256);
+  k_mx4_product<T, GATE_UP><<<dim3(grid), dim3(kGNT), bytes, s>>>(
       x, static_cast<const char*>(w0.codes), static_cast<const char*>(w0.scales),
       static_cast<const char*>(w1.codes), static_cast<const char*>(w1.scales), tiles, num_tiles, out, L, C);
   return hipGetLastError();
@@ -215,17 +327,9 @@ hipError_t product(const moe_launch::Dims& d, const Rows& x, const moe_launch::M
 template <bool GATE_UP>
 hipError_t product_any(const moe_launch::Dims& d, const Rows& x, const moe_launch::Mx4& w0, const moe_launch::Mx4& w1,
                        const int32_t* tiles, const int32_t* num_tiles, void* out, int L, int C, hipStream_t s) {
-  const double rows = double(d.NK()) / double(d.E);
-  auto run = [&](auto rg) {
-    constexpr int RG = decltype(rg)::value;
-    return d.dtype == MOE_BF16 ? product<bf16_t, RG, GATE_UP>(d, x, w0, w1, tiles, num_tiles,
-                                                              static_cast<bf16_t*>(out), L, C, s)
-                               : product<float, RG, GATE_UP>(d, x, w0, w1, tiles, num_tiles,
-                                                             static_cast<float*>(out), L, C, s);
-  };
-  return rows <= 64.0    ? run(std::integral_constant<int, 4>())
-         : rows <= 160.0 ? run(std::integral_constant<int, 8>())
-                         : run(std::integral_constant<int, 16>());
+  return d.dtype == MOE_BF16
+             ? product<bf16_t, GATE_UP>(d, x, w0, w1, tiles, num_tiles, static_cast<bf16_t*>(out), L, C, s)
+             : product<float, GATE_UP>(d, x, w0, w1, tiles, num_tiles, static_cast<float*>(out), L, C, s);
 }
 
 Rows rows_of(const moe_launch::Mx4& x, const int32_t* sorted_flat, int64_t K) {

@@ -102,12 +102,14 @@ class MoEMx4DecodeRunner:
             raise L.MoEError("moe_mx4_decode_workspace_bytes",
                              L.MOE_EUNSUPPORTED if max_tokens > L.MOE_DECODE_MAX_TOKENS else L.MOE_EINVAL)
         self.device = dev = _cuda_device(device)
-        self.ws = torch.empty((max(16, max(need)),), dtype=torch.uint8, device=dev)
+        self._ws_bytes = max(16, *need)
+        self.ws = torch.empty((self._ws_bytes,), dtype=torch.uint8, device=dev)
         self._topk = torch.empty((max_tokens, K), dtype=torch.int32, device=dev)
         self._gates = torch.empty((max_tokens, K), dtype=torch.float32, device=dev)
         self._y = torch.empty((max_tokens, H), dtype=dtype, device=dev)
         self.topk, self.gates, self.y = self._topk, self._gates, self._y
-        self._at = self._topk.data_ptr(), self._gates.data_ptr(), self._y.data_ptr()  # of any first n rows too
+        # of any first n rows too
+        self._at = self._topk.data_ptr(), self._gates.data_ptr(), self._y.data_ptr(), self.ws.data_ptr()
 
     def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None, shared=None):
         """Returns y [n, H] of x [n, H], n <= max_tokens; topk and gates [n, K]
@@ -124,10 +126,10 @@ class MoEMx4DecodeRunner:
         _expect("w_r", w_r, (H, E), dt, dev)
         if bias is not None:
             _expect("bias", bias, (E,), torch.float32, dev)
-        w = [_expect_mx4(name, q, L.MOE_MX4_WEIGHTS, shape, dev)
-             for name, q, shape in (("w_gate", w_gate, (E, H, F)), ("w_up", w_up, (E, H, F)),
-                                    ("w_down", w_down, (E, F, H)))]
-        s = [None] * 3
+        w = (_expect_mx4("w_gate", w_gate, L.MOE_MX4_WEIGHTS, (E, H, F), dev),
+             _expect_mx4("w_up", w_up, L.MOE_MX4_WEIGHTS, (E, H, F), dev),
+             _expect_mx4("w_down", w_down, L.MOE_MX4_WEIGHTS, (E, F, H), dev))
+        s = (None, None, None)
         if shared is not None:
             Fs = self.shared_ffn
             s = [_expect_mx4(name, q, L.MOE_MX4_WEIGHTS, shape, dev)
@@ -136,7 +138,7 @@ class MoEMx4DecodeRunner:
         d, ds = self._dims[n]
         if n:
             with _on(dev):
-                L.moe_mx4_decode(d, x, w_r, bias, *w, ds, *s, *self._at, self.ws, stream)
+                L.moe_mx4_decode(d, x, w_r, bias, *w, ds, *s, *self._at, stream, self._ws_bytes)
         if n != self.y.shape[0]:  # not before the call: a refused one changes nothing
             self.topk, self.gates, self.y = self._topk[:n], self._gates[:n], self._y[:n]
         return self.y

@@ -245,6 +245,25 @@ def test_products(dtype, N, H, F, E, K, counts):
     assert torch.equal(r.gate_up(xq, qg, qu), act) and torch.equal(r.down(aq, qd), ys)  # bit for bit
 
 
+def test_gathered_rows_past_2_gib():
+    """The last of 400000 tokens of 16384 values, their codes 3 GiB from the first, as in a tensor of their own."""
+    from mixture_experts_layer_sort_amd import MoEMx4Runner, MoEMx4Tensor as Q
+    N, H, F, last = 400000, 16384, 128, 333
+    w = Q.weights(randn(1, 1, H, F, scale=H ** -0.5)), Q.weights(randn(2, 1, H, F, scale=H ** -0.5))
+    some = Q.rows(randn(3, last, H))
+    many = Q(some.order, (N, H), "cuda")
+    many.codes.zero_()
+    many.scales.fill_(127)
+    many.codes.view(N, -1)[-last:] = some.codes.view(last, -1)
+    many.scales.view(N, -1)[-last:] = some.scales.view(last, -1)
+    out = []
+    for q, n in ((many, N), (some, last)):
+        r = MoEMx4Runner(n, H, F, 1, 1, torch.bfloat16)
+        r.meta(torch.zeros((n, 1), dtype=torch.int32, device="cuda"))
+        out.append(r.gate_up(q, *w)[-last:])
+    assert bool(out[1].any()) and torch.equal(*out)
+
+
 def test_products_leave_dropped_rows():
     from mixture_experts_layer_sort_amd import MoEMx4Runner, MoEMx4Tensor as Q
     N, H, F, E, K = 200, 256, 256, 3, 2
