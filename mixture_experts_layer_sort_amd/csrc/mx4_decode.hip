@@ -8,8 +8,8 @@
 //    order in which a wave takes it: a 16-byte load a lane is a tile of 128 rows,
 //    lane (g, c) holding the 32 values from 32g on of column c.  A strip can be as
 //    narrow as that without reading less than whole lines, so work is dealt to
-//    workgroups in strips and not in parts of the contraction, and no partial sums
-//    travel through memory between workgroups.
+//    workgroups in strips, and in parts of the contraction, whose sums travel through
+//    memory, only for long down products of few experts.
 //  - The four waves of a workgroup (sixteen where one token leaves few strips)
 //    split the contraction; their float32 sums meet in LDS in wave order.
 //  - Eight values of a lane are one operand of a 16x16x32 bf16 matrix instruction:
@@ -232,6 +232,7 @@ __device__ __forceinline__ void join(const f32x4_t (&acc)[MT][NM * CG], f32x4_t*
 // What the kernels share.
 struct Shape {
   int N, H, F, Fs, E, K, units;
+  int parts;  // of the down contraction
 };
 
 // Weights of one form: codes and scales of all experts.
@@ -406,11 +407,11 @@ __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_gate_up(
   }
 }
 
-// CG strips of one expert's down product for the M rows slot(0 ..): sums to
-// out[slot][H].
+// CG strips of one expert's down product for the M rows slot(0 ..), the contraction's
+// tiles from .. to (`from` a multiple of 4): sums to out[slot][H].
 template <int MT, int CG, int PA, typename Slot>
 __device__ __forceinline__ void down_rows(const Operands& a, const Strips& w, int64_t col0, int64_t H, Slot slot,
-                                          int M, float* out, f32x4_t* red) {
+                                          int M, float* out, int from, int to, f32x4_t* red) {
   constexpr int U = kUnroll<CG, MT, PA>;
   const int c = lane_id() % 16, wave = wave_id();
   f32x4_t acc[MT][CG];
@@ -418,14 +419,14 @@ __device__ __forceinline__ void down_rows(const Operands& a, const Strips& w, in
   int at[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) at[m] = slot(16 * m + c < M ? 16 * m + c : 0);
-  for (int kt = wave * U; kt < w.tiles; kt += kWaves * U) multiply<MT, 1, CG, U, PA>(w, a, kt, at, acc);
+  for (int kt = from + wave * U; kt < to; kt += kWaves * U) multiply<MT, 1, CG, U, PA>(w, a, kt, at, acc);
   join<MT, 1, CG, kWaves>(acc, red, [&](int m, int s, int lane, const f32x4_t* v) {
     const int r = 16 * m + lane % 16;
     if (r < M) *reinterpret_cast<f32x4_t*>(out + slot(r) * H + col0 + 16 * s + 4 * (lane / 16)) = v[0];
   });
 }
 
-// More than one token: ys [slot][H], then sys [token][H] of the shared expert.  Pieces
+// More than one token: ys [part][slot][H], then sys [part][token][H] of the shared expert.  Pieces
 // as in k_mx4_gate_up.
 template <int MTMAX, int CG, int PA>
 __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_down(const bf16_t* __restrict__ act,
@@ -436,11 +437,12 @@ __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_down(const bf16_
   __shared__ Units units;
   __shared__ f32x4_t red[kWaves * CG * kWave];
   const int found = uniform(find_units(topk, q.N * q.K, &units));
-  const int chunks = q.H / (16 * CG), shared = q.Fs > 0 ? chunks : 0, all = shared + found * chunks;
+  const int chunks = q.H / (16 * CG), each = chunks * q.parts, shared = q.Fs > 0 ? each : 0, all = shared + found * each;
   for (int i = blockIdx.x; i < all; i += gridDim.x) {
-    const int b = i - shared, u = b < 0 ? 0 : b / chunks, F = b < 0 ? q.Fs : q.F;
+    const int b = i - shared, u = b < 0 ? 0 : b / each, F = b < 0 ? q.Fs : q.F, part = i % each / chunks;
     const bool routed = b >= 0;
     const int64_t col0 = int64_t(i % chunks) * 16 * CG;
+    const int per = (F / kMxTile + 4 * q.parts - 1) / (4 * q.parts) * 4;  // tiles of a part
     const int64_t strip = (routed ? uniform(units.expert[u]) * int64_t(q.H / 16) : 0) + col0 / 16, R = routed ? q.N * q.K : q.N;
     const View& d = routed ? wd : swd;
     const Strips w{{d.code(strip, F), nullptr}, {d.scale(strip, F), nullptr}, F / kMxTile};
@@ -449,7 +451,7 @@ __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_down(const bf16_
       down_rows<decltype(mt)::value, CG, PA>(
           packed(routed ? act : sact, R, F), w, col0, q.H,
           [&](int r) { return routed ? int64_t(units.slots[first + m0 + r]) : int64_t(m0 + r); }, m,
-          routed ? ys : sys, red);
+          (routed ? ys : sys) + part * R * q.H, part * per, min((part + 1) * per, F / kMxTile), red);
     });
   }
 }
@@ -504,7 +506,7 @@ struct Plan {
 // Strips of a piece, of `strips` in all: the rows are read again for each piece, so as many as
 // leave every CU one (8 strips of both kinds of product at most: their sums take the registers).
 // 64 tokens of 8 experts, H 4096, F 14336: gate/up 98 us with four strips of both matrices, 114 with
-// two, 160 with one; down 83 with eight, 85 with four, 127 with two.
+// two, 160 with one; down (whole contractions) 83 with eight, 85 with four, 127 with two.
 int strips_of(int64_t strips, int most) {
   int cg = most;
   while (cg > 1 && strips / cg < kCUs) cg /= 2;
@@ -513,7 +515,7 @@ int strips_of(int64_t strips, int most) {
 
 Plan plan(const moe_launch::Dims& d, int64_t Fs) {
   Plan p;
-  p.q = Shape{int(d.N), int(d.H), int(d.F), int(Fs), int(d.E), int(d.K), int(std::min(d.NK(), d.E))};
+  p.q = Shape{int(d.N), int(d.H), int(d.F), int(Fs), int(d.E), int(d.K), int(std::min(d.NK(), d.E)), 1};
   const bool bf = d.dtype == MOE_BF16;
   const int64_t NK = d.NK(), px = bf ? 1 : 3, pa = bf ? 2 : 3;
   const double used = double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N)));
@@ -521,8 +523,13 @@ Plan plan(const moe_launch::Dims& d, int64_t Fs) {
   p.route = d.N <= 16 && d.N * d.E <= kPairs;
   const bool small_router = (d.E + 15) / 16 * (d.H / 32) <= 4 * kWaves;
   p.logit_parts = p.route && small_router && bf && d.N <= 4 ? 0 : int((d.H + kLogitRows - 1) / kLogitRows);
-  p.gu_cg = strips_of(int64_t(used * double(d.F / 16)) + Fs / 16, 4);
-  p.dn_cg = strips_of(int64_t(used * double(d.H / 16)), 8);
+  p.gu_cg = strips_of(std::llround(used * double(d.F / 16)) + Fs / 16, 4);
+  const int64_t strips = std::llround(used * double(d.H / 16));
+  p.dn_cg = strips_of(strips, 8);
+  // Where that leaves a CU few pieces, each takes a part of the contraction, 16 tiles or more: pieces of
+  // experts with more rows take longer.  The parts' sums meet in the kernel that adds a token's.
+  // 64 tokens of 8 experts, H 4096, F 14336: down and that kernel 79 us with four parts, 90 with one.
+  p.q.parts = d.N == 1 ? 1 : int(std::max<int64_t>(1, std::min<int64_t>(d.F / kMxTile / 16, 4 * kCUs * p.dn_cg / strips)));
   p.row_tiles = d.N <= 16 ? 1 : std::max(rows, Fs > 0 ? double(d.N) : 0.0) > 24.0 ? 4 : 2;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -534,8 +541,8 @@ Plan plan(const moe_launch::Dims& d, int64_t Fs) {
   p.xp = take(p.logit_parts == 0 ? 0 : size_t(px) * d.N * d.H * 2);
   p.act = take(size_t(pa) * NK * d.F * 2);
   p.sact = take(size_t(pa) * d.N * Fs * 2);
-  p.ys = take(d.N == 1 ? 0 : size_t(NK) * d.H * 4);
-  p.sys = take(d.N == 1 || Fs == 0 ? 0 : size_t(d.N) * d.H * 4);
+  p.ys = take(d.N == 1 ? 0 : size_t(p.q.parts) * NK * d.H * 4);
+  p.sys = take(d.N == 1 || Fs == 0 ? 0 : size_t(p.q.parts) * d.N * d.H * 4);
   p.bytes = at;
   return p;
 }
@@ -591,11 +598,12 @@ hipError_t down(const Plan& p, const Args<T>& a, hipStream_t s) {
   float* ys = reinterpret_cast<float*>(a.ws + p.ys);
   float* sys = reinterpret_cast<float*>(a.ws + p.sys);
   k_mx4_down<MTMAX, CG, sizeof(T) == 2 ? 2 : 3>
-      <<<grid_of((int64_t(q.units) + (q.Fs > 0 ? 1 : 0)) * q.H / (16 * CG)), dim3(kNT), 0, s>>>(
+      <<<grid_of((int64_t(q.units) + (q.Fs > 0 ? 1 : 0)) * q.parts * q.H / (16 * CG)), dim3(kNT), 0, s>>>(
           reinterpret_cast<const bf16_t*>(a.ws + p.act), reinterpret_cast<const bf16_t*>(a.ws + p.sact), a.wd, a.swd,
           a.topk, ys, sys, q);
   MOE_LAUNCHED()
-  k_decode_combine<T><<<dim3(q.H / 64, q.N), dim3(256), 0, s>>>(ys, sys, a.y, q.N, q.H, q.K, 1, q.Fs > 0 ? 1 : 0);
+  k_decode_combine<T><<<dim3(q.H / 64, q.N), dim3(256), 0, s>>>(ys, sys, a.y, q.N, q.H, q.K, q.parts,
+                                                                       q.Fs > 0 ? q.parts : 0);
   return hipGetLastError();
 }
 

@@ -347,7 +347,8 @@ DECODE = [(1, 128, 128, 1, 1, 0, False), (1, 512, 1024, 8, 2, 0, False), (1, 640
           (13, 512, 640, 64, 6, 896, True), (16, 384, 512, 4, 1, 0, False), (17, 256, 384, 2, 2, 128, False),
           (24, 640, 256, 1, 1, 0, False), (33, 256, 256, 3, 2, 0, True), (48, 128, 640, 8, 2, 256, False),
           (64, 512, 384, 8, 2, 0, False), (64, 384, 256, 1, 1, 512, False), (64, 256, 256, 200, 8, 0, False),
-          (40, 128, 2176, 2, 1, 0, False)]
+          (40, 128, 2176, 2, 1, 0, False), (20, 128, 4096, 4, 2, 1152, False), (9, 128, 4352, 2, 1, 128, True),
+          (2, 256, 6144, 3, 2, 0, False)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
