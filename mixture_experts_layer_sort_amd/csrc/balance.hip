@@ -23,7 +23,7 @@ using namespace moe;
 
 constexpr int kLanes = 16;       // of a token
 constexpr int kRows = 256 / kLanes;  // tokens a workgroup has under way
-constexpr int64_t kMostChunks = 1024;
+constexpr int64_t kMostChunks = 768;  // three workgroups a CU: what the registers allow
 
 // Over the sixteen lanes of a token, all of them getting the result: each step
 // takes the value of a lane with the lowest 1, 2, 3, 4 bits of its number mirrored.
@@ -38,9 +38,10 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
 __device__ __forceinline__ float lanes_sum(float v) {
   return over_lanes(v, [](float a, float b) { return a + b; });
 }
-__device__ __forceinline__ float lanes_max(float v) {
-  return over_lanes(v, [](float a, float b) { return fmaxf(a, b); });
-}
+// The larger one; of a number and NaN the number.  (fmaxf makes its operands quiet
+// first, an instruction for each.)
+__device__ __forceinline__ float max_of(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ float lanes_max(float v) { return over_lanes(v, max_of); }
 
 // A token's NV * 16 >= E values over its lanes: VEC, four neighbours at a time
 // (E a multiple of 4), else every sixteenth.
@@ -103,7 +104,7 @@ template <int NV> struct Token {
   __device__ __forceinline__ void set(const float (&l)[NV], bool sigmoid) {
     float top = l[0];  // of those that are numbers; a NaN reaches the sum
 #pragma unroll
-    for (int v = 1; v < NV; ++v) top = fmaxf(top, l[v]);
+    for (int v = 1; v < NV; ++v) top = max_of(top, l[v]);
     top = lanes_max(top);
     float sum = 0.f;
 #pragma unroll
@@ -120,9 +121,9 @@ template <int NV> struct Token {
       float all = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const float t = __expf(-fabsf(l[v])), r = __builtin_amdgcn_rcpf(1.f + t);
-        rest[v] = l[v] >= 0.f ? t * r : r;
-        p[v] = l[v] >= 0.f ? r : t * r;
+        const float t = __expf(-l[v]);  // infinite below -88: a sigmoid of 0
+        p[v] = __builtin_amdgcn_rcpf(1.f + t);
+        rest[v] = l[v] >= 0.f ? t * p[v] : 1.f - p[v];
         all += p[v];
       }
       if (top <= 0.f) {
@@ -163,35 +164,60 @@ __device__ __forceinline__ uint32_t next_below(const uint32_t (&key)[NV], uint32
   return below - 1u - ~lanes_max(~d);
 }
 
-// The K experts of largest value, each counted by the lane that holds it.  Only the
-// set matters, so the K-th largest value is found by going down from one value to
-// the next; everything above it is chosen, and of its equals the first ones by their
-// expert.  RARE: equals are rare (float32 logits), so they are looked for at the end
-// only (131072 tokens of 256 experts: a third of the time of counting at each step).
-template <int NV, bool VEC, bool RARE>
-__device__ __forceinline__ void choose(const float (&l)[NV], const float* __restrict__ bias, int sub, int E, int K,
-                                       int (&count)[NV]) {
-  uint32_t key[NV];
+// The K-th largest value of a token where no lane has more than four of the largest K
+// and none of them equals another one; otherwise some value.
+template <int NV>
+__device__ __forceinline__ float kth_value(const float (&f)[NV], int K) {
+  constexpr int D = 4;
+  float m[D];  // the lane's largest ones, descending
+#pragma unroll
+  for (int i = 0; i < D; ++i) m[i] = -INFINITY;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int e = Place<NV, VEC>::expert(sub, v);
-    key[v] = e < E ? choice_key(bias != nullptr ? l[v] + bias[e] : l[v]) : 0u;
+#pragma unroll
+    for (int i = D - 1; i > 0; --i) m[i] = __builtin_amdgcn_fmed3f(m[i - 1], m[i], f[v]);
+    m[0] = max_of(m[0], f[v]);
   }
-  uint32_t last = ~0u;
-  int left = K, equal = 0;  // still to choose; how many equals the last value has
+  float best = INFINITY;
+  for (int k = 0; k < K; ++k) {
+    best = lanes_max(m[0]);
+    const bool took = m[0] == best;
+#pragma unroll
+    for (int i = 0; i + 1 < D; ++i) m[i] = took ? m[i + 1] : m[i];
+    m[D - 1] = took ? -INFINITY : m[D - 1];
+  }
+  return best;
+}
+
+// The K experts of largest value l + b, each counted by the lane that holds it.  Only
+// the set matters: a value that exactly K reach tells it.  RARE: equals are rare
+// (float32 logits), so such a value is first looked for among the largest few of each
+// lane: the loss of 131072 tokens, 8 of 256 sigmoid experts, takes 62 us so and 83
+// without; bfloat16 logits, whose equals spoil it for most waves, 107 and 91.
+// Otherwise the K-th largest is found by going down from one value to the next;
+// everything above it is chosen, and of its equals the first ones by their expert.
+template <int NV, bool VEC, bool RARE>
+__device__ __forceinline__ void choose(const float (&l)[NV], const float (&b)[NV], int sub, int E, int K,
+                                       int (&count)[NV]) {
+  float f[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) f[v] = l[v] + b[v];
   if constexpr (RARE) {
-    for (int k = 0; k < K; ++k) last = next_below(key, last);
+    const float last = kth_value(f, K);
     int got = 0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) got += key[v] >= last;
-    // no equals among the first K (fewer distinct values than K end at 0, which all keys reach)
+    for (int v = 0; v < NV; ++v) got += f[v] >= last;  // places past E too where it is -inf: more than K
     if (lanes_sum(got) == K) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) count[v] += key[v] >= last;
+      for (int v = 0; v < NV; ++v) count[v] += f[v] >= last;
       return;
     }
-    last = ~0u;
   }
+  uint32_t key[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) key[v] = Place<NV, VEC>::expert(sub, v) < E ? choice_key(f[v]) : 0u;
+  uint32_t last = ~0u;
+  int left = K, equal = 0;  // still to choose; how many equals the last value has
   while (left > 0) {
     last = next_below(key, last);
     equal = 0;
@@ -227,7 +253,9 @@ __device__ __forceinline__ void choose(const float (&l)[NV], const float* __rest
 // One chunk's sums: P [E], counts [E], the sum of lse^2, the number of tokens.
 __host__ __device__ constexpr int64_t part_words(int64_t E) { return 2 * E + 2; }
 
-template <typename T, int NV, bool VEC>
+// CHOOSE: counts are of the largest K values, otherwise of topk.  (Kernels of their own: the choice
+// takes the registers of half of the waves.)
+template <typename T, int NV, bool VEC, bool CHOOSE>
 __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ logits, const int32_t* __restrict__ topk,
                                                        const float* __restrict__ bias,
                                                        const uint8_t* __restrict__ mask, float* __restrict__ parts,
@@ -243,8 +271,11 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
   const int64_t row0 = int64_t(blockIdx.x / chunks) * seq_len;
   float p[NV], z = 0.f, l[NV], next[NV];
   int chosen[NV];
+  float b[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
+    const int e = Place<NV, VEC>::expert(sub, v);
+    b[v] = CHOOSE && bias != nullptr && e < E ? bias[e] : 0.f;
     p[v] = 0.f;
     chosen[v] = 0;
   }
@@ -266,8 +297,8 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
       for (int v = 0; v < NV; ++v) p[v] += a.p[v];
       z += a.lse * a.lse;
       ++mine;
-      if (topk == nullptr) {
-        choose<NV, VEC, sizeof(T) == 4>(l, bias, sub, E, K, chosen);
+      if constexpr (CHOOSE) {
+        choose<NV, VEC, sizeof(T) == 4>(l, b, sub, E, K, chosen);
       } else if (sub < K) {
         const int e = topk[(row0 + r) * K + sub];
         if (e >= 0 && e < E) atomicAdd(count + e, 1);
@@ -280,7 +311,7 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     sp[q][Place<NV, VEC>::expert(sub, v)] = p[v];
-    if (chosen[v] > 0) atomicAdd(count + Place<NV, VEC>::expert(sub, v), chosen[v]);
+    if (CHOOSE && chosen[v] > 0) atomicAdd(count + Place<NV, VEC>::expert(sub, v), chosen[v]);
   }
   if (sub == 0) {
     sz[q] = z;
@@ -555,9 +586,11 @@ hipError_t loss_t(const moe_balance& b, const T* logits, const int32_t* topk, co
   SeqSum* sums = reinterpret_cast<SeqSum*>(ws + parts_bytes(b));
   int32_t* seq_counts = B == 1 ? counts : reinterpret_cast<int32_t*>(ws + parts_bytes(b) + pad(size_t(B) * sizeof(SeqSum)));
   const hipError_t st = by_experts<T>(b.E, [&](auto nv, auto vec) {
-    k_balance_parts<T, nv.value, vec.value><<<dim3(unsigned(B * chunks)), dim3(256), 0, s>>>(
-        logits, topk, bias, mask, parts, int(b.E), int(b.K), int(b.seq_len), int(chunk), int(chunks),
-        b.score == MOE_SCORE_SIGMOID);
+    const auto kernel =
+        topk == nullptr ? k_balance_parts<T, nv.value, vec.value, true> : k_balance_parts<T, nv.value, vec.value, false>;
+    kernel<<<dim3(unsigned(B * chunks)), dim3(256), 0, s>>>(logits, topk, bias, mask, parts, int(b.E), int(b.K),
+                                                            int(b.seq_len), int(chunk), int(chunks),
+                                                            b.score == MOE_SCORE_SIGMOID);
     return hipGetLastError();
   });
   if (st != hipSuccess) return st;
