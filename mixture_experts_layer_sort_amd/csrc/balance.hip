@@ -206,8 +206,8 @@ __device__ __forceinline__ void choose(const float (&l)[NV], const float (&b)[NV
     const float last = kth_value(f, K);
     int got = 0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) got += f[v] >= last;  // places past E too where it is -inf: more than K
-    if (lanes_sum(got) == K) {
+    for (int v = 0; v < NV; ++v) got += f[v] >= last;
+    if (last > -INFINITY && lanes_sum(got) == K) {  // places past E reach -inf
 #pragma unroll
       for (int v = 0; v < NV; ++v) count[v] += f[v] >= last;
       return;

@@ -4,7 +4,8 @@ Tolerances.  u = 2^-24.  expf, logf and the quotients are good to a few u; a flo
 positive terms is off by at most m u of it.  With R = max|l| + 10 over finite l:
   a softmax probability is exp(l - max) / sum: the difference rounded once (R u), so (R + E + 16) u
   of it; a normalised sigmoid alike;
-  P_s,e adds up a chunk's tokens in float32: (chunk + 16) u more, chunk <= N / 512 + 16;
+  P_s,e adds up a chunk's tokens in float32, sixteen sums of chunk / 16 of them, then these: with
+  chunk <= max(64, N / 768 + 16) at most (N / 512 + 64) u more;
   lse: R u + (E + 8) u absolutely, at most (R + E + 8) u, and its square 2 |lse| times that.
 The loss adds alpha times the first and z times the second, and is rounded once.  A gradient
     c p_e (f_e - f.p) [1 - sigmoid] + zc lse softmax_e
@@ -148,6 +149,26 @@ def test_ties_infinities_and_nan():
     l[:] = float("nan")
     r.forward(l)
     assert r.counts.tolist() == [N] * K + [0] * (E - K)
+
+
+@pytest.mark.parametrize("E", [12, 20, 60, 100])
+def test_choice_among_few_numbers(E):
+    """Tokens of 0 to 12 logits that are numbers, 0 to 10 of these -inf, the others NaN: -inf in front of
+    NaN, NaN by its expert, and K chosen experts for every token, also where the numbers and the places
+    behind the last expert are K together."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    N, K = 13 * 11, 8
+    l = logits_of(N, E, torch.float32, seed=E)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    place = torch.argsort(torch.rand((N, E), generator=g, device="cuda"), dim=1)
+    i = torch.arange(N, device="cuda")[:, None]
+    l = torch.where(place < i % 13, l, torch.full_like(l, float("nan")))
+    l = torch.where(place < torch.minimum(i % 13, i // 13), torch.full_like(l, -float("inf")), l)
+    r = MoEBalanceRunner(N, E, K, torch.float32)
+    r.forward(l)
+    want = torch.bincount(order(l, None, K).reshape(-1), minlength=E)
+    assert int(want.sum()) == N * K and torch.equal(r.counts.long(), want)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
