@@ -638,7 +638,8 @@ int moe_mx4_dequantize(int32_t order, int64_t count, int64_t k, int64_t cols, in
  *   (dropped ones) are left as they were.  gemm_tiles is ignored.  The output
  *   overlaps no other argument.
  * Errors: MOE_EINVAL for a null, misaligned or overlapping pointer;
- * MOE_EUNSUPPORTED for N*H >= 2^33 (moe_mx4_gate_up). */
+ * MOE_EUNSUPPORTED for H or F > 2^20 or N*H >= 2^33 (the latter
+ * moe_mx4_gate_up). */
 int moe_mx4_gate_up(const moe_dims* d, const moe_mx4* x, const int32_t* sorted_flat, const moe_mx4* w_gate,
                     const moe_mx4* w_up, const int32_t* tiles, const int32_t* num_tiles, void* act,
                     hipStream_t stream);
@@ -650,8 +651,9 @@ int moe_mx4_down(const moe_dims* d, const moe_mx4* act, const moe_mx4* w_down, c
  * y have the type dims->dtype; x enters the products with all its bits, the
  * activations with 16 bits or more (bfloat16 layers) or 24 (float32), every sum is
  * float32, router logits float64, y is rounded once.  Weights below 2^-126
- * may count as 0.  Everything else, the shared expert (ds and its weights
- * [1, H, Fs] and [1, Fs, H]) included, as moe_decode. */
+ * may count as 0.  H, F or Fs > 2^20: MOE_EUNSUPPORTED.  Everything else, the
+ * shared expert (ds and its weights [1, H, Fs] and [1, Fs, H]) included, as
+ * moe_decode. */
 size_t moe_mx4_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds);
 int moe_mx4_decode(const moe_dims* d, const void* x, const void* w_r, const float* logit_bias, const moe_mx4* w_gate,
                    const moe_mx4* w_up, const moe_mx4* w_down, const moe_dims* ds, const moe_mx4* ws_gate,

@@ -80,6 +80,7 @@ int check_decode(const moe_dims* d, const moe_dims* ds, Dims* D, int64_t* Fs) {
 }
 
 // Sizes of a 4-bit tensor; its bytes.
+constexpr int64_t kMx4Side = int64_t(1) << 20;
 struct Mx4Sizes {
   size_t codes, scales, values;  // values: how many
 };
@@ -87,12 +88,18 @@ int check_mx4_sizes(int32_t order, int64_t count, int64_t k, int64_t cols, Mx4Si
   if (order != MOE_MX4_WEIGHTS && order != MOE_MX4_ROWS) return MOE_EINVAL;
   if (count < 0 || k <= 0 || cols <= 0 || k % 128 != 0) return MOE_EINVAL;
   if (order == MOE_MX4_ROWS ? cols != 1 : cols % 128 != 0) return MOE_EINVAL;
-  const int64_t side = int64_t(1) << 20;
-  if (k > side || cols > side || count >= int64_t(1) << 31) return MOE_EUNSUPPORTED;
+  if (k > kMx4Side || cols > kMx4Side || count >= int64_t(1) << 31) return MOE_EUNSUPPORTED;
   if (count > (int64_t(1) << 40) / k / cols) return MOE_EUNSUPPORTED;
   const size_t n = size_t(count) * size_t(k) * size_t(cols);
   *out = Mx4Sizes{n / 2, size_t(count) * size_t(cols) * size_t((k + 511) / 512) * 16, n};
   return MOE_OK;
+}
+
+// moe_mx4_decode's dims: those of moe_decode, sides that a 4-bit tensor can have.
+int check_mx4_decode(const moe_dims* d, const moe_dims* ds, Dims* D, int64_t* Fs) {
+  const int st = check_decode(d, ds, D, Fs);
+  if (st != MOE_OK) return st;
+  return D->H > kMx4Side || D->F > kMx4Side || *Fs > kMx4Side ? MOE_EUNSUPPORTED : MOE_OK;
 }
 
 bool mx4_ok(const moe_mx4* q) { return q != nullptr && ptrs_ok(q->codes, q->scales); }
@@ -663,6 +670,7 @@ int moe_mx4_gate_up(const moe_dims* d, const moe_mx4* x, const int32_t* sorted_f
                     hipStream_t stream) {
   MOE_CHECK_DIMS(d, D);
   if (!mx4_ok(x) || !mx4_ok(w_gate) || !mx4_ok(w_up) || !ptrs_ok(sorted_flat, tiles, num_tiles, act)) return MOE_EINVAL;
+  if (D.H > kMx4Side || D.F > kMx4Side) return MOE_EUNSUPPORTED;
   // the rows' codes are addressed by 32 bits from the first token's on
   if (D.N * D.H >= int64_t(1) << 33) return MOE_EUNSUPPORTED;
   Span s[10] = {{act, size_t(D.NK()) * size_t(D.F) * (D.dtype == MOE_BF16 ? 2 : 4)},
@@ -683,6 +691,7 @@ int moe_mx4_down(const moe_dims* d, const moe_mx4* act, const moe_mx4* w_down, c
                  const int32_t* num_tiles, void* ys, hipStream_t stream) {
   MOE_CHECK_DIMS(d, D);
   if (!mx4_ok(act) || !mx4_ok(w_down) || !ptrs_ok(tiles, num_tiles, ys)) return MOE_EINVAL;
+  if (D.H > kMx4Side || D.F > kMx4Side) return MOE_EUNSUPPORTED;
   Span s[7] = {{ys, size_t(D.NK()) * size_t(D.H) * (D.dtype == MOE_BF16 ? 2 : 4)},
                {tiles, size_t(moe_launch::max_tiles(D)) * 12},
                {num_tiles, 4}};
@@ -697,7 +706,7 @@ int moe_mx4_down(const moe_dims* d, const moe_mx4* act, const moe_mx4* w_down, c
 size_t moe_mx4_decode_workspace_bytes(const moe_dims* d, const moe_dims* ds) {
   Dims D;
   int64_t Fs;
-  if (check_decode(d, ds, &D, &Fs) != MOE_OK) return size_t(-1);
+  if (check_mx4_decode(d, ds, &D, &Fs) != MOE_OK) return size_t(-1);
   return D.N == 0 ? 0 : moe_launch::mx4_decode_ws(D, Fs);
 }
 
@@ -707,7 +716,7 @@ int moe_mx4_decode(const moe_dims* d, const void* x, const void* w_r, const floa
                    size_t ws_bytes, hipStream_t stream) {
   Dims D;
   int64_t Fs;
-  const int st = check_decode(d, ds, &D, &Fs);
+  const int st = check_mx4_decode(d, ds, &D, &Fs);
   if (st != MOE_OK) return st;
   if (!ptrs_ok(x, w_r, topk_idx, gates, y) || !mx4_ok(w_gate) || !mx4_ok(w_up) || !mx4_ok(w_down)) return MOE_EINVAL;
   if (logit_bias != nullptr && !aligned16(logit_bias)) return MOE_EINVAL;

@@ -99,6 +99,9 @@ def test_mx4_products_refuse(lib):
     for d, st in ((D(H=100), L.MOE_EINVAL), (D(E=300), L.MOE_EUNSUPPORTED), (D(dtype=5), L.MOE_EUNSUPPORTED)):
         assert gate_up(d) == st and down(d) == st
     assert gate_up(D(N=0)) == L.MOE_OK and down(D(N=0)) == L.MOE_OK
+    for d in (D(H=(1 << 20) + 128), D(F=(1 << 20) + 128)):  # no 4-bit tensor has such a side
+        assert gate_up(d) == down(d) == L.MOE_EUNSUPPORTED
+        assert L.moe_mx4_decode_workspace_bytes(d) == 2 ** 64 - 1 and decode(d, nb=1 << 40) == L.MOE_EUNSUPPORTED
     # the rows' codes have 32-bit offsets
     assert gate_up(D(N=1 << 20, H=1 << 13), act=at(1)) == L.MOE_EUNSUPPORTED
     assert gate_up(D(N=(1 << 20) - 1, H=1 << 13), act=at(1)) == L.MOE_EINVAL  # the next check's
