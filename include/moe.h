@@ -614,7 +614,7 @@ size_t moe_mx4_scale_bytes(int32_t order, int64_t count, int64_t k, int64_t cols
  * Errors: MOE_EINVAL for an unknown order, count < 0, k or cols <= 0 or not a
  * multiple of 128 (rows: cols != 1), a null, misaligned or overlapping
  * pointer; MOE_EUNSUPPORTED for an unknown dtype, k or cols > 2^20, count >=
- * 2^31 or more than 2^40 values. */
+ * 2^27 or more than 2^36 values. */
 int moe_mx4_quantize(int32_t order, int64_t count, int64_t k, int64_t cols, int32_t dtype, const void* v,
                      const moe_mx4* q, hipStream_t stream);
 
@@ -679,7 +679,7 @@ int moe_mx4_decode(const moe_dims* d, const void* x, const void* w_r, const floa
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
 typedef struct moe_balance {
-  int64_t N, E, K, seq_len; /* N a multiple of seq_len; limits of moe_dims */
+  int64_t N, E, K, seq_len; /* N a multiple of seq_len; limits of moe_dims, N < 2^28, at most 2^23 sequences */
   int32_t dtype;            /* of logits and dlogits */
   int32_t score;            /* moe_score */
   float alpha, z_coef;      /* finite */
@@ -697,8 +697,8 @@ size_t moe_balance_workspace_bytes(const moe_balance* b);
  * alone.  mask [N] bytes or NULL (every token counts).
  *   loss [1] f32 out; counts [E] int32 out; state: moe_balance_state_bytes.
  * Outputs, state and ws overlap neither each other nor an input.  N == 0
- * enqueues nothing and leaves the outputs untouched.  Errors: MOE_EINVAL, MOE_EUNSUPPORTED (limits, dtype),
- * MOE_EWORKSPACE (state or ws). */
+ * enqueues nothing and leaves the outputs untouched.  Errors: MOE_EINVAL,
+ * MOE_EUNSUPPORTED (limits, dtype), MOE_EWORKSPACE (state or ws). */
 int moe_balance_loss(const moe_balance* b, const void* logits, const int32_t* topk_idx, const float* logit_bias,
                      const uint8_t* mask, float* loss, int32_t* counts, void* state, size_t state_bytes, void* ws,
                      size_t ws_bytes, hipStream_t stream);

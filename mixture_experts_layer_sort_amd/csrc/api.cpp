@@ -88,8 +88,9 @@ int check_mx4_sizes(int32_t order, int64_t count, int64_t k, int64_t cols, Mx4Si
   if (order != MOE_MX4_WEIGHTS && order != MOE_MX4_ROWS) return MOE_EINVAL;
   if (count < 0 || k <= 0 || cols <= 0 || k % 128 != 0) return MOE_EINVAL;
   if (order == MOE_MX4_ROWS ? cols != 1 : cols % 128 != 0) return MOE_EINVAL;
-  if (k > kMx4Side || cols > kMx4Side || count >= int64_t(1) << 31) return MOE_EUNSUPPORTED;
-  if (count > (int64_t(1) << 40) / k / cols) return MOE_EUNSUPPORTED;
+  if (k > kMx4Side || cols > kMx4Side || count >= int64_t(1) << 27) return MOE_EUNSUPPORTED;
+  // a launch has less than 2^32 threads: 2^28 groups of 512 values of a row, and fewer workgroups of weights
+  if (count > (int64_t(1) << 36) / k / cols) return MOE_EUNSUPPORTED;
   const size_t n = size_t(count) * size_t(k) * size_t(cols);
   *out = Mx4Sizes{n / 2, size_t(count) * size_t(cols) * size_t((k + 511) / 512) * 16, n};
   return MOE_OK;
@@ -133,7 +134,9 @@ int check_balance(const moe_balance* b) {
   if (!std::isfinite(b->alpha) || !std::isfinite(b->z_coef)) return MOE_EINVAL;
   if (b->E > MOE_MAX_EXPERTS || b->K > MOE_MAX_TOPK || b->K > b->E) return MOE_EUNSUPPORTED;
   const int64_t lim = int64_t(1) << 31;
-  if (b->N >= lim || b->seq_len >= lim - 4096 || b->N * b->K >= lim || b->N * b->E >= lim) return MOE_EUNSUPPORTED;
+  if (b->N >= lim || b->N * b->K >= lim || b->N * b->E >= lim) return MOE_EUNSUPPORTED;
+  // launches of less than 2^32 threads: sixteen for a token, 256 for a sequence
+  if (b->N >= int64_t(1) << 28 || b->N / b->seq_len > int64_t(1) << 23) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 

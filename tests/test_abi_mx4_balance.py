@@ -46,7 +46,8 @@ SIZES = [((2, 1, 128, 128), L.MOE_EINVAL), ((W, -1, 128, 128), L.MOE_EINVAL), ((
          ((W, 1, 128, 0), L.MOE_EINVAL), ((W, 1, 96, 128), L.MOE_EINVAL), ((W, 1, 128, 64), L.MOE_EINVAL),
          ((R, 1, 128, 128), L.MOE_EINVAL), ((R, 1, 64, 1), L.MOE_EINVAL),
          ((W, 1, (1 << 20) + 128, 128), L.MOE_EUNSUPPORTED), ((W, 1, 128, (1 << 20) + 128), L.MOE_EUNSUPPORTED),
-         ((R, 1 << 31, 128, 1), L.MOE_EUNSUPPORTED), ((W, 2, 1 << 20, 1 << 20), L.MOE_EUNSUPPORTED)]
+         ((R, 1 << 31, 128, 1), L.MOE_EUNSUPPORTED), ((R, 1 << 27, 128, 1), L.MOE_EUNSUPPORTED),
+         ((R, (1 << 16) + 1, 1 << 20, 1), L.MOE_EUNSUPPORTED), ((W, 2, 1 << 20, 1 << 20), L.MOE_EUNSUPPORTED)]
 
 
 @pytest.mark.parametrize("sizes,status", SIZES)
@@ -184,7 +185,8 @@ def bwd(b, **kw):
     (B(K=0), L.MOE_EINVAL), (B(K=9, E=16), L.MOE_EUNSUPPORTED), (B(K=5, E=4), L.MOE_EUNSUPPORTED),
     (B(E=257), L.MOE_EUNSUPPORTED), (B(dtype=3), L.MOE_EUNSUPPORTED), (B(score=2), L.MOE_EINVAL),
     (B(alpha=float("nan")), L.MOE_EINVAL), (B(z_coef=float("inf")), L.MOE_EINVAL),
-    (B(N=1 << 30, seq_len=1, E=8), L.MOE_EUNSUPPORTED)])
+    (B(N=1 << 30, seq_len=1, E=8), L.MOE_EUNSUPPORTED), (B(N=1 << 28, seq_len=1 << 20, E=2, K=1), L.MOE_EUNSUPPORTED),
+    (B(N=(1 << 23) + 1, seq_len=1, E=2, K=1), L.MOE_EUNSUPPORTED)])
 def test_balance_options_refused(lib, b, status):
     assert L.moe_balance_state_bytes(b) == BAD and L.moe_balance_workspace_bytes(b) == BAD
     assert loss(b, 1 << 40, 1 << 40) == status
