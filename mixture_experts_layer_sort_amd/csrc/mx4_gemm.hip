@@ -58,18 +58,19 @@ __device__ __forceinline__ i32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off
 // 32 values from 32 (2 * half + h) on of each tile, of column c of the pair.
 struct Weights {
   i32x4_t b[kStep][2][kPairs];
-  int s[2][kPairs];
 };
+// Their scales, a word for the four tiles of two steps.
+typedef int Scales[2][kPairs];
 
-// acc[row group][pair] += weights . rows over one step, the scales of its first tile
-// `shift` bits up in their words; tiles past the last one have zero weights.  Two row
+// acc[row group][pair] += weights . rows over one step, the first (ODD = 0) or second of
+// two that share their scales' words; tiles past the last one have zero weights.  Two row
 // groups at a time; the next two are read while the products of these run (left to
 // itself the compiler reads them right before their use).  behind(n) after batch n of
 // products: memory requests that go out there one or two at a time, as a row of them
 // holds up the wave, and its products.
 constexpr int kBatch = 2, kBatches = 2 * kGroups / kBatch;  // of a tile
-template <typename Behind>
-__device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, int shift,
+template <int ODD, typename Behind>
+__device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, const Scales& ws,
                                      f32x16_t (&acc)[kGroups][kPairs], Behind behind) {
   const int lane = lane_id(), h = lane / 32;
   const char* mine = rows + lane % 32 * 128;
@@ -80,13 +81,6 @@ __device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, 
 #pragma unroll
     for (int r = 0; r < kGroups; ++r)
       s[f][r] = *reinterpret_cast<const int*>(rows + kRowBytes + (r * 32 + lane % 32) * 16 + (2 * f + h) * 4);
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-#pragma unroll
-    for (int r = 0; r < kGroups; ++r) s[f][r] >>= shift;
-#pragma unroll
-    for (int p = 0; p < kPairs; ++p) w.s[f][p] >>= shift;
-  }
   i32x4_t a[2][kBatch];
   auto read = [&](int n, i32x4_t (&to)[kBatch]) {  // of all tiles' halves' row groups
 #pragma unroll
@@ -112,7 +106,7 @@ __device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, 
         for (int p = 0; p < kPairs; ++p) {
           const i32x4_t q = w.b[KT][f][p];
           acc[r][p] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              i32x8_t{q[0], q[1], q[2], q[3], 0, 0, 0, 0}, x, acc[r][p], 4, 4, KT, w.s[f][p], KT, s[f][r]);
+              i32x8_t{q[0], q[1], q[2], q[3], 0, 0, 0, 0}, x, acc[r][p], 4, 4, KT + 2 * ODD, ws[f][p], KT + 2 * ODD, s[f][r]);
           // in this order: without a side effect products sink to the end of the step, and the
           // operands of all of them stay in registers until there
           asm volatile("" : "+v"(acc[r][p]));
@@ -127,12 +121,12 @@ __device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, 
   tile(std::integral_constant<int, 1>());
 }
 
-// One step from `from`, with the requests for the next one, whose rows go to `to`:
+// One step from `from`, with the requests for the one after the next, whose rows go to `to`:
 // distinct buffers, so that reads of one do not wait for the other.
-template <typename Request>
+template <int ODD, typename Request>
 __device__ __forceinline__ void step_and_next(char* __restrict__ to, const char* __restrict__ from, Request request,
-                                              Weights& w, int shift, f32x16_t (&acc)[kGroups][kPairs]) {
-  step(from, w, shift, acc, [&](int n) { request(n, to); });
+                                              Weights& w, const Scales& ws, f32x16_t (&acc)[kGroups][kPairs]) {
+  step<ODD>(from, w, ws, acc, [&](int n) { request(n, to); });
 }
 
 struct Rows {
@@ -194,7 +188,7 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
   // a lane's place behind the first strip of a pair
   const uint32_t lane_code = lane % 32 / 16 * uint32_t(kts * 1024) + lane / 32 * 256 + lane % 16 * 16;
   const uint32_t lane_scale = lane % 32 / 16 * uint32_t(groups * 256) + lane / 32 * 64 + lane % 16 * 4;
-  auto fetch_scales = [&](int q, int (&to)[2][kPairs]) {
+  auto fetch_scales = [&](int q, Scales& to) {  // of step q and the next one
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -236,13 +230,18 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
     }
   };
 
-  Weights w;
+  Weights w[2];
+  Scales ws, next;
 #pragma unroll
-  for (int k = 0; k < MOVED; ++k) fetch_rows(0, k, lds);
-  fetch_scales(0, w.s);
-  __builtin_amdgcn_sched_barrier(0);
+  for (int q = 0; q < 2; ++q) {
 #pragma unroll
-  for (int k = 0; k < LOADS; ++k) fetch_tile(0, k / PARTS, k % PARTS, w);
+    for (int k = 0; k < MOVED; ++k) fetch_rows(q, k, lds + q * kStageBytes);
+    if (q == 0) fetch_scales(0, ws);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k) fetch_tile(q, k / PARTS, k % PARTS, w[q]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   f32x16_t acc[kGroups][kPairs];
 #pragma unroll
   for (int r = 0; r < kGroups; ++r)
@@ -250,38 +249,47 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
     for (int p = 0; p < kPairs; ++p)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[r][p][k] = 0.f;
-#pragma clang loop unroll(disable)
-  for (int i = 0; i < steps; ++i) {
-    wait_vm<LOADS>();  // the rows are here; the weights behind them may still be on their way
+  // Step i from its buffer, while what step i + 2 needs is asked for: behind the batches of the first tile
+  // its rows, behind those of the second the weights of the first.  Past the last step too, where they
+  // bring nothing: with as many requests on every path, the compiler's waits need not take the fewest.
+  int from = 0;  // buffer of step i
+  auto turn = [&](int i, auto odd) {
+    constexpr int ODD = decltype(odd)::value;
+    // the rows are here; the weights, and what the step before asked for, may still be on their way
+    wait_vm<MOVED - 1 + LOADS + (ODD ? 2 * kPairs : 0)>();
     lds_barrier();
-    int s[2][kPairs];
-    // Behind the batches of the first tile the next step's rows are asked for, behind those of the second
-    // the weights of the first.  Past the last step too, where they bring nothing: with as many requests on
-    // every path, the compiler's waits need not take the fewest.
     constexpr int EACH = (PARTS + kBatches - 1) / kBatches, TWO = (MOVED + kBatches - 1) / kBatches;
     auto request = [&](int n, char* to) {
       const int b = n % kBatches;
-      if (n == 0) fetch_scales(i + 1, s);
+      if (!ODD && n == 0) fetch_scales(i + 2, next);
       if (n < kBatches) {
 #pragma unroll
         for (int k = TWO * b; k < TWO * b + TWO; ++k)
-          if (k < MOVED) fetch_rows(i + 1, k, to);
+          if (k < MOVED) fetch_rows(i + 2, k, to);
       } else {
 #pragma unroll
         for (int k = EACH * b; k < EACH * b + EACH; ++k)
-          if (k < PARTS) fetch_tile(i + 1, 0, k, w);
+          if (k < PARTS) fetch_tile(i + 2, 0, k, w[ODD]);
       }
       if (n + 1 == 2 * kBatches) {
 #pragma unroll
-        for (int k = 0; k < PARTS; ++k) fetch_tile(i + 1, 1, k, w);
+        for (int k = 0; k < PARTS; ++k) fetch_tile(i + 2, 1, k, w[ODD]);
       }
     };
-    step_and_next(lds + (i + 1) % 2 * kStageBytes, lds + i % 2 * kStageBytes, request, w, i % 2 * 16, acc);
+    const int to = from == 0 ? 2 : from - 1;
+    step_and_next<ODD>(lds + to * kStageBytes, lds + from * kStageBytes, request, w[ODD], ws, acc);
+    from = from == 2 ? 0 : from + 1;
+  };
+#pragma clang loop unroll(disable)
+  for (int i = 0; i + 1 < steps; i += 2) {
+    turn(i, std::integral_constant<int, 0>());
+    turn(i + 1, std::integral_constant<int, 1>());
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int p = 0; p < kPairs; ++p) w.s[f][p] = s[f][p];
+      for (int p = 0; p < kPairs; ++p) ws[f][p] = next[f][p];
   }
+  if (steps % 2 != 0) turn(steps - 1, std::integral_constant<int, 0>());
 
   // 32-bit offsets from the piece's first row
   const uint32_t mine = (lane % 32 * uint32_t(C) + lane / 32 * 16) * uint32_t(sizeof(T));
@@ -312,7 +320,7 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
 template <typename T, bool GATE_UP>
 hipError_t product(const moe_launch::Dims& d, const Rows& x, const moe_launch::Mx4& w0, const moe_launch::Mx4& w1,
                    const int32_t* tiles, const int32_t* num_tiles, T* out, int L, int C, hipStream_t s) {
-  constexpr int bytes = 2 * kStageBytes, BN = (GATE_UP ? 1 : 2) * 32 * kGWaves;
+  constexpr int bytes = 3 * kStageBytes, BN = (GATE_UP ? 1 : 2) * 32 * kGWaves;
   const hipError_t e = allow_lds<k_mx4_product<T, GATE_UP>>(bytes);
   if (e != hipSuccess) return e;
   const int64_t pieces = moe_launch::max_tiles(d) * (MOE_TILE_M / kRows) * ((C + BN - 1) / BN);
