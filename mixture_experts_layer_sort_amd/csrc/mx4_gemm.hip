@@ -9,17 +9,21 @@
 // that the activation is formed in registers); two workgroups share a CU, so that one
 // of them multiplies while the other waits for its first loads or stores its results.
 // Per step, 256 values of the contraction:
-//  - rows: moved by the LDS DMA one step ahead, two buffers; a wave's request takes
+//  - rows: moved by the LDS DMA two steps ahead, three buffers; a wave's request takes
 //    8 rows of 128 bytes, whole cache lines (the gather costs nothing).  Requests of 64
 //    bytes of 16 rows, half a line each, and rows through registers took 2220 us where
 //    this takes 1910 to 1980: gate/up of 16384 tokens, H 4096, F 14336, E 8, K 2;
 //  - weights: each strip is read by one wave only, so they go straight to
-//    registers: behind its last product a tile's registers take the same tile of the
-//    next step;
+//    registers, of two steps: behind its last product a tile's registers take the same
+//    tile of the step after the next (one step ahead and two buffers: 2 to 6 % slower
+//    where few rows an expert leave the time to memory);
 //  - scales: a word for four tiles of the contraction; the instruction picks the
 //    byte.
 // Weights are the row operand: a lane ends with groups of four neighbouring columns
 // of a row.
+// What bounds it there: the instruction runs 56 % of the cycles, at the 1.7 GHz that its
+// power leaves on such data; a third of a workgroup's time is first loads, activation and
+// stores.
 #include <algorithm>
 
 #include "mma_lds.h"
@@ -39,8 +43,8 @@ constexpr int kPairs = 2;  // pairs of strips of a wave
 constexpr int kStep = 2;  // tiles of a step
 
 constexpr int kRows = 128, kGroups = kRows / 32;
-// Of a step, in LDS: the rows, [row][(k/32)%8 ^ row%8][16 bytes] so that 8 rows' blocks lie in all banks, and
-// their scales, [row][16 bytes].
+// Of a step, in LDS: the rows, [row][(k/32)%8 ^ (row/2)%8][16 bytes], so that a block of 16 rows lies in all
+// banks (with row%8 in half of them: 2.3 times the conflicts, 0.5 % more time), and their scales, [row][16 bytes].
 constexpr int kRowBytes = kRows * 128, kStageBytes = kRowBytes + kRows * 16;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* base, int bytes) {
@@ -74,7 +78,7 @@ __device__ __forceinline__ void step(const char* __restrict__ rows, Weights& w, 
                                      f32x16_t (&acc)[kGroups][kPairs], Behind behind) {
   const int lane = lane_id(), h = lane / 32;
   const char* mine = rows + lane % 32 * 128;
-  const int first = (h ^ lane % 8) * 16;
+  const int first = (h ^ lane / 2 % 8) * 16;
   int s[2][kGroups];
 #pragma unroll
   for (int f = 0; f < 2; ++f)
@@ -215,16 +219,16 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
   // a request takes 8 rows, lane (r, b) the block of row r whose place in LDS is b; the last one scales of 64
   // rows (of waves 0 and 1)
   constexpr int REQUESTS = kRows / 8 / kGWaves, MOVED = REQUESTS + 1;
-  const uint32_t block = (lane % 8 ^ lane / 8) * 16;
+  auto block = [&](int j) -> uint32_t { return (lane % 8 ^ (lane / 16 + j % 2 * 4)) * 16; };
   uint32_t px[MOVED];
 #pragma unroll
-  for (int j = 0; j < REQUESTS; ++j) px[j] = source((wave * REQUESTS + j) * 8 + lane / 8) * uint32_t(L / 2) + block;
+  for (int j = 0; j < REQUESTS; ++j) px[j] = source((wave * REQUESTS + j) * 8 + lane / 8) * uint32_t(L / 2) + block(j);
   px[REQUESTS] = source(wave * kWave + lane) * uint32_t(groups * 16);
   // Request n of step q's rows.  An odd last tile is brought twice; past the last step nothing is (zeros).
   auto fetch_rows = [&](int q, int n, char* to) {
     const int live = uniform(q < steps ? -1 : 0);
     if (n < REQUESTS) {
-      dma_bytes(resource(codes + q * 128, live), px[n] - (2 * q + 1 < kts ? 0 : block & 64), to + (wave * REQUESTS + n) * 1024);
+      dma_bytes(resource(codes + q * 128, live), px[n] - (2 * q + 1 < kts ? 0 : block(n) & 64), to + (wave * REQUESTS + n) * 1024);
     } else if (wave * kWave < kRows) {
       dma_bytes(resource(scales + q * kStep / 4 * 16, live), px[REQUESTS], to + kRowBytes + wave * 1024);
     }
