@@ -108,61 +108,57 @@ template <> struct Vec<float> {
   }
 };
 
-// Weights [count][K][C].  A workgroup has V strips of 16 columns and 512 rows, a
-// wave 128 of them; lane (g, o) the 32 rows from 32g on of V adjacent columns, one
-// 16-byte load a row (256 contiguous bytes for 16 lanes), so that each column's
-// block is in one lane's registers: its codes need no exchange, and leave in
-// V * 16 contiguous bytes.
+// Weights [count][K][C].  A wave has 128 rows of V strips of 16 columns; lane (g, o) the
+// 32 rows from 32g on of V adjacent columns, one 16-byte load a row (256 contiguous
+// bytes for 16 lanes), so that each column's block is in one lane's registers: its
+// codes need no exchange, and leave in V * 16 contiguous bytes.  A workgroup is one
+// wave, which fills the chip with small tensors too (8 x 512 x 1024 bf16: 5.2 us,
+// with four waves 6.7; a scale's bytes meet in the L2).
 template <typename T>
-__global__ __launch_bounds__(256) void k_mx4_weights(const T* __restrict__ v, words4_t* __restrict__ codes,
-                                                     uint32_t* __restrict__ scales, int K, int C, int chunks,
-                                                     int groups) {
+__global__ __launch_bounds__(kWave) void k_mx4_weights(const T* __restrict__ v, words4_t* __restrict__ codes,
+                                                       uint8_t* __restrict__ scales, int K, int C, int chunks,
+                                                       int groups) {
   typedef Vec<T> W;
   constexpr int V = W::V;
-  __shared__ uint8_t sc[V * kWave * 4];
-  const int wave = threadIdx.x / kWave, g = lane_id() / 16, o = lane_id() % 16;
-  const int chunk = blockIdx.x % chunks, b = blockIdx.x / chunks, q = b % groups;
-  const int64_t m = b / groups, strip0 = m * (C / 16) + int64_t(chunk) * V;
-  const int kt = 4 * q + wave, strip = o * V / 16, c = o * V % 16;
-  uint8_t* mine = sc + (strip * kWave + g * 16 + c) * 4 + wave;
-  if (kt < K / kMxTile) {
-    const T* p = v + (m * K + kt * kMxTile + 32 * g) * C + int64_t(chunk) * 16 * V + o * V;
-    words4_t w[32];
-#pragma unroll
-    for (int r = 0; r < 32; ++r)
-      w[r] = __builtin_nontemporal_load(reinterpret_cast<const words4_t*>(p + int64_t(r) * C));
-    uint32_t f[V];
-    W::fields(w, f);
-    words4_t* to = codes + ((strip0 + strip) * (K / kMxTile) + kt) * kWave + g * 16 + c;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const uint32_t s = scale_byte(f[j]);
-      words4_t out;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) out[d] = W::column(w + 8 * d, j, scale_of(s));
-      to[j] = out;
-      mine[4 * j] = uint8_t(s);
-    }
-  } else {
+  const int g = lane_id() / 16, o = lane_id() % 16;
+  const int b = blockIdx.x / (4 * groups), kt = blockIdx.x % (4 * groups), chunk = b % chunks;
+  const int64_t m = b / chunks, strip = m * (C / 16) + int64_t(chunk) * V + o * V / 16;
+  const int c = o * V % 16;
+  uint8_t* mine = scales + ((strip * groups + kt / 4) * kWave + g * 16 + c) * 4 + kt % 4;
+  if (kt >= K / kMxTile) {
 #pragma unroll
     for (int j = 0; j < V; ++j) mine[4 * j] = 0;
+    return;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < V * kWave; i += 256)
-    scales[((strip0 + i / kWave) * groups + q) * kWave + i % kWave] = reinterpret_cast<const uint32_t*>(sc)[i];
+  const T* p = v + (m * K + kt * kMxTile + 32 * g) * C + int64_t(chunk) * 16 * V + o * V;
+  words4_t w[32];
+#pragma unroll
+  for (int r = 0; r < 32; ++r) w[r] = __builtin_nontemporal_load(reinterpret_cast<const words4_t*>(p + int64_t(r) * C));
+  uint32_t f[V];
+  W::fields(w, f);
+  words4_t* to = codes + (strip * (K / kMxTile) + kt) * kWave + g * 16 + c;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t s = scale_byte(f[j]);
+    words4_t out;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) out[d] = W::column(w + 8 * d, j, scale_of(s));
+    to[j] = out;
+    mine[4 * j] = uint8_t(s);
+  }
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void k_mx4_weights_back(const words4_t* __restrict__ codes,
-                                                          const uint8_t* __restrict__ scales, T* __restrict__ v, int K,
-                                                          int C, int chunks) {
+__global__ __launch_bounds__(kWave) void k_mx4_weights_back(const words4_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, T* __restrict__ v,
+                                                            int K, int C, int chunks) {
   typedef Vec<T> W;
   constexpr int V = W::V;
-  const int wave = threadIdx.x / kWave, g = lane_id() / 16, o = lane_id() % 16;
+  const int g = lane_id() / 16, o = lane_id() % 16;
   const int tiles = K / kMxTile, groups = mx_groups(K);
-  const int chunk = blockIdx.x % chunks, b = blockIdx.x / chunks, kt = b % groups * 4 + wave;
+  const int b = blockIdx.x / (4 * groups), kt = blockIdx.x % (4 * groups), chunk = b % chunks;
   if (kt >= tiles) return;
-  const int64_t m = b / groups, strip = m * (C / 16) + int64_t(chunk) * V + o * V / 16;
+  const int64_t m = b / chunks, strip = m * (C / 16) + int64_t(chunk) * V + o * V / 16;
   const int c = o * V % 16;
   const words4_t* from = codes + (strip * tiles + kt) * kWave + g * 16 + c;
   const uint8_t* s = scales + ((strip * groups + kt / 4) * kWave + g * 16 + c) * 4 + kt % 4;
@@ -271,8 +267,8 @@ hipError_t quantize_t(bool rows, int64_t count, int64_t k, int64_t cols, const T
         v, static_cast<uint32_t*>(codes), static_cast<uint32_t*>(scales), items, int(k), groups);
   } else {
     const int64_t chunks = cols / (16 * Vec<T>::V);
-    k_mx4_weights<T><<<dim3(unsigned(count * groups * chunks)), dim3(256), 0, s>>>(
-        v, static_cast<words4_t*>(codes), static_cast<uint32_t*>(scales), int(k), int(cols), int(chunks), groups);
+    k_mx4_weights<T><<<dim3(unsigned(count * chunks * groups * 4)), dim3(kWave), 0, s>>>(
+        v, static_cast<words4_t*>(codes), static_cast<uint8_t*>(scales), int(k), int(cols), int(chunks), groups);
   }
   return hipGetLastError();
 }
@@ -287,7 +283,7 @@ hipError_t dequantize_t(bool rows, int64_t count, int64_t k, int64_t cols, const
         static_cast<const uint32_t*>(q.codes), static_cast<const uint8_t*>(q.scales), v, words, int(k), groups);
   } else {
     const int64_t chunks = cols / (16 * Vec<T>::V);
-    k_mx4_weights_back<T><<<dim3(unsigned(count * groups * chunks)), dim3(256), 0, s>>>(
+    k_mx4_weights_back<T><<<dim3(unsigned(count * chunks * groups * 4)), dim3(kWave), 0, s>>>(
         static_cast<const words4_t*>(q.codes), static_cast<const uint8_t*>(q.scales), v, int(k), int(cols),
         int(chunks));
   }
