@@ -23,6 +23,7 @@ using namespace moe;
 
 constexpr int kLanes = 16;       // of a token
 constexpr int kRows = 256 / kLanes;  // tokens a workgroup has under way
+constexpr int kOneRows = 1024 / kLanes;  // where one workgroup does all
 constexpr int64_t kMostChunks = 768;  // three workgroups a CU: what the registers allow
 
 // Over the sixteen lanes of a token, all of them getting the result: each step
@@ -253,18 +254,49 @@ __device__ __forceinline__ void choose(const float (&l)[NV], const float (&b)[NV
 // One chunk's sums: P [E], counts [E], the sum of lse^2, the number of tokens.
 __host__ __device__ constexpr int64_t part_words(int64_t E) { return 2 * E + 2; }
 
+// What the backward pass needs: words 0 and 1 the sequences and tokens that count,
+// then of every sequence f [E] and its tokens.
+constexpr int kStateHead = 4;
+__host__ __device__ constexpr int64_t state_words(int64_t B, int64_t E) { return kStateHead + B * (E + 1); }
+
+// Of every sequence, for the sums over them.
+struct SeqSum {
+  double loss, z;  // f.P, sum of lse^2
+  int64_t tokens;
+};
+
+// alpha / B' sum f.P + z / n sum lse^2, from the sums over the sequences.
+__device__ __forceinline__ float total_loss(double fp, double z, int64_t seqs, int64_t tokens, float alpha,
+                                            float z_coef) {
+  if (tokens == 0) return 0.f;
+  const double balance = double(alpha) * fp / double(seqs);
+  return float(z_coef == 0.f ? balance : balance + double(z_coef) * z / double(tokens));  // no 0 * infinity
+}
+// f_e of a sequence of n tokens.
+__device__ __forceinline__ double expert_share(int count, int E, int K, int64_t n) {
+  return n == 0 ? 0.0 : double(E) * double(count) / (double(K) * double(n));
+}
+
+// Where results go: a chunk's to parts; ONE, of one sequence in one workgroup, itself to
+// state, counts and loss.
+struct Results {
+  float *parts, *state, *loss;
+  int32_t* counts;
+  float alpha, z_coef;
+};
+
 // CHOOSE: counts are of the largest K values, otherwise of topk.  (Kernels of their own: the choice
-// takes the registers of half of the waves.)
-template <typename T, int NV, bool VEC, bool CHOOSE>
-__global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ logits, const int32_t* __restrict__ topk,
-                                                       const float* __restrict__ bias,
-                                                       const uint8_t* __restrict__ mask, float* __restrict__ parts,
-                                                       int E, int K, int seq_len, int chunk, int chunks, bool sigmoid) {
-  __shared__ float sp[kRows][NV * kLanes];
-  __shared__ float sz[kRows];
+// takes the registers of half of the waves.)  ROWS tokens at a time.
+template <typename T, int NV, bool VEC, bool CHOOSE, bool ONE>
+__global__ __launch_bounds__(ONE ? 1024 : 256) void k_balance_parts(
+    const T* __restrict__ logits, const int32_t* __restrict__ topk, const float* __restrict__ bias,
+    const uint8_t* __restrict__ mask, Results to, int E, int K, int seq_len, int chunk, int chunks, bool sigmoid) {
+  constexpr int ROWS = ONE ? kOneRows : kRows, NT = ROWS * kLanes;
+  __shared__ float sp[ROWS][NV * kLanes];
+  __shared__ float sz[ROWS];
   __shared__ int count[NV * kLanes], tokens;
   const int t = threadIdx.x, sub = t % kLanes, q = t / kLanes;
-  for (int i = t; i < NV * kLanes; i += 256) count[i] = 0;
+  for (int i = t; i < NV * kLanes; i += NT) count[i] = 0;
   if (t == 0) tokens = 0;
   __syncthreads();
   const int first = int(blockIdx.x % chunks) * chunk, last = min(first + chunk, seq_len);
@@ -288,8 +320,8 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
     return is;
   };
   live = fetch(first + q, l);
-  for (int r = first + q; r < last; r += kRows) {
-    ahead = fetch(r + kRows, next);  // the next token's logits on their way
+  for (int r = first + q; r < last; r += ROWS) {
+    ahead = fetch(r + ROWS, next);  // the next token's logits on their way
     if (live) {
       Token<NV> a;
       a.set(l, sigmoid);
@@ -318,40 +350,45 @@ __global__ __launch_bounds__(256) void k_balance_parts(const T* __restrict__ log
     atomicAdd(&tokens, mine);
   }
   __syncthreads();
-  float* out = parts + int64_t(blockIdx.x) * part_words(E);
-  for (int e = t; e < E; e += 256) {
+  if constexpr (ONE) {
+    static_assert(NV * kLanes <= kWave && ROWS == kWave, "a lane for each expert and each row");
+    if (t >= kWave) return;
+    double p_sum = 0.0, z_sum = double(sz[t]);
+    if (t < E) {
+      for (int i = 0; i < ROWS; ++i) p_sum += double(sp[i][t]);
+      const double f = expert_share(count[t], E, K, tokens);
+      to.state[kStateHead + t] = float(f);
+      to.counts[t] = count[t];
+      p_sum = tokens == 0 ? 0.0 : f * p_sum / double(tokens);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      p_sum += __shfl_xor(p_sum, off, kWave);
+      z_sum += __shfl_xor(z_sum, off, kWave);
+    }
+    if (t == 0) {
+      int32_t* head = reinterpret_cast<int32_t*>(to.state);
+      head[0] = tokens > 0;
+      head[1] = head[kStateHead + E] = tokens;
+      to.loss[0] = total_loss(p_sum, z_sum, 1, tokens, to.alpha, to.z_coef);
+    }
+    return;
+  }
+  float* out = to.parts + int64_t(blockIdx.x) * part_words(E);
+  for (int e = t; e < E; e += NT) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) s += sp[i][e];
+    for (int i = 0; i < ROWS; ++i) s += sp[i][e];
     out[e] = s;
     reinterpret_cast<int*>(out)[E + e] = count[e];
   }
   if (t == 0) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) s += sz[i];
+    for (int i = 0; i < ROWS; ++i) s += sz[i];
     out[2 * E] = s;
     reinterpret_cast<int*>(out)[2 * E + 1] = tokens;
   }
-}
-
-// What the backward pass needs: words 0 and 1 the sequences and tokens that count,
-// then of every sequence f [E] and its tokens.
-constexpr int kStateHead = 4;
-__host__ __device__ constexpr int64_t state_words(int64_t B, int64_t E) { return kStateHead + B * (E + 1); }
-
-// Of every sequence, for the sums over them.
-struct SeqSum {
-  double loss, z;  // f.P, sum of lse^2
-  int64_t tokens;
-};
-
-// alpha / B' sum f.P + z / n sum lse^2, from the sums over the sequences.
-__device__ __forceinline__ float total_loss(double fp, double z, int64_t seqs, int64_t tokens, float alpha,
-                                            float z_coef) {
-  if (tokens == 0) return 0.f;
-  const double balance = double(alpha) * fp / double(seqs);
-  return float(z_coef == 0.f ? balance : balance + double(z_coef) * z / double(tokens));  // no 0 * infinity
 }
 
 // A sequence a workgroup of 256 or 1024 threads: its chunks added up by (expert, slice
@@ -422,7 +459,7 @@ __global__ __launch_bounds__(1024) void k_balance_seq(const float* __restrict__ 
   double fp = 0.0;
   if (t < E) {
     c = sc[t];
-    const double f = n == 0 ? 0.0 : double(E) * double(c) / (double(K) * double(n));
+    const double f = expert_share(c, E, K, n);
     state[kStateHead + int64_t(s) * (E + 1) + t] = float(f);
     seq_counts[int64_t(s) * E + t] = c;  // the counts themselves where there is one sequence
     fp = n == 0 ? 0.0 : f * sp[t] / double(n);
@@ -559,6 +596,13 @@ int64_t chunk_of(const moe_balance& b) {
 }
 int64_t chunks_of(const moe_balance& b) { return (b.seq_len + chunk_of(b) - 1) / chunk_of(b); }
 
+// Few tokens of one sequence, at most 64 experts: all in one workgroup, without the launch that adds
+// chunks up.  203 tokens of 8 experts: 5.8 us, 6.6 in two launches, and the call takes the host 2 us less;
+// 256: 6.6 and 6.6; 128 tokens of 64 experts: 6.8 and 7.0, 203: 9.1 and 7.3.
+bool in_one(const moe_balance& b) {
+  return b.N == b.seq_len && b.N <= (b.E <= 16 ? 4 : 2) * kOneRows && b.E <= kWave;
+}
+
 size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
 size_t parts_bytes(const moe_balance& b) {
   return pad(size_t(b.N / b.seq_len * chunks_of(b)) * part_words(b.E) * 4);
@@ -585,15 +629,25 @@ hipError_t loss_t(const moe_balance& b, const T* logits, const int32_t* topk, co
   float* parts = reinterpret_cast<float*>(ws);
   SeqSum* sums = reinterpret_cast<SeqSum*>(ws + parts_bytes(b));
   int32_t* seq_counts = B == 1 ? counts : reinterpret_cast<int32_t*>(ws + parts_bytes(b) + pad(size_t(B) * sizeof(SeqSum)));
+  const Results to{parts, state, loss, counts, b.alpha, b.z_coef};
+  const bool one = in_one(b);
   const hipError_t st = by_experts<T>(b.E, [&](auto nv, auto vec) {
-    const auto kernel =
-        topk == nullptr ? k_balance_parts<T, nv.value, vec.value, true> : k_balance_parts<T, nv.value, vec.value, false>;
-    kernel<<<dim3(unsigned(B * chunks)), dim3(256), 0, s>>>(logits, topk, bias, mask, parts, int(b.E), int(b.K),
-                                                            int(b.seq_len), int(chunk), int(chunks),
-                                                            b.score == MOE_SCORE_SIGMOID);
+    const bool sigmoid = b.score == MOE_SCORE_SIGMOID;
+    if constexpr (nv.value * kLanes <= kWave)
+      if (one) {
+        const auto kernel = topk == nullptr ? k_balance_parts<T, nv.value, vec.value, true, true>
+                                            : k_balance_parts<T, nv.value, vec.value, false, true>;
+        kernel<<<dim3(1), dim3(kOneRows * kLanes), 0, s>>>(logits, topk, bias, mask, to, int(b.E), int(b.K), int(b.N),
+                                                           int(b.N), 1, sigmoid);
+        return hipGetLastError();
+      }
+    const auto kernel = topk == nullptr ? k_balance_parts<T, nv.value, vec.value, true, false>
+                                        : k_balance_parts<T, nv.value, vec.value, false, false>;
+    kernel<<<dim3(unsigned(B * chunks)), dim3(256), 0, s>>>(logits, topk, bias, mask, to, int(b.E), int(b.K),
+                                                            int(b.seq_len), int(chunk), int(chunks), sigmoid);
     return hipGetLastError();
   });
-  if (st != hipSuccess) return st;
+  if (st != hipSuccess || one) return st;
   int lanes = 1;
   while (lanes < b.E) lanes *= 2;
   const unsigned threads = lanes * chunks > 2048 ? 1024 : 256;  // lanes is 256 at most

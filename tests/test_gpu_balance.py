@@ -92,7 +92,8 @@ def check(l, K, T, alpha, z, score, topk=None, mask=None, bias=None, loss=None, 
 
 CASES = [(1, 1, 1, 1), (1, 203, 8, 2), (3, 67, 12, 3), (1, 1, 256, 8), (5, 64, 7, 7), (1, 5000, 64, 6), (4, 513, 60, 4),
          (2, 300, 33, 5), (8, 16, 128, 8), (3, 130, 100, 2), (1, 700, 255, 8), (2, 1025, 256, 8), (300, 1, 16, 2),
-         (77, 3, 250, 1), (1, 40000, 4, 2)]
+         (77, 3, 250, 1), (1, 40000, 4, 2), (1, 100, 33, 4), (1, 128, 64, 6), (1, 129, 64, 6), (1, 256, 16, 2),
+         (1, 257, 16, 2)]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
