@@ -161,11 +161,11 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
                                                          const char* __restrict__ scales1,
                                                          const int32_t* __restrict__ tiles,
                                                          const int32_t* __restrict__ num_tiles,
-                                                         T* __restrict__ out, int L, int C) {
+                                                         T* __restrict__ out, int L, int C, bool seconds_last) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
   constexpr int SUB = MOE_TILE_M / kRows;
   constexpr int BN = (GATE_UP ? 1 : 2) * 32 * kGWaves;  // columns
-  const int ncols = (C + BN - 1) / BN, nrows = *num_tiles * SUB, all = nrows * ncols;
+  const int ncols = (C + BN - 1) / BN, tile_count = *num_tiles, nrows = tile_count * SUB, all = nrows * ncols;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = lane_id();
   const int kts = L / kMxTile, steps = (kts + kStep - 1) / kStep, groups = mx_groups(L);
   const int64_t strips = C / 16;
@@ -175,9 +175,10 @@ __global__ __launch_bounds__(kGNT, 2) void k_mx4_product(Rows x, const char* __r
   if (b < 0) return;
   const int group = b / (8 * ncols), in = b % (8 * ncols), high = min(8, nrows - group * 8);
   const int rt = group * 8 + in % high, ct = in / high;
+  const int part = seconds_last ? rt / tile_count : rt % SUB;
+  const int32_t* tile = tiles + 3 * (seconds_last ? rt - part * tile_count : rt / SUB);
   auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-  const int e = uniform(tiles[3 * (rt / SUB)]), row0 = uniform(tiles[3 * (rt / SUB) + 1]) + rt % SUB * kRows;
-  const int M = min(kRows, uniform(tiles[3 * (rt / SUB) + 2]) - rt % SUB * kRows);
+  const int e = uniform(tile[0]), row0 = uniform(tile[1]) + part * kRows, M = min(kRows, uniform(tile[2]) - part * kRows);
   if (M <= 0) return;
 
   // the wave's strips, two a pair; a pair past the last column repeats the last one, its results
@@ -329,10 +330,15 @@ hipError_t product(const moe_launch::Dims& d, const Rows& x, const moe_launch::M
   if (e != hipSuccess) return e;
   const int64_t pieces = moe_launch::max_tiles(d) * (MOE_TILE_M / kRows) * ((C + BN - 1) / BN);
   if (pieces > (int64_t(1) << 31) - 512) return hipErrorInvalidValue;
+  // With few rows an expert most list tiles have no second 128 rows: those workgroups, which end at once, hold
+  // up the ones behind them, so they come last.  With more, both read the expert's weights, side by side.
+  // Gate/up of 8 experts, H 4096, F 14336: 32 rows each 94 us with them last, 113 otherwise; 96 118 and 136;
+  // 128 164 and 142; down of 64 experts, H 2048, F 1408: 32 rows 21 and 27, 96 33 and 36, 128 39 and 42.
+  const bool seconds_last = d.NK() <= 96 * d.E;
   const unsigned grid = unsigned((pieces + 255) / 256 * 256);
   k_mx4_product<T, GATE_UP><<<dim3(grid), dim3(kGNT), bytes, s>>>(
       x, static_cast<const char*>(w0.codes), static_cast<const char*>(w0.scales),
-      static_cast<const char*>(w1.codes), static_cast<const char*>(w1.scales), tiles, num_tiles, out, L, C);
+      static_cast<const char*>(w1.codes), static_cast<const char*>(w1.scales), tiles, num_tiles, out, L, C, seconds_last);
   return hipGetLastError();
 }
 

@@ -207,7 +207,8 @@ def choice(seed, N, E, K, counts=None):
 PRODUCTS = [(1, 128, 128, 1, 1, None), (3, 128, 256, 2, 2, None), (65, 256, 128, 5, 3, None),
             (70, 640, 384, 64, 8, None), (257, 512, 640, 1, 1, None), (300, 1408, 256, 3, 2, None),
             (513, 384, 512, 4, 1, [0, 256, 1, 256]), (400, 128, 1408, 4, 1, [17, 0, 383, 0]),
-            (1000, 256, 256, 256, 8, None), (2100, 896, 384, 6, 4, None), (700, 2048, 256, 2, 1, [699, 1])]
+            (1000, 256, 256, 256, 8, None), (2100, 896, 384, 6, 4, None), (700, 2048, 256, 2, 1, [699, 1]),
+            (500, 256, 384, 8, 1, [300, 1, 128, 71, 0, 0, 0, 0])]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
