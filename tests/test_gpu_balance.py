@@ -355,3 +355,23 @@ def test_on_another_stream_and_captured():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((r.loss, r.counts, r.dlogits), want))
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]) and torch.equal(grad, want[2])
+
+
+def test_two_streams_at_once():
+    """Runners of their own on two streams, one with its sums in one workgroup: the results of one after the other."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    l = [logits_of(203, 8, torch.float32, seed=1), logits_of(4096, 64, torch.float32, seed=2)]
+    r = [MoEBalanceRunner(203, 8, 2, torch.float32, z_coef=0.01), MoEBalanceRunner(4096, 64, 6, torch.float32, seq_len=512)]
+    want = []
+    for run, v in zip(r, l):
+        loss = run.forward(v).clone()
+        want.append((loss, run.counts.clone(), run.backward().clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for run, v, s in zip(r, l, streams):
+            run.forward(v, stream=s)
+            run.backward(stream=s)
+    torch.cuda.synchronize()
+    for run, (loss, counts, d) in zip(r, want):
+        assert torch.equal(run.loss, loss) and torch.equal(run.counts, counts) and torch.equal(run.dlogits, d)

@@ -524,3 +524,41 @@ def test_on_another_stream_and_captured():
         assert torch.equal(many.y, eager[0]) and torch.equal(few.y, eager[1])
         if scale == 1.0:
             assert torch.equal(many.y, want[0]) and torch.equal(few.y, want[1])
+
+
+def test_two_streams_at_once():
+    """Runners of their own on two streams, sharing the weights: the results of one after the other."""
+    from mixture_experts_layer_sort_amd import MoEMx4DecodeRunner, MoEMx4Runner, MoEMx4Tensor as Q
+    H, F, E, K = 512, 4096, 4, 2
+    t, w, _ = layer_inputs(700, H, F, E, torch.bfloat16)
+    q = [Q.weights(v) for v in w]
+    x = [t["x"][:20].contiguous(), t["x"][20:40].contiguous()]
+    few = [MoEMx4DecodeRunner(20, H, F, E, K, torch.bfloat16) for _ in x]
+    many = MoEMx4Runner(700, H, F, E, K, torch.bfloat16)
+    want = [r.forward(v, t["w_r"], *q).clone() for r, v in zip(few, x)] + [many.forward(t["x"], t["w_r"], *q).clone()]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for r, v, s in zip(few, x, streams):
+            r.forward(v, t["w_r"], *q, stream=s)
+        many.forward(t["x"], t["w_r"], *q, stream=streams[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(r.y, y) for r, y in zip(few + [many], want))
+
+
+def test_the_same_expert_twice():
+    """A given choice that names an expert twice for a token: two rows of it."""
+    from mixture_experts_layer_sort_amd import MoEMx4Runner, MoEMx4Tensor as Q
+    N, H, F = 37, 256, 128
+    x = randn(1, N, H, dtype=torch.bfloat16)
+    q = Q.weights(randn(2, 3, H, F, scale=H ** -0.5)), Q.weights(randn(3, 3, H, F, scale=H ** -0.5))
+    r = MoEMx4Runner(N, H, F, 3, 2, torch.bfloat16)
+    one = torch.arange(N, dtype=torch.int32, device="cuda")[:, None] % 3
+    r.meta(one.expand(N, 2).contiguous())
+    act = r.gate_up(Q.rows(x), *q)
+    assert torch.equal(r.counts.cpu(), 2 * torch.bincount(one.cpu()[:, 0], minlength=3).int())
+    i = r.inv.view(N, 2).long()
+    assert torch.equal(act[i[:, 0]], act[i[:, 1]])
+    s = MoEMx4Runner(N, H, F, 3, 1, torch.bfloat16)
+    s.meta(one.contiguous())
+    assert torch.equal(act[i[:, 0]], s.gate_up(Q.rows(x), *q)[s.inv.long()])
