@@ -648,9 +648,9 @@ int moe_mx4_down(const moe_dims* d, const moe_mx4* act, const moe_mx4* w_down, c
 
 /* moe_decode with 4-bit experts (MOE_MX4_WEIGHTS): only the weights are in 4
  * bits, so a call reads about (chosen experts)*3*H*F*17/32 bytes.  x, W_r and
- * y have the type dims->dtype; x enters the products with all its bits, the
- * activations with 16 bits or more (bfloat16 layers) or 24 (float32), every sum is
- * float32, router logits float64, y is rounded once.  Weights below 2^-126
+ * y have the type dims->dtype; x and the float32 activations enter the products
+ * with all their bits, every sum is float32, router logits float64, y is rounded
+ * once.  Weights below 2^-126
  * may count as 0.  H, F or Fs > 2^20: MOE_EUNSUPPORTED.  Everything else, the
  * shared expert (ds and its weights [1, H, Fs] and [1, Fs, H]) included, as
  * moe_decode. */

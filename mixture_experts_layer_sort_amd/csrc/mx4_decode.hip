@@ -15,8 +15,8 @@
 //  - Eight values of a lane are one operand of a 16x16x32 bf16 matrix instruction:
 //    four conversions give them exactly, scale included.  The other operand is 16
 //    token rows, packed so that a load of it is contiguous over the lanes.
-//  - float32 rows enter as the exact sum of three bf16 operands, activations of
-//    bfloat16 layers as the sum of two.
+//  - float32 rows, and the activations of either type, enter as the exact sum of
+//    three bf16 operands.
 // Weights are the row operand, so that a lane ends with four neighbouring columns
 // of one token.
 #include <algorithm>
@@ -30,10 +30,10 @@ namespace {
 using namespace moe;
 
 // Eight float32 values as the sum of P bf16 operands.  P = 3: their bits cut in
-// three, exact.  P = 2: the nearest bf16 and the rest, rounded: 2^-16 of the value
-// at most.  P = 1: they are bf16.  An infinite or NaN value is all in the first.
+// three, exact.  P = 1: they are bf16.  An infinite or NaN value is all in the first.
 template <int P>
 __device__ __forceinline__ void split(const float* v, words4_t (&out)[P]) {
+  static_assert(P == 1 || P == 3, "exact");
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if constexpr (P == 1) {
@@ -44,10 +44,6 @@ __device__ __forceinline__ void split(const float* v, words4_t (&out)[P]) {
       for (int i = 0; i < 2; ++i) {
         const float f = v[2 * j + i];
         hi[i] = __float_as_uint(f) & 0xffff0000u;
-        if (P == 2) {
-          const uint32_t near = uint32_t(f32_to_bf16(f)) << 16;
-          hi[i] = (near & 0x7f800000u) == 0x7f800000u ? hi[i] : near;  // not to infinity
-        }
         const float r = isfinite(f) ? f - __uint_as_float(hi[i]) : 0.f;
         mid[i] = __float_as_uint(r);
         lo[i] = __float_as_uint(r - __uint_as_float(mid[i] & 0xffff0000u));
@@ -55,12 +51,8 @@ __device__ __forceinline__ void split(const float* v, words4_t (&out)[P]) {
       }
       constexpr uint32_t upper = 0x07060302u;
       out[0][j] = __builtin_amdgcn_perm(hi[1], hi[0], upper);
-      if constexpr (P == 2) {
-        out[1][j] = pack_bf16x2(__uint_as_float(mid[0]), __uint_as_float(mid[1]));
-      } else {
-        out[1][j] = __builtin_amdgcn_perm(mid[1], mid[0], upper);
-        out[2][j] = __builtin_amdgcn_perm(lo[1], lo[0], upper);
-      }
+      out[1][j] = __builtin_amdgcn_perm(mid[1], mid[0], upper);
+      out[2][j] = __builtin_amdgcn_perm(lo[1], lo[0], upper);
     }
   }
 }
@@ -97,6 +89,9 @@ __device__ __forceinline__ bf16x8_t values(uint32_t w, float scale) {
   b[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
   return __builtin_bit_cast(bf16x8_t, b);
 }
+
+// Operands of an activation: all 24 bits of it, whatever the layer's type.
+constexpr int kActParts = 3;
 
 // Rows as operands: the eight values of operand 4*kt + j that lane (g, c) takes of row
 // r start at p[kt * tile + j * word + r * row + g * group], plane by plane.
@@ -337,7 +332,7 @@ __device__ __forceinline__ void by_rows(int M, F f) {
 
 // Activations of CG strips of one expert's gate and up for the M rows slot(0 ..), as
 // operands.
-template <int MT, int CG, int PX, int PA, typename Slot>
+template <int MT, int CG, int PX, typename Slot>
 __device__ __forceinline__ void gate_up_rows(const Operands& x, const Strips& w, int64_t col0, int64_t F, Slot slot,
                                              int M, int div, const float* gates, bf16_t* act, int64_t R,
                                              f32x4_t* red) {
@@ -357,11 +352,11 @@ __device__ __forceinline__ void gate_up_rows(const Operands& x, const Strips& w,
     activate(v[0], v[1], gates != nullptr ? gates[row] : 1.f, f);
 #pragma unroll
     for (int i = 4; i < 8; ++i) f[i] = 0.f;
-    words4_t o[PA];
-    split<PA>(f, o);
+    words4_t o[kActParts];
+    split<kActParts>(f, o);
     bf16_t* to = act + operand_at(col0 + 16 * s + 4 * (lane / 16), row, R);
 #pragma unroll
-    for (int p = 0; p < PA; ++p) *reinterpret_cast<uint2*>(to + p * R * F) = make_uint2(o[p][0], o[p][1]);
+    for (int p = 0; p < kActParts; ++p) *reinterpret_cast<uint2*>(to + p * R * F) = make_uint2(o[p][0], o[p][1]);
   });
 }
 
@@ -372,7 +367,7 @@ template <typename T, int MTMAX, int CG, bool ROUTE>
 __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_gate_up(
     Operands x, View wg, View wu, View swg, View swu, int32_t* __restrict__ topk_out, float* __restrict__ gates_out,
     Route<T> route, bf16_t* __restrict__ act, bf16_t* __restrict__ sact, Shape q) {
-  constexpr int PX = sizeof(T) == 2 ? 1 : 3, PA = sizeof(T) == 2 ? 2 : 3;
+  constexpr int PX = sizeof(T) == 2 ? 1 : 3;
   __shared__ Units units;
   __shared__ f32x4_t red[kWaves * 2 * CG * kWave];
   const int32_t* topk = topk_out;
@@ -400,7 +395,7 @@ __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_gate_up(
                    q.H / kMxTile};
     const int first = uniform(units.start[u]), M = routed ? uniform(units.start[u + 1]) - first : q.N;
     by_rows<MTMAX>(M, [&](auto mt, int m0, int m) {
-      gate_up_rows<decltype(mt)::value, CG, PX, PA>(
+      gate_up_rows<decltype(mt)::value, CG, PX>(
           x, w, col0, F, [&](int r) { return routed ? int(units.slots[first + m0 + r]) : m0 + r; }, m,
           routed ? q.K : 1, routed ? gates : nullptr, routed ? act : sact, routed ? int64_t(q.N) * q.K : q.N, red);
     });
@@ -409,17 +404,17 @@ __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_gate_up(
 
 // CG strips of one expert's down product for the M rows slot(0 ..), the contraction's
 // tiles from .. to (`from` a multiple of 4): sums to out[slot][H].
-template <int MT, int CG, int PA, typename Slot>
+template <int MT, int CG, typename Slot>
 __device__ __forceinline__ void down_rows(const Operands& a, const Strips& w, int64_t col0, int64_t H, Slot slot,
                                           int M, float* out, int from, int to, f32x4_t* red) {
-  constexpr int U = kUnroll<CG, MT, PA>;
+  constexpr int U = kUnroll<CG, MT, kActParts>;
   const int c = lane_id() % 16, wave = wave_id();
   f32x4_t acc[MT][CG];
   clear(acc);
   int at[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) at[m] = slot(16 * m + c < M ? 16 * m + c : 0);
-  for (int kt = from + wave * U; kt < to; kt += kWaves * U) multiply<MT, 1, CG, U, PA>(w, a, kt, at, acc);
+  for (int kt = from + wave * U; kt < to; kt += kWaves * U) multiply<MT, 1, CG, U, kActParts>(w, a, kt, at, acc);
   join<MT, 1, CG, kWaves>(acc, red, [&](int m, int s, int lane, const f32x4_t* v) {
     const int r = 16 * m + lane % 16;
     if (r < M) *reinterpret_cast<f32x4_t*>(out + slot(r) * H + col0 + 16 * s + 4 * (lane / 16)) = v[0];
@@ -428,7 +423,7 @@ __device__ __forceinline__ void down_rows(const Operands& a, const Strips& w, in
 
 // More than one token: ys [part][slot][H], then sys [part][token][H] of the shared expert.  Pieces
 // as in k_mx4_gate_up.
-template <int MTMAX, int CG, int PA>
+template <int MTMAX, int CG>
 __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_down(const bf16_t* __restrict__ act,
                                                                      const bf16_t* __restrict__ sact, View wd,
                                                                      View swd, const int32_t* __restrict__ topk,
@@ -448,7 +443,7 @@ __global__ __launch_bounds__(kNT, MTMAX > 2 ? 1 : 2) void k_mx4_down(const bf16_
     const Strips w{{d.code(strip, F), nullptr}, {d.scale(strip, F), nullptr}, F / kMxTile};
     const int first = uniform(units.start[u]), M = routed ? uniform(units.start[u + 1]) - first : q.N;
     by_rows<MTMAX>(M, [&](auto mt, int m0, int m) {
-      down_rows<decltype(mt)::value, CG, PA>(
+      down_rows<decltype(mt)::value, CG>(
           packed(routed ? act : sact, R, F), w, col0, q.H,
           [&](int r) { return routed ? int64_t(units.slots[first + m0 + r]) : int64_t(m0 + r); }, m,
           (routed ? ys : sys) + part * R * q.H, part * per, min((part + 1) * per, F / kMxTile), red);
@@ -464,7 +459,7 @@ __global__ __launch_bounds__(kOneWaves* kWave) void k_mx4_down_one(const bf16_t*
                                                                    const bf16_t* __restrict__ sact, View wd, View swd,
                                                                    const int32_t* __restrict__ topk,
                                                                    T* __restrict__ y, Shape q) {
-  constexpr int PA = sizeof(T) == 2 ? 2 : 3, U = kUnroll<1, 1, PA>;
+  constexpr int U = kUnroll<1, 1, kActParts>;
   __shared__ f32x4_t red[kOneWaves * kWave];
   const int wave = wave_id();
   const int64_t col0 = int64_t(blockIdx.x) * 16;
@@ -477,7 +472,7 @@ __global__ __launch_bounds__(kOneWaves* kWave) void k_mx4_down_one(const bf16_t*
     const int64_t strip = (sh ? 0 : int64_t(uniform(topk[k])) * (q.H / 16)) + blockIdx.x;
     const View& d = sh ? swd : wd;
     const int at[1] = {k};
-    multiply<1, 1, 1, U, PA>(Strips{{d.code(strip, F), nullptr}, {d.scale(strip, F), nullptr}, F / kMxTile},
+    multiply<1, 1, 1, U, kActParts>(Strips{{d.code(strip, F), nullptr}, {d.scale(strip, F), nullptr}, F / kMxTile},
                              packed(sh ? sact : act, sh ? 1 : q.K, F), (sh ? i - routed : i % per) * U, at, acc);
   }
   join<1, 1, 1, kOneWaves>(acc, red, [&](int, int, int lane, const f32x4_t* v) {
@@ -517,7 +512,7 @@ Plan plan(const moe_launch::Dims& d, int64_t Fs) {
   Plan p;
   p.q = Shape{int(d.N), int(d.H), int(d.F), int(Fs), int(d.E), int(d.K), int(std::min(d.NK(), d.E)), 1};
   const bool bf = d.dtype == MOE_BF16;
-  const int64_t NK = d.NK(), px = bf ? 1 : 3, pa = bf ? 2 : 3;
+  const int64_t NK = d.NK(), px = bf ? 1 : 3;
   const double used = double(d.E) * (1.0 - std::pow(1.0 - double(d.K) / double(d.E), double(d.N)));
   const double rows = double(NK) / used;
   p.route = d.N <= 16 && d.N * d.E <= kPairs;
@@ -539,8 +534,8 @@ Plan plan(const moe_launch::Dims& d, int64_t Fs) {
   };
   p.logits = take(size_t(p.logit_parts) * d.N * d.E * sizeof(double));
   p.xp = take(p.logit_parts == 0 ? 0 : size_t(px) * d.N * d.H * 2);
-  p.act = take(size_t(pa) * NK * d.F * 2);
-  p.sact = take(size_t(pa) * d.N * Fs * 2);
+  p.act = take(size_t(kActParts) * NK * d.F * 2);
+  p.sact = take(size_t(kActParts) * d.N * Fs * 2);
   p.ys = take(d.N == 1 ? 0 : size_t(p.q.parts) * NK * d.H * 4);
   p.sys = take(d.N == 1 || Fs == 0 ? 0 : size_t(p.q.parts) * d.N * d.H * 4);
   p.bytes = at;
@@ -597,7 +592,7 @@ hipError_t down(const Plan& p, const Args<T>& a, hipStream_t s) {
   const Shape& q = p.q;
   float* ys = reinterpret_cast<float*>(a.ws + p.ys);
   float* sys = reinterpret_cast<float*>(a.ws + p.sys);
-  k_mx4_down<MTMAX, CG, sizeof(T) == 2 ? 2 : 3>
+  k_mx4_down<MTMAX, CG>
       <<<grid_of((int64_t(q.units) + (q.Fs > 0 ? 1 : 0)) * q.parts * q.H / (16 * CG)), dim3(kNT), 0, s>>>(
           reinterpret_cast<const bf16_t*>(a.ws + p.act), reinterpret_cast<const bf16_t*>(a.ws + p.sact), a.wd, a.swd,
           a.topk, ys, sys, q);

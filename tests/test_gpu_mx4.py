@@ -562,3 +562,40 @@ def test_the_same_expert_twice():
     s = MoEMx4Runner(N, H, F, 3, 1, torch.bfloat16)
     s.meta(one.contiguous())
     assert torch.equal(act[i[:, 0]], s.gate_up(Q.rows(x), *q)[s.inv.long()])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,F,E", [(1, 128, 1), (3, 256, 2), (16, 128, 1), (24, 256, 2), (40, 384, 1), (64, 128, 2),
+                                   (16, 6528, 8), (24, 6528, 8), (64, 6656, 8)])
+def test_decode_activations_keep_24_bits(dtype, N, F, E):
+    """Tokens with one nonzero value, so that G and U are single exact products.  Neighbouring hidden columns have
+    the same G, and U of 3 : 1 (times powers of two), so their activations are as 3 : 1 too; each column of W_down
+    weighs one such pair with 1 : -3, so that the sum is 0 but for the activations' own errors: 8 u of each, and
+    4 u of the sum's.  |y| <= 12 u |A|.|W_down|.  All E experts are chosen with gates of 1/E (exact); all but one
+    have a W_down of 0.  Activations of 16 bits are off by up to 2^-18 of themselves: five times that bound."""
+    from mixture_experts_layer_sort_amd import MoEMx4DecodeRunner, MoEMx4Tensor as Q
+    g = torch.Generator()
+    g.manual_seed(N + F)
+    H, e, P = 128, E // 2, F // 2
+    pick = lambda n, *shape: torch.randint(n, shape, generator=g)  # noqa: E731
+    x, wr = torch.zeros(N, H), torch.zeros(H, E)
+    x[:, 77] = (0.5 + 1.5 * torch.rand(N, generator=g)).bfloat16().float()
+    wg, wu, wd = torch.zeros(E, H, F), torch.zeros(E, H, F), torch.zeros(E, F, H)
+    same = GRID.float()[1 + pick(7, E, P)] * torch.exp2(-pick(4, E, P).float())
+    wg[:, 77] = same.repeat_interleave(2, 1)
+    i, j = pick(2, E, P).float(), pick(2, E, P).float()
+    wu[:, 77, 0::2], wu[:, 77, 1::2] = 3 * torch.exp2(i), torch.exp2(j)
+    pair, h = pick(P, H), torch.arange(H)
+    wd[e, 2 * pair, h], wd[e, 2 * pair + 1, h] = torch.exp2(j - i)[e, pair], -3.0
+    for w in (wg, wu, wd):
+        assert torch.equal(quantised(w)[0], w.double())  # exact in 4 bits
+    G, Uu = x.double()[:, 77:78] * wg[e, 77].double(), x.double()[:, 77:78] * wu[e, 77].double()
+    A = G * torch.sigmoid(G) * Uu / E
+    ref, bound = A @ wd[e].double(), 12 * U * (A.abs() @ wd[e].double().abs())
+    assert bool((ref.abs() <= 2.0 ** -48 * bound / U).all())
+    r = MoEMx4DecodeRunner(N, H, F, E, E, dtype)
+    y = r.forward(x.cuda().to(dtype), wr.cuda().to(dtype), *(Q.weights(w.cuda()) for w in (wg, wu, wd)))
+    s = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    worst = float(((y.cpu().double() - ref).abs() / ((1 + s) * 1.01 * bound)).max())
+    print(f"[mx4 decode] worst err/tol {worst:.3f}", flush=True)
+    assert worst <= 1.0
