@@ -242,11 +242,13 @@ struct View {
   }
 };
 
-// gate * silu(G) * U of four columns.  The hardware's reciprocal is good to 1 ulp;
-// below 2^-126 it gives 0, an activation of less than 1e-36 of the up product.
+// gate * silu(G) * U of four columns, from exp(-|G|), which does not overflow.
 __device__ __forceinline__ void activate(const f32x4_t& g, const f32x4_t& u, float gate, float* v) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] = gate * (g[r] * __builtin_amdgcn_rcpf(1.0f + expf(-g[r])) * u[r]);
+  for (int r = 0; r < 4; ++r) {
+    const float t = expf(-fabsf(g[r]));
+    v[r] = gate * ((g[r] < 0.f ? g[r] * t : g[r]) / (1.0f + t) * u[r]);
+  }
 }
 
 // Tiles a wave has under way: 16 KiB of weights at most, half of it where the rows

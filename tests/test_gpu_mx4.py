@@ -599,3 +599,27 @@ def test_decode_activations_keep_24_bits(dtype, N, F, E):
     worst = float(((y.cpu().double() - ref).abs() / ((1 + s) * 1.01 * bound)).max())
     print(f"[mx4 decode] worst err/tol {worst:.3f}", flush=True)
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [1, 5, 24])
+def test_decode_silu_far_below_zero(dtype, N):
+    """G around -88, where 1 + exp(-G) is past 2^126 and silu(G) a normal 1e-36.  exp(G) below 2^-126 comes in steps
+    of 2^-149, at -88.2 half of one is 2^-22 of it; 16 u of an activation and its gate, F + 16 of the sum, all of whose
+    terms are equal: |y - ref| <= (s + 2^-21 + (F + 32) u) |ref|."""
+    from mixture_experts_layer_sort_amd import MoEMx4DecodeRunner, MoEMx4Tensor as Q
+    H = F = 128
+    x, wr = torch.zeros(N, H), torch.zeros(H, 1)
+    x[:, 3] = torch.tensor([14.5625, 14.625, 14.6875])[torch.arange(N) % 3]
+    wg, wu, wd = torch.zeros(1, H, F), torch.zeros(1, H, F), torch.zeros(1, F, H)
+    wg[:, 3], wu[:, 3] = -6.0, 2.0 ** 20
+    wd[:] = 2.0 ** 60
+    G, Uu = x.double()[:, 3:4] * -6.0, x.double()[:, 3:4] * 2.0 ** 20
+    assert bool((G < -87.35).all()) and bool((G > -88.2).all())
+    ref = (G * torch.sigmoid(G) * Uu * F * 2.0 ** 60).expand(N, H)
+    r = MoEMx4DecodeRunner(N, H, F, 1, 1, dtype)
+    y = r.forward(x.cuda().to(dtype), wr.cuda().to(dtype), *(Q.weights(w.cuda()) for w in (wg, wu, wd))).cpu().double()
+    s = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    worst = float(((y - ref).abs() / ((s + 2.0 ** -21 + (F + 32) * U) * ref.abs())).max())
+    print(f"[mx4 decode] worst err/tol {worst:.3f}", flush=True)
+    assert worst <= 1.0
