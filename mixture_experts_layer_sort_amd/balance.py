@@ -17,7 +17,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib as L
-from .layer import _cuda_device, _dense, _expect, _on, _stream_of
+from .layer import _Made, _cuda_device, _dense, _expect, _on, _stream_of
 
 _SCORES = {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}
 
@@ -63,6 +63,7 @@ class MoEBalanceRunner:
         self.dlogits = torch.empty((N, E), dtype=dtype, device=dev)
         self._at = self.loss.data_ptr(), self.counts.data_ptr(), self.state.data_ptr(), self.ws.data_ptr()
         self._sizes, self._d_at = (state, ws), self.dlogits.data_ptr()
+        self._made = _Made(dev)
         self.inputs = None
 
     def forward(self, logits, topk=None, mask=None, bias=None, stream=None):
@@ -79,8 +80,9 @@ class MoEBalanceRunner:
         if mask is not None:
             with _stream_of(dev, stream):
                 mask = _mask(mask, self.N, dev)
-        if self.N:
-            with _on(dev):
+        with _on(dev):
+            stream = self._made.before(dev, stream)
+            if self.N:
                 L.moe_balance_loss(self.b, logits, topk, bias, mask, *self._at, stream, self._sizes)
         self.inputs = logits, mask
         return self.loss

@@ -378,6 +378,29 @@ def _stream_of(dev: torch.device, stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream)
 
 
+class _Made:
+    """The stream on which buffers were made.  The allocator hands out memory that work queued there
+    may still use, and first values are written there, so a first call on another stream waits for it.
+    Later calls come in the caller's order, as they share the buffers."""
+
+    def __init__(self, dev: torch.device):
+        self.stream = torch.cuda.current_stream(dev) if dev.type == "cuda" else None
+
+    def before(self, dev: torch.device, stream) -> int:
+        """The raw handle of a call's ``stream`` (dev is current), behind the making."""
+        raw = L._stream(stream)
+        if self.stream is not None:
+            if raw != self.stream.cuda_stream:
+                with _stream_of(dev, raw):
+                    # a captured call cannot wait for a stream outside its graph; torch.cuda.graph waits
+                    # for the device first
+                    if torch.cuda.is_current_stream_capturing():
+                        return raw
+                    torch.cuda.current_stream().wait_stream(self.stream)
+            self.stream = None
+        return raw
+
+
 def _expect(name: str, t: torch.Tensor, shape, dtype: torch.dtype, dev: torch.device):
     if t.shape != shape or t.dtype != dtype or t.device != dev:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")

@@ -21,12 +21,15 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from .layer import _cuda_device, _dense, _expect, _on
+from .layer import _Made, _cuda_device, _expect, _on, _stream_of
 
 
 class MoEMx4Tensor:
     """Codes and scales of a tensor in 4 bits, in device memory of its own.
-    ``shape`` is that of the values it stands for; ``order`` a moe_mx4_order."""
+    ``shape`` is that of the values it stands for; ``order`` a moe_mx4_order.
+    As with any tensor, a call on another stream than the one that filled it comes
+    behind that one in the caller's order, and record_stream() keeps its memory
+    from new tensors until such a call has ended."""
 
     def __init__(self, order: int, shape, device="cuda"):
         """Room for weights of shape [count, K, cols] or rows [N, K]; fill it
@@ -43,18 +46,28 @@ class MoEMx4Tensor:
         self.codes = torch.empty((max(16, need[0]),), dtype=torch.uint8, device=dev)
         self.scales = torch.empty((max(16, need[1]),), dtype=torch.uint8, device=dev)
         self.mx4 = L.mx4(self.codes, self.scales)
+        self._made = _Made(dev)
 
     @classmethod
     def weights(cls, w, stream=None) -> "MoEMx4Tensor":
         """Quantised weights w [count, K, cols] or [K, cols] (one matrix), float32
         or bfloat16."""
         w = w[None] if w.dim() == 2 else w
-        return cls(L.MOE_MX4_WEIGHTS, w.shape, w.device).quantize(w, stream)
+        with _stream_of(w.device, stream):
+            q = cls(L.MOE_MX4_WEIGHTS, w.shape, w.device)
+        return q.quantize(w, stream)
 
     @classmethod
     def rows(cls, x, stream=None) -> "MoEMx4Tensor":
         """Quantised token rows x [N, K]."""
-        return cls(L.MOE_MX4_ROWS, x.shape, x.device).quantize(x, stream)
+        with _stream_of(x.device, stream):
+            q = cls(L.MOE_MX4_ROWS, x.shape, x.device)
+        return q.quantize(x, stream)
+
+    def record_stream(self, stream):
+        """As torch.Tensor.record_stream."""
+        self.codes.record_stream(stream)
+        self.scales.record_stream(stream)
 
     def quantize(self, v, stream=None) -> "MoEMx4Tensor":
         """Take over the values of v; returns self."""
@@ -62,13 +75,14 @@ class MoEMx4Tensor:
         code = L.dtype_code(v.dtype)
         if self.shape[0]:
             with _on(self.device):
-                L.moe_mx4_quantize(self.order, *self._sizes, code, v, self.mx4, stream)
+                L.moe_mx4_quantize(self.order, *self._sizes, code, v, self.mx4, self._made.before(self.device, stream))
         return self
 
     def dequantize(self, dtype: Optional[torch.dtype] = None, out=None, stream=None):
         """The values, as a new tensor (bfloat16 by default) or in ``out``."""
         if out is None:
-            out = torch.empty(self.shape, dtype=torch.bfloat16 if dtype is None else dtype, device=self.device)
+            with _stream_of(self.device, stream):
+                out = torch.empty(self.shape, dtype=torch.bfloat16 if dtype is None else dtype, device=self.device)
         _expect("out", out, self.shape, out.dtype if dtype is None else dtype, self.device)
         code = L.dtype_code(out.dtype)
         if self.shape[0]:
@@ -110,6 +124,7 @@ class MoEMx4DecodeRunner:
         self.topk, self.gates, self.y = self._topk, self._gates, self._y
         # of any first n rows too
         self._at = self._topk.data_ptr(), self._gates.data_ptr(), self._y.data_ptr(), self.ws.data_ptr()
+        self._made = _Made(dev)
 
     def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None, shared=None):
         """Returns y [n, H] of x [n, H], n <= max_tokens; topk and gates [n, K]
@@ -138,7 +153,7 @@ class MoEMx4DecodeRunner:
         d, ds = self._dims[n]
         if n:
             with _on(dev):
-                L.moe_mx4_decode(d, x, w_r, bias, *w, ds, *s, *self._at, stream, self._ws_bytes)
+                L.moe_mx4_decode(d, x, w_r, bias, *w, ds, *s, *self._at, self._made.before(dev, stream), self._ws_bytes)
         if n != self.y.shape[0]:  # not before the call: a refused one changes nothing
             self.topk, self.gates, self.y = self._topk[:n], self._gates[:n], self._y[:n]
         return self.y
@@ -179,6 +194,7 @@ class MoEMx4Runner:
         self.act = make((NK, F), dtype=dtype, device=dev)
         self.ys = make((NK, H), dtype=dtype, device=dev)
         self.y = torch.empty((N, H), dtype=dtype, device=dev)
+        self._made = _Made(dev)
 
     def meta(self, topk, stream=None):
         """Group the rows by a given choice topk [N, K] int32, values in [0, E)."""
@@ -187,7 +203,7 @@ class MoEMx4Runner:
         if self.N:
             with _on(self.device):
                 L.moe_permute_meta_capacity(self.d, topk, cap, self.sorted_flat, self.inv, self.counts, self.offsets,
-                                            self.tiles, self.num_tiles, self.ws, stream)
+                                            self.tiles, self.num_tiles, self.ws, self._made.before(self.device, stream))
 
     def gate_up(self, xq, w_gate, w_up, stream=None):
         """silu(G) * U [N*K, F] of quantised token rows xq [N, H], in the grouped order of
@@ -199,7 +215,7 @@ class MoEMx4Runner:
         if self.N:
             with _on(dev):
                 L.moe_mx4_gate_up(self.d, q[0], self.sorted_flat, q[1], q[2], self.tiles, self.num_tiles, self.act,
-                                  stream)
+                                  self._made.before(dev, stream))
         return self.act
 
     def down(self, aq, w_down, stream=None):
@@ -209,7 +225,7 @@ class MoEMx4Runner:
         w = _expect_mx4("w_down", w_down, L.MOE_MX4_WEIGHTS, (self.E, self.F, self.H), dev)
         if self.N:
             with _on(dev):
-                L.moe_mx4_down(self.d, a, w, self.tiles, self.num_tiles, self.ys, stream)
+                L.moe_mx4_down(self.d, a, w, self.tiles, self.num_tiles, self.ys, self._made.before(dev, stream))
         return self.ys
 
     def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None):
@@ -227,7 +243,8 @@ class MoEMx4Runner:
         cap = 2 ** 31 - 1 if self.capacity is None else self.capacity
         with _on(dev):
             L.moe_route_meta(self.d, x, w_r, bias, cap, self.topk, self.gates, self.sorted_flat, self.inv,
-                             self.counts, self.offsets, self.tiles, self.num_tiles, self.ws, stream)
+                             self.counts, self.offsets, self.tiles, self.num_tiles, self.ws,
+                             self._made.before(dev, stream))
         act = self.gate_up(self.xq.quantize(x, stream), w_gate, w_up, stream)
         self.down(self.aq.quantize(act, stream), w_down, stream)
         with _on(dev):

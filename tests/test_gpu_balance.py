@@ -375,3 +375,23 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for run, (loss, counts, d) in zip(r, want):
         assert torch.equal(run.loss, loss) and torch.equal(run.counts, counts) and torch.equal(run.dlogits, d)
+
+
+def test_runner_of_another_stream():
+    """A runner made behind work of the current stream and called on another one: its first values (zeros) come
+    before the call's, not after them."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    l = logits_of(203, 8, torch.float32)
+    r = MoEBalanceRunner(203, 8, 2, torch.float32, z_coef=0.01)
+    want = r.forward(l).clone(), r.counts.clone(), r.backward().clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    v = torch.zeros(1 << 28, device="cuda")
+    for _ in range(40):
+        v.add_(1.0)
+    r = MoEBalanceRunner(203, 8, 2, torch.float32, z_coef=0.01)
+    r.forward(l, stream=side)
+    r.backward(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((r.loss, r.counts, r.dlogits), want))

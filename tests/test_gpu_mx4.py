@@ -623,3 +623,56 @@ def test_decode_silu_far_below_zero(dtype, N):
     worst = float(((y - ref).abs() / ((s + 2.0 ** -21 + (F + 32) * U) * ref.abs())).max())
     print(f"[mx4 decode] worst err/tol {worst:.3f}", flush=True)
     assert worst <= 1.0
+
+
+def _busy():
+    """Work of some ten milliseconds on the current stream."""
+    v = torch.zeros(1 << 28, device="cuda")
+    for _ in range(40):
+        v.add_(1.0)
+
+
+@pytest.mark.parametrize("rows", [True, False])
+def test_tensors_of_another_stream(rows):
+    """4-bit tensors and their values, made on a side stream while the current one still works on memory that it has
+    given back: the values of a call on one stream."""
+    from mixture_experts_layer_sort_amd import MoEMx4Tensor as Q
+    v = randn(1, 2048, 2048)
+    make = Q.rows if rows else Q.weights
+    plain = make(v)
+    want = plain.dequantize()
+    sizes = [plain.codes.numel(), plain.scales.numel(), 2 * want.numel()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy()
+    for n in sizes:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x55)
+    q = make(v, stream=side)
+    got = q.dequantize(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(q.codes, plain.codes) and torch.equal(q.scales, plain.scales) and torch.equal(got, want)
+    q.record_stream(torch.cuda.current_stream())
+
+
+def test_runners_of_another_stream():
+    """Runners made behind work of the current stream and called on another one: what they hold of their making
+    (zeros of rows that a capacity drops) comes before the call, not after it."""
+    from mixture_experts_layer_sort_amd import MoEMx4DecodeRunner, MoEMx4Runner, MoEMx4Tensor as Q
+    N, H, F, E, K = 600, 512, 512, 4, 2
+    t, w, _ = layer_inputs(N, H, F, E, torch.bfloat16)
+    q = [Q.weights(v) for v in w]
+    x16 = t["x"][:16].contiguous()
+    make = lambda: (MoEMx4Runner(N, H, F, E, K, torch.bfloat16, capacity=200),  # noqa: E731
+                    MoEMx4DecodeRunner(16, H, F, E, K, torch.bfloat16))
+    many, few = make()
+    want = many.forward(t["x"], t["w_r"], *q).clone(), few.forward(x16, t["w_r"], *q).clone(), many.act.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy()
+    many, few = make()
+    many.forward(t["x"], t["w_r"], *q, stream=side)
+    few.forward(x16, t["w_r"], *q, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(many.y, want[0]) and torch.equal(few.y, want[1]) and torch.equal(many.act, want[2])
