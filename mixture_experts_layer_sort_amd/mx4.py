@@ -184,7 +184,9 @@ class MoEMx4Runner:
         self.counts = torch.empty((E,), dtype=i32, device=dev)
         self.offsets = torch.empty((E + 1,), dtype=i32, device=dev)
         self.tiles = torch.empty((max(1, mt) * 3,), dtype=i32, device=dev)
-        self.num_tiles = torch.empty((1,), dtype=i32, device=dev)
+        # no tiles until meta() or forward() has run, so that products behind a captured one do nothing
+        self.num_tiles = torch.zeros((1,), dtype=i32, device=dev)
+        self._grouped = False
         need = [L.moe_workspace_bytes(self.d, e) for e in (L.MOE_ENTRY_ROUTE_META, L.MOE_ENTRY_PERMUTE_META)]
         self.ws = torch.empty((max(16, *need),), dtype=torch.uint8, device=dev)
         self.xq = MoEMx4Tensor(L.MOE_MX4_ROWS, (N, H), dev)
@@ -204,6 +206,11 @@ class MoEMx4Runner:
             with _on(self.device):
                 L.moe_permute_meta_capacity(self.d, topk, cap, self.sorted_flat, self.inv, self.counts, self.offsets,
                                             self.tiles, self.num_tiles, self.ws, self._made.before(self.device, stream))
+        self._grouped = True
+
+    def _expect_groups(self, name: str):
+        if not self._grouped:
+            raise RuntimeError(f"{name} before meta or forward")
 
     def gate_up(self, xq, w_gate, w_up, stream=None):
         """silu(G) * U [N*K, F] of quantised token rows xq [N, H], in the grouped order of
@@ -213,6 +220,7 @@ class MoEMx4Runner:
              _expect_mx4("w_gate", w_gate, L.MOE_MX4_WEIGHTS, (E, H, F), dev),
              _expect_mx4("w_up", w_up, L.MOE_MX4_WEIGHTS, (E, H, F), dev))
         if self.N:
+            self._expect_groups("gate_up")
             with _on(dev):
                 L.moe_mx4_gate_up(self.d, q[0], self.sorted_flat, q[1], q[2], self.tiles, self.num_tiles, self.act,
                                   self._made.before(dev, stream))
@@ -224,6 +232,7 @@ class MoEMx4Runner:
         a = _expect_mx4("aq", aq, L.MOE_MX4_ROWS, (self.N * self.K, self.F), dev)
         w = _expect_mx4("w_down", w_down, L.MOE_MX4_WEIGHTS, (self.E, self.F, self.H), dev)
         if self.N:
+            self._expect_groups("down")
             with _on(dev):
                 L.moe_mx4_down(self.d, a, w, self.tiles, self.num_tiles, self.ys, self._made.before(dev, stream))
         return self.ys
@@ -245,6 +254,7 @@ class MoEMx4Runner:
             L.moe_route_meta(self.d, x, w_r, bias, cap, self.topk, self.gates, self.sorted_flat, self.inv,
                              self.counts, self.offsets, self.tiles, self.num_tiles, self.ws,
                              self._made.before(dev, stream))
+        self._grouped = True
         act = self.gate_up(self.xq.quantize(x, stream), w_gate, w_up, stream)
         self.down(self.aq.quantize(act, stream), w_down, stream)
         with _on(dev):

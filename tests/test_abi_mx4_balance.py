@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from mixture_experts_layer_sort_amd import _lib as L
 
@@ -221,3 +222,23 @@ def test_balance_scratch_grows_with_sequences(lib, B_, T, E):
     assert L.moe_balance_state_bytes(b) >= 4 * B_ * (E + 1)
     assert 4 * B_ * (2 * E + 2) <= L.moe_balance_workspace_bytes(b) < BAD
     assert L.moe_balance_workspace_bytes(b) <= 4 * (B_ + 1024) * (2 * E + 2) + B_ * (E * 4 + 24) + 1024
+
+
+def test_products_before_any_grouping_are_refused(monkeypatch):
+    """gate_up() and down() of a runner that has no tile list yet (CPU tensors, the 4-bit ones without addresses)."""
+    from mixture_experts_layer_sort_amd import mx4
+    monkeypatch.setattr(L, "mx4", lambda codes, scales: None)
+    r = mx4.MoEMx4Runner(5, 128, 256, 2, 2, torch.float32, "cpu")
+    x, a = mx4.MoEMx4Tensor(R, (5, 128), "cpu"), mx4.MoEMx4Tensor(R, (10, 256), "cpu")
+    up, down = mx4.MoEMx4Tensor(W, (2, 128, 256), "cpu"), mx4.MoEMx4Tensor(W, (2, 256, 128), "cpu")
+    with pytest.raises(RuntimeError, match="before meta"):
+        r.gate_up(x, up, up)
+    with pytest.raises(RuntimeError, match="before meta"):
+        r.down(a, down)
+    assert int(r.num_tiles) == 0
+    with pytest.raises(ValueError):  # a refused grouping is none
+        r.meta(torch.zeros((4, 2), dtype=torch.int32))
+    with pytest.raises(RuntimeError):
+        r.down(a, down)
+    none = mx4.MoEMx4Runner(0, 128, 256, 2, 2, torch.float32, "cpu")
+    assert none.gate_up(mx4.MoEMx4Tensor(R, (0, 128), "cpu"), up, up).shape == (0, 256)
