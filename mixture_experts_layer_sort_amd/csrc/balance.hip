@@ -95,11 +95,24 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
   return max(v, uint32_t(MOE_DPP(int(v), 0x140)));
 }
 
+// exp(x) for x <= 0 (0 below 2^-126): the hardware's 2^h of h = x / ln 2, rounded, and the
+// first order of what the rounding (at most 2^-17) and the constant's leave out: about an
+// ulp of the hardware's, where 2^h alone is off by |x| 2^-24 of itself.
+__device__ __forceinline__ float exp_below(float x) {
+  constexpr double kLog2E = 1.4426950408889634074;
+  constexpr float kHigh = float(kLog2E), kLow = float(kLog2E - double(kHigh));
+  x = x < -200.f ? -200.f : x;  // NaN stays
+  const float h = x * kHigh, r = __builtin_amdgcn_exp2f(h);
+  return fmaf(r, fmaf(x, kLow, fmaf(x, kHigh, -h)) * float(1.0 / kLog2E), r);
+}
+// 1 / a for a from 1 to 2: the hardware's, which is off by an ulp, and a Newton step.
+__device__ __forceinline__ float inverse(float a) {
+  const float r = __builtin_amdgcn_rcpf(a);
+  return fmaf(fmaf(-a, r, 1.f), r, r);
+}
+
 // Probabilities of one token: soft the softmax, p the score's, rest 1 - sigmoid
-// (sigmoid scores), lse its log-sum-exp.  Places past E hold -inf: 0 in all.  The
-// hardware's exponential of x / ln 2 is off by about |x| 2^-24 of itself, its
-// reciprocal by one unit in the last place: about a third of the time of the exact
-// functions, which bound the kernel.
+// (sigmoid scores), lse its log-sum-exp.  Places past E hold -inf: 0 in all.
 template <int NV> struct Token {
   float soft[NV], p[NV], rest[NV], lse;
   __device__ __forceinline__ void set(const float (&l)[NV], bool sigmoid) {
@@ -110,33 +123,33 @@ template <int NV> struct Token {
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      soft[v] = __expf(l[v] - top);
+      soft[v] = exp_below(l[v] - top);
       sum += soft[v];
     }
     sum = lanes_sum(sum);
     lse = top + logf(sum);
-    const float inv = __builtin_amdgcn_rcpf(sum);
+    const float inv = 1.f / sum;
     if (sigmoid) {
       // Where all logits are negative every sigmoid may be tiny: there all of them
       // over exp(top), whose largest is 1 / (1 + exp(top)).
       float all = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const float t = __expf(-l[v]);  // infinite below -88: a sigmoid of 0
-        p[v] = __builtin_amdgcn_rcpf(1.f + t);
-        rest[v] = l[v] >= 0.f ? t * p[v] : 1.f - p[v];
+        const float t = exp_below(-fabsf(l[v])), large = inverse(1.f + t), small = t * large;
+        p[v] = l[v] < 0.f ? small : large;
+        rest[v] = l[v] < 0.f ? large : small;
         all += p[v];
       }
       if (top <= 0.f) {
-        const float down = __expf(top);
+        const float down = exp_below(top);
         all = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          p[v] = soft[v] * __builtin_amdgcn_rcpf(1.f + soft[v] * down);
+          p[v] = soft[v] * inverse(1.f + soft[v] * down);
           all += p[v];
         }
       }
-      const float a = __builtin_amdgcn_rcpf(lanes_sum(all));
+      const float a = 1.f / lanes_sum(all);
 #pragma unroll
       for (int v = 0; v < NV; ++v) p[v] *= a;
     }

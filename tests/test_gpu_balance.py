@@ -395,3 +395,34 @@ def test_runner_of_another_stream():
     side.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((r.loss, r.counts, r.dlogits), want))
+
+
+@pytest.mark.parametrize("top", [0.0, 1.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [4, 40, 256])
+def test_small_probabilities(E, score, top):
+    """Tokens whose first logit is 0 or 1 and whose others go down to -85 in steps of 2^-10, so that differences are
+    exact.  A gradient is c p_e (f_e - f.p) [1 - sigmoid].  A sum over the experts, of one sign, adds up E / 16 values in
+    a lane and sixteen lanes pairwise: E / 16 + 5 u of itself.  p_e: 3 u of an exponential, 3 u of a sigmoid, the sum, 2 u
+    of the quotient; f.p: the same and a product, and the sum; f_e 1 u; 10 u of the products.  So its error is at most
+    (E / 8 + 39) u c p_e (f_e + f.p) [1 - sigmoid].  An exponential that is off by |x| u alone is past that at 4 and
+    40 experts (61 to 65 u)."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    N = 512
+    g = torch.Generator(device="cuda")
+    g.manual_seed(E)
+    l = -torch.randint(1024, 85 * 1024, (N, E), generator=g, device="cuda").float() / 1024
+    l[:, 0] = top
+    ids = torch.randint(1, E, (N, 1), generator=g, device="cuda", dtype=torch.int32)
+    ids[:E - 1, 0] = torch.arange(1, E, device="cuda")
+    r = MoEBalanceRunner(N, E, 1, torch.float32, alpha=float(N), score=score)
+    r.forward(l, topk=ids)
+    d = r.backward().double()
+    x = l.double()
+    f = torch.bincount(ids[:, 0].long(), minlength=E).double() * E / N
+    p = torch.softmax(x, 1) if score == "softmax" else torch.sigmoid(x) / torch.sigmoid(x).sum(1, keepdim=True)
+    rest = torch.ones_like(x) if score == "softmax" else torch.sigmoid(-x)
+    fp = (p * f).sum(1, keepdim=True)
+    worst = float(((d - p * (f - fp) * rest).abs() / (p * (f + fp) * rest)).max() / U)
+    print(f"[balance] worst {worst:.1f} u", flush=True)
+    assert worst <= E / 8 + 39
