@@ -53,7 +53,7 @@ template <int NV, bool VEC> struct Place {
 };
 
 template <typename T, int NV, bool VEC>
-__device__ __forceinline__ void load_row(const T* __restrict__ p, int sub, int E, float (&l)[NV]) {
+__device__ __forceinline__ void load_row(const T* p, int sub, int E, float (&l)[NV]) {
   if constexpr (VEC) {
 #pragma unroll
     for (int v = 0; v < NV; v += 4) {
@@ -539,10 +539,11 @@ __global__ __launch_bounds__(256) void k_balance_total(const SeqSum* __restrict_
   }
 }
 
+// dlogits may be logits: a lane stores where it alone has loaded.
 template <typename T, int NV, bool VEC>
-__global__ __launch_bounds__(256) void k_balance_bwd(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
+__global__ __launch_bounds__(256) void k_balance_bwd(const T* logits, const uint8_t* __restrict__ mask,
                                                      const float* __restrict__ state, const float* __restrict__ dloss,
-                                                     T* __restrict__ dlogits, int64_t N, int E, int seq_len,
+                                                     T* dlogits, int64_t N, int E, int seq_len,
                                                      float alpha, float z_coef, bool sigmoid) {
   const int sub = threadIdx.x % kLanes;
   const int64_t n = int64_t(blockIdx.x) * kRows + threadIdx.x / kLanes;

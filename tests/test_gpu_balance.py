@@ -426,3 +426,19 @@ def test_small_probabilities(E, score, top):
     worst = float(((d - p * (f - fp) * rest).abs() / (p * (f + fp) * rest)).max() / U)
     print(f"[balance] worst {worst:.1f} u", flush=True)
     assert worst <= E / 8 + 39
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [1, 16, 33, 60, 128, 250, 256])
+def test_gradient_in_place_of_the_logits(E, dtype):
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    from mixture_experts_layer_sort_amd import _lib as L
+    N = 700
+    l = logits_of(N, E, dtype, seed=E)
+    mask = torch.arange(N, device="cuda") % 5 != 0
+    for score in ("softmax", "sigmoid"):
+        r = MoEBalanceRunner(N, E, 1, dtype, seq_len=100, alpha=0.3, z_coef=0.01, score=score)
+        r.forward(l, mask=mask)
+        want, d = r.backward().clone(), l.clone()
+        L.moe_balance_loss_bwd(r.b, d, mask, r.state, None, d)
+        assert torch.equal(d, want)
