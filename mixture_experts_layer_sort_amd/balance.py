@@ -5,9 +5,13 @@ MoELayerRunner's aux_alpha is the Switch loss of the layer's own logits over the
 whole batch.  Here the logits are given, sequences are balanced one by one, padding is
 left out, scores may be sigmoids, and the z loss keeps the logits small:
 
-    logits = x @ w_r
-    loss, counts = moe_balance_loss(logits, K, seq_len=T, mask=mask, alpha=0.01, z_coef=1e-3)
+    y, topk = moe_layer(x, w_r, w_gate, w_up, w_down, K, return_topk=True)
+    logits = x.float() @ w_r.float()
+    loss, counts = moe_balance_loss(logits, K, topk=topk, seq_len=T, mask=mask, alpha=0.01, z_coef=1e-3)
     (task_loss + loss).backward()
+
+topk is the layer's own choice: it is made on wider logits than a bfloat16 x @ w_r holds,
+whose equals are frequent, so a choice made again on those would count other experts.
 """
 from __future__ import annotations
 
@@ -152,9 +156,10 @@ def moe_balance_loss(logits, K: int, topk=None, mask=None, bias=None, seq_len: O
     counts [E] int32).
 
     The last axis but one and those before it are tokens, seq_len of them (None: all) a
-    sequence.  topk: the K experts that each token chose, int32 [..., K]; None: those of
-    largest logit (+ bias [E] float32, which moves the choice alone).  mask: bool or uint8
-    [...], false for padding.  score: "softmax" or "sigmoid" (normalised over the experts).
+    sequence.  topk: the K experts that each token chose, int32 [..., K] (moe_layer's, with
+    return_topk); None: those of largest logit (+ bias [E] float32, which moves the choice
+    alone).  mask: bool or uint8 [...], false for padding.  score: "softmax" or "sigmoid"
+    (normalised over the experts).
     loss = alpha / sequences * sum_s sum_e f_s,e P_s,e + z_coef * mean(logsumexp^2), f_s,e the
     share of a sequence's choices that expert e has, times E, and P_s,e its mean probability.
     A backward pass is captured into a graph only while no eager graph of the same leaves lives

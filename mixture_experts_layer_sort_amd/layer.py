@@ -306,12 +306,13 @@ class MoEFunction(torch.autograd.Function):
     is returned as a second output that carries no autograd edge: its
     gradient is added to the router's in the backward as if aux_grad * loss
     were part of the training loss (aux_grad is a constant, so no device
-    value is read back to the host).
+    value is read back to the host).  With return_topk the experts that each
+    token chose follow as a third output, int32 [N, K] without an edge.
     """
 
     @staticmethod
     def forward(ctx, x, w_r, w_gate, w_up, w_down, w_gate_s, w_up_s, w_down_s, K: int, bias, capacity, aux_alpha,
-                aux_grad, dw_gather):
+                aux_grad, dw_gather, return_topk: bool = False):
         N, H = x.shape
         E = w_r.shape[1]
         F = w_gate.shape[2]
@@ -324,34 +325,42 @@ class MoEFunction(torch.autograd.Function):
         ctx.aux_grad = aux_grad
         aux = r.aux_loss.clone() if aux_alpha is not None else torch.zeros((1,), dtype=torch.float32,
                                                                              device=x.device)
-        ctx.mark_non_differentiable(aux)
-        return y.clone(), aux
+        if not return_topk:
+            ctx.mark_non_differentiable(aux)
+            return y.clone(), aux
+        topk = r.topk.clone()  # the backward reads the runner's own
+        ctx.mark_non_differentiable(aux, topk)
+        return y.clone(), aux, topk
 
     @staticmethod
-    def backward(ctx, dy, _daux):
+    def backward(ctx, dy, *_):
         r = ctx.runner
         g = r.backward(dy.contiguous(), aux_grad=ctx.aux_grad)
         cast = lambda t: t.to(r.dtype)
         shared = ((cast(g["dw_gate_s"]), cast(g["dw_up_s"]), cast(g["dw_down_s"])) if r.shared_ffn is not None
                   else (None, None, None))
-        return ((g["dx"].clone(), cast(g["dw_r"]), cast(g["dw_gate"]), cast(g["dw_up"]), cast(g["dw_down"])) + shared
-                + (None,) * 6)
+        grads = (g["dx"].clone(), cast(g["dw_r"]), cast(g["dw_gate"]), cast(g["dw_up"]), cast(g["dw_down"])) + shared
+        return grads + (None,) * (len(ctx.needs_input_grad) - len(grads))
 
 
 def moe_layer(x, w_r, w_gate, w_up, w_down, K: int, bias=None, *, capacity: Optional[int] = None,
-              shared=None, aux_alpha: Optional[float] = None, aux_grad: float = 1.0, dw_gather: bool = False):
+              shared=None, aux_alpha: Optional[float] = None, aux_grad: float = 1.0, dw_gather: bool = False,
+              return_topk: bool = False):
     """Functional form of the layer with autograd support.
 
     shared = (W_gate_s [H,Fs], W_up_s [H,Fs], W_down_s [Fs,H]) adds a shared
     expert; capacity caps the rows per expert (token dropping); aux_alpha
     turns on the Switch load-balancing loss; dw_gather keeps no grouped copy
     of x for the weight gradients (less memory, slower).  Returns y, or
-    (y, aux_loss) when aux_alpha is set.
+    (y, aux_loss) when aux_alpha is set.  With return_topk the experts that
+    each token chose, int32 [N, K], come last: what a loss of the router's
+    own (moe_balance_loss) has to count.
     """
     ws = (None, None, None) if shared is None else tuple(shared)
-    y, aux = MoEFunction.apply(x, w_r, w_gate, w_up, w_down, ws[0], ws[1], ws[2], K, bias, capacity, aux_alpha,
-                               aux_grad, dw_gather)
-    return (y, aux) if aux_alpha is not None else y
+    y, aux, *topk = MoEFunction.apply(x, w_r, w_gate, w_up, w_down, ws[0], ws[1], ws[2], K, bias, capacity, aux_alpha,
+                                      aux_grad, dw_gather, return_topk)
+    out = (y,) + ((aux,) if aux_alpha is not None else ()) + tuple(topk)
+    return out if len(out) > 1 else y
 
 
 # ------------------------------------------------------------ around the layer

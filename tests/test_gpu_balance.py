@@ -442,3 +442,38 @@ def test_gradient_in_place_of_the_logits(E, dtype):
         want, d = r.backward().clone(), l.clone()
         L.moe_balance_loss_bwd(r.b, d, mask, r.state, None, d)
         assert torch.equal(d, want)
+
+
+def test_the_layers_own_choice_in_bf16():
+    """A bf16 training step as a user writes it: the loss counts the experts that the layer chose, which a choice made
+    again on bf16 logits does not; gradients are those of the loss and of the layer taken apart."""
+    from mixture_experts_layer_sort_amd import MoELayerRunner, moe_balance_loss, moe_layer
+    N, H, F, E, K = 4000, 128, 128, 64, 6
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    x = torch.randn((N, H), generator=g, device="cuda").bfloat16()
+    w = [(torch.randn(s, generator=g, device="cuda") * 0.1).bfloat16() for s in ((H, E), (E, H, F), (E, H, F), (E, F, H))]
+    leaves = [t.clone().requires_grad_() for t in (x, *w)]
+    y, topk = moe_layer(*leaves, K, return_topk=True)
+    assert topk.dtype == torch.int32 and topk.shape == (N, K) and not topk.requires_grad
+    loss, counts = moe_balance_loss(leaves[0].float() @ leaves[1].float(), K, topk=topk, alpha=0.1)
+    kept = topk.clone()
+    r = MoELayerRunner(N, H, F, E, K, torch.bfloat16)
+    r.forward(x, *w)
+    assert torch.equal(topk, r.topk) and torch.equal(counts, r.counts)
+    again = moe_balance_loss(x @ w[0], K)[1]
+    assert not torch.equal(again, counts)
+    # float32 logits are off by (H + 1) u |x|.|W_r|, probabilities by twice that of themselves
+    want, tol = reference((x.double() @ w[0].double()).float(), topk, None, N, 0.1, 0.0, "softmax")[:2]
+    off = (H + 1) * U * float((x.double().abs() @ w[0].double().abs()).max())
+    assert abs(float(loss.detach()) - want) <= 1.01 * (tol + 2 * off * want)
+    both = torch.autograd.grad(y.float().square().mean() + loss.sum(), leaves, retain_graph=True)
+    topk.zero_()  # the caller's own
+    again = torch.autograd.grad(y.float().square().mean(), leaves)
+    ref = r.backward((2 * y.detach().float() / y.numel()).bfloat16())
+    assert torch.equal(again[0], ref["dx"]) and torch.equal(again[1], ref["dw_r"].bfloat16())
+    assert not torch.equal(both[1], again[1])
+    # in the order y, aux loss, choice; and y alone as before
+    out = moe_layer(x, *w, K, aux_alpha=0.01, return_topk=True)
+    assert len(out) == 3 and torch.equal(out[0], y.detach()) and torch.equal(out[2], kept)
+    assert torch.equal(moe_layer(x, *w, K), y.detach())
