@@ -11,7 +11,7 @@
 A trained layer's weights are quantised once and serve both:
 
     w = [MoEMx4Tensor.weights(t) for t in (w_gate, w_up, w_down)]
-    y = MoEMx4Runner(N, H, F, E, K, dtype).forward(x, w_r, *w)
+    y = MoEMx4Runner(N, H, F, E, K, dtype).forward(x, w_r, *w)   # shared=: a shared expert's, in both
     y = MoEMx4DecodeRunner(16, H, F, E, K, dtype).forward(x, w_r, *w)
 """
 from __future__ import annotations
@@ -98,6 +98,12 @@ def _expect_mx4(name: str, q, order: int, shape, dev):
     return q.mx4
 
 
+def _shared_weights(shared, H: int, Fs: int, dev):
+    return [_expect_mx4(name, q, L.MOE_MX4_WEIGHTS, shape, dev)
+            for name, q, shape in zip(("shared w_gate", "shared w_up", "shared w_down"), shared,
+                                      ((1, H, Fs), (1, H, Fs), (1, Fs, H)))]
+
+
 class MoEMx4DecodeRunner:
     """The layer's forward for the few tokens of a decoding step with experts in
     4 bits: MoEDecodeRunner with MoEMx4Tensor weights.  Outputs are the runner's
@@ -146,10 +152,7 @@ class MoEMx4DecodeRunner:
              _expect_mx4("w_down", w_down, L.MOE_MX4_WEIGHTS, (E, F, H), dev))
         s = (None, None, None)
         if shared is not None:
-            Fs = self.shared_ffn
-            s = [_expect_mx4(name, q, L.MOE_MX4_WEIGHTS, shape, dev)
-                 for name, q, shape in zip(("shared w_gate", "shared w_up", "shared w_down"), shared,
-                                           ((1, H, Fs), (1, H, Fs), (1, Fs, H)))]
+            s = _shared_weights(shared, H, self.shared_ffn, dev)
         d, ds = self._dims[n]
         if n:
             with _on(dev):
@@ -166,8 +169,10 @@ class MoEMx4Runner:
     MoELayerRunner.  Outputs are the runner's own buffers; one call at a time."""
 
     def __init__(self, N: int, H: int, F: int, E: int, K: int, dtype: torch.dtype, device="cuda",
-                 capacity: Optional[int] = None):
-        """capacity: rows per expert, the overflow dropped; None is the dropless layer."""
+                 capacity: Optional[int] = None, shared_ffn: Optional[int] = None):
+        """capacity: rows per expert, the overflow dropped; None is the dropless layer.
+        shared_ffn: intermediate size of a shared expert that every token passes through
+        (weights passed to forward as ``shared``); None: no shared expert."""
         self.N, self.H, self.F, self.E, self.K, self.dtype, self.capacity = N, H, F, E, K, dtype, capacity
         if capacity is not None and capacity < 0:
             raise ValueError("capacity must not be negative")
@@ -196,6 +201,19 @@ class MoEMx4Runner:
         self.act = make((NK, F), dtype=dtype, device=dev)
         self.ys = make((NK, H), dtype=dtype, device=dev)
         self.y = torch.empty((N, H), dtype=dtype, device=dev)
+        self.shared_ffn = shared_ffn
+        if shared_ffn is not None:
+            # one expert that every token has chosen: all rows, in their order
+            self.ds = L.dims(N, H, shared_ffn, 1, 1, L.dtype_code(dtype))
+            if L.moe_max_tiles(self.ds) < 0:
+                raise L.MoEError("moe_max_tiles", L.MOE_EINVAL)
+            self.rows_s = torch.arange(max(1, N), dtype=i32, device=dev)
+            first = self.rows_s[::L.MOE_TILE_M]
+            self.tiles_s = torch.stack([torch.zeros_like(first), first, (N - first).clamp(max=L.MOE_TILE_M)], 1)
+            self.num_tiles_s = torch.full((1,), first.numel(), dtype=i32, device=dev)
+            self.aq_s = MoEMx4Tensor(L.MOE_MX4_ROWS, (N, shared_ffn), dev)
+            self.act_s = torch.empty((N, shared_ffn), dtype=dtype, device=dev)
+            self.ys_s = torch.empty((N, H), dtype=dtype, device=dev)
         self._made = _Made(dev)
 
     def meta(self, topk, stream=None):
@@ -237,16 +255,21 @@ class MoEMx4Runner:
                 L.moe_mx4_down(self.d, a, w, self.tiles, self.num_tiles, self.ys, self._made.before(dev, stream))
         return self.ys
 
-    def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None):
+    def forward(self, x, w_r, w_gate, w_up, w_down, bias=None, stream=None, shared=None):
         """Returns y [N, H] of x [N, H]; topk and gates are attributes.  w_gate, w_up
-        [E,H,F] and w_down [E,F,H]: MoEMx4Tensor weights."""
+        [E,H,F] and w_down [E,F,H]: MoEMx4Tensor weights.  ``shared`` as in
+        MoEMx4DecodeRunner.forward."""
         E, H, F, dev = self.E, self.H, self.F, self.device
+        if (shared is None) != (self.shared_ffn is None):
+            raise ValueError("shared weights must be given exactly when the runner has a shared expert")
         _expect("x", x, (self.N, H), self.dtype, dev)
         _expect("w_r", w_r, (H, E), self.dtype, dev)
         if bias is not None:
             _expect("bias", bias, (E,), torch.float32, dev)
         for name, q, shape in (("w_gate", w_gate, (E, H, F)), ("w_up", w_up, (E, H, F)), ("w_down", w_down, (E, F, H))):
             _expect_mx4(name, q, L.MOE_MX4_WEIGHTS, shape, dev)
+        if shared is not None:
+            s = _shared_weights(shared, H, self.shared_ffn, dev)
         if self.N == 0:
             return self.y
         cap = 2 ** 31 - 1 if self.capacity is None else self.capacity
@@ -258,5 +281,12 @@ class MoEMx4Runner:
         act = self.gate_up(self.xq.quantize(x, stream), w_gate, w_up, stream)
         self.down(self.aq.quantize(act, stream), w_down, stream)
         with _on(dev):
-            L.moe_combine(self.d, self.ys, self.gates, self.inv, self.y, stream)
+            if shared is None:
+                L.moe_combine(self.d, self.ys, self.gates, self.inv, self.y, stream)
+                return self.y
+            L.moe_mx4_gate_up(self.ds, self.xq.mx4, self.rows_s, s[0], s[1], self.tiles_s, self.num_tiles_s, self.act_s,
+                              stream)
+            self.aq_s.quantize(self.act_s, stream)
+            L.moe_mx4_down(self.ds, self.aq_s.mx4, s[2], self.tiles_s, self.num_tiles_s, self.ys_s, stream)
+            L.moe_combine_shared(self.d, self.ys, self.gates, self.inv, self.ys_s, self.y, stream)
         return self.y

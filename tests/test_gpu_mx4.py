@@ -676,3 +676,77 @@ def test_runners_of_another_stream():
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(many.y, want[0]) and torch.equal(few.y, want[1]) and torch.equal(many.act, want[2])
+
+
+def prompt_check(r, y, t, wv, N, K, s, shared=None):
+    """y of MoEMx4Runner.forward against float64, step by step on the values that each product had (its quantised
+    activations, as the runner holds them); rows that a capacity dropped count nothing."""
+    F, H = wv[2].shape[1:]
+    xv, av = quantised(t["x"])[0], quantised(r.act)[0]
+    ref, tol = torch.zeros((N, H), dtype=torch.float64, device="cuda"), torch.zeros((N, H), dtype=torch.float64, device="cuda")
+    for e in range(wv[0].shape[0]):
+        lo, hi = int(r.offsets[e]), int(r.offsets[e + 1])
+        f = r.sorted_flat[lo:hi].long()
+        A, eA = ffn_parts(xv[f // K], wv[0][e], wv[1][e])
+        assert bool(((r.act[lo:hi].double() - A).abs() <= s * A.abs() + 1.01 * eA).all()), e
+        o = av[lo:hi] @ wv[2][e]
+        eo = (F + 8) * U * (av[lo:hi].abs() @ wv[2][e].abs()) + s * o.abs()
+        g = r.gates.reshape(-1)[f].double()[:, None]
+        ref.index_add_(0, f // K, g * o)
+        tol.index_add_(0, f // K, g * (eo + 8 * U * o.abs()))
+    if shared is not None:
+        A, eA = ffn_parts(xv, shared[0][0], shared[1][0])
+        assert bool(((r.act_s.double() - A).abs() <= s * A.abs() + 1.01 * eA).all())
+        a, Fs = quantised(r.act_s)[0], shared[2].shape[1]
+        o = a @ shared[2][0]
+        ref += o
+        tol += (Fs + 8) * U * (a.abs() @ shared[2][0].abs()) + s * o.abs() + 8 * U * o.abs()
+    err, lim = (y.double() - ref).abs(), s * ref.abs() + 1.01 * tol
+    assert bool((err <= lim).all()), float((err / lim).max())
+
+
+# N, H, F, E, K, Fs, capacity, bias
+PROMPTS = [(1, 128, 128, 1, 1, 0, None, False), (333, 256, 512, 6, 2, 0, None, True), (333, 256, 512, 6, 2, 384, None, True),
+           (256, 128, 256, 3, 1, 128, None, False), (257, 384, 640, 5, 3, 1408, None, False),
+           (700, 640, 384, 4, 2, 0, 100, False), (700, 256, 1408, 8, 2, 640, 60, True), (90, 128, 128, 4, 2, 0, 0, False),
+           (90, 128, 128, 4, 2, 256, 0, False), (1500, 512, 256, 64, 8, 256, None, True)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,H,F,E,K,Fs,capacity,bias", PROMPTS)
+def test_prompt(dtype, N, H, F, E, K, Fs, capacity, bias):
+    from mixture_experts_layer_sort_amd import MoEMx4DecodeRunner, MoEMx4Runner, MoEMx4Tensor as Q
+    s = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    t, w, sh = layer_inputs(N, H, F, E, dtype, Fs, bias)
+    r = MoEMx4Runner(N, H, F, E, K, dtype, capacity=capacity, shared_ffn=Fs or None)
+    q = [Q.weights(v) for v in w]
+    qs = tuple(Q.weights(v) for v in sh) if sh else None
+    y = r.forward(t["x"], t["w_r"], *q, bias=t["bias"], shared=qs).clone()
+    kept = int(r.offsets[-1])
+    assert kept == N * K if capacity is None else kept <= min(N * K, E * capacity)
+    prompt_check(r, y, t, [quantised(v)[0] for v in w], N, K, s, [quantised(v)[0] for v in sh] if sh else None)
+    # the same bits again, with NaN in the rows that were dropped
+    r.act[kept:] = float("nan")
+    r.ys[kept:] = float("nan")
+    r.y.zero_()
+    assert torch.equal(r.forward(t["x"], t["w_r"], *q, bias=t["bias"], shared=qs), y)
+    few = MoEMx4DecodeRunner(1, H, F, E, K, dtype, shared_ffn=Fs or None)
+    few.forward(t["x"][:1].contiguous(), t["w_r"], *q, bias=t["bias"], shared=qs)
+    assert torch.equal(few.topk, r.topk[:1])
+
+
+def test_prompt_refuses_shared_weights_that_do_not_fit():
+    from mixture_experts_layer_sort_amd import MoEError, MoEMx4Runner, MoEMx4Tensor as Q
+    N, H, F, E, K = 20, 128, 256, 4, 2
+    t, w, sh = layer_inputs(N, H, F, E, torch.bfloat16, 384)
+    q, qs = [Q.weights(v) for v in w], tuple(Q.weights(v) for v in sh)
+    r, plain = (MoEMx4Runner(N, H, F, E, K, torch.bfloat16, shared_ffn=Fs) for Fs in (384, None))
+    y = r.forward(t["x"], t["w_r"], *q, shared=qs).clone()
+    for run, bad in ((r, None), (plain, qs), (r, (qs[0], qs[1], qs[0])), (r, (q[0], q[1], q[2])), (r, sh)):
+        with pytest.raises(ValueError):
+            run.forward(t["x"], t["w_r"], *q, shared=bad)
+    assert torch.equal(r.y, y)
+    with pytest.raises(MoEError):
+        MoEMx4Runner(N, H, F, E, K, torch.bfloat16, shared_ffn=100)
+    none = MoEMx4Runner(0, H, F, E, K, torch.bfloat16, shared_ffn=384)
+    assert none.forward(t["x"][:0], t["w_r"], *q, shared=qs).shape == (0, H)
