@@ -750,3 +750,37 @@ def test_prompt_refuses_shared_weights_that_do_not_fit():
         MoEMx4Runner(N, H, F, E, K, torch.bfloat16, shared_ffn=100)
     none = MoEMx4Runner(0, H, F, E, K, torch.bfloat16, shared_ffn=384)
     assert none.forward(t["x"][:0], t["w_r"], *q, shared=qs).shape == (0, H)
+
+
+# N, H, F, E, K, Fs, the expert that all tokens choose: strips of a piece 1, 2, 4 of gate/up and 1, 2, 4, 8 of down,
+# for kernels of one, two and four row tiles (N up to 16; experts of up to 24 rows on average; more, or a shared expert)
+PIECES = [(9, 1024, 128, 64, 8, 0, None), (16, 1024, 512, 16, 4, 256, None), (16, 1024, 1024, 24, 4, 0, None),
+          (20, 1024, 640, 16, 2, 0, None), (30, 1024, 1152, 20, 2, 0, None), (48, 2048, 256, 24, 2, 0, None),
+          (41, 512, 384, 16, 2, 0, 3), (64, 512, 384, 16, 2, 0, 15), (64, 1024, 1152, 20, 2, 0, 0),
+          (33, 512, 384, 32, 2, 256, None), (64, 1024, 1024, 20, 3, 128, 7), (64, 2048, 128, 24, 2, 128, None),
+          (40, 2048, 768, 24, 4, 256, None), (64, 1024, 2304, 8, 4, 0, None), (17, 256, 1152, 16, 8, 1152, 2)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,H,F,E,K,Fs,all_to", PIECES)
+def test_decode_pieces(dtype, N, H, F, E, K, Fs, all_to):
+    """As test_decode, over the ways in which the work is cut; rows of an expert in two turns of 32 too."""
+    from mixture_experts_layer_sort_amd import MoEMx4DecodeRunner, MoEMx4Tensor as Q
+    s = 2.0 ** -8 if dtype == torch.bfloat16 else U
+    t, w, sh = layer_inputs(N, H, F, E, dtype, Fs, all_to is not None, seed=N + E)
+    if all_to is not None:
+        t["bias"][all_to] += 3.0
+    r = MoEMx4DecodeRunner(N, H, F, E, K, dtype, shared_ffn=Fs or None)
+    q = [Q.weights(v) for v in w]
+    qs = tuple(Q.weights(v) for v in sh) if sh else None
+    y = r.forward(t["x"], t["w_r"], *q, bias=t["bias"], shared=qs).clone()
+    ids, gates, ge, ref, e = layer_reference(t, [quantised(v)[0] for v in w], K, 0.0, s,
+                                             [quantised(v)[0] for v in sh] if sh else None)
+    assert torch.equal(r.topk.long(), ids)
+    if all_to is not None:
+        assert int((ids == all_to).sum()) > (32 if N > 32 else 16)
+    assert bool(((r.gates.double() - gates).abs() <= ge * gates).all())
+    err, tol = (y.double() - ref).abs(), s * ref.abs() + 1.01 * e
+    assert bool((err <= tol).all()), float((err / tol).max())
+    r.y.zero_()
+    assert torch.equal(r.forward(t["x"], t["w_r"], *q, bias=t["bias"], shared=qs), y)  # bit for bit
