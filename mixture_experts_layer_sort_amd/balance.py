@@ -50,7 +50,7 @@ def _mask(mask, N, dev):
 
 
 class MoEBalanceRunner:
-    """The loss of up to N tokens' logits, in buffers of its own: loss [1], counts [E]
+    """The loss of N tokens' logits, in buffers of its own: loss [1], counts [E]
     int32 and dlogits.  One call at a time."""
 
     def __init__(self, N: int, E: int, K: int, dtype: torch.dtype, device="cuda", seq_len: Optional[int] = None,

@@ -238,7 +238,7 @@ hipError_t mx4_quantize(bool rows, int64_t count, int64_t k, int64_t cols, int d
                         void* scales, hipStream_t s);
 hipError_t mx4_dequantize(bool rows, int64_t count, int64_t k, int64_t cols, int dtype, const Mx4& q, void* v,
                           hipStream_t s);
-// Grouped products of 4-bit rows; wu null: the plain product (down).
+// Grouped products of 4-bit rows.
 hipError_t mx4_gate_up(const Dims& d, const Mx4& x, const int32_t* sorted_flat, const Mx4& wg, const Mx4& wu,
                        const int32_t* tiles, const int32_t* num_tiles, void* act, hipStream_t s);
 hipError_t mx4_down(const Dims& d, const Mx4& act, const Mx4& wd, const int32_t* tiles, const int32_t* num_tiles,

@@ -1,6 +1,5 @@
 // What the layer for few tokens does whatever the form of its experts' weights:
-// router logits in float64, top-K and gates, the chosen experts and the rows of
-// one of them, the sum of a token's rows.
+// router logits in float64, top-K and gates, the sum of a token's rows.
 #pragma once
 
 #include "common.h"
@@ -53,17 +52,6 @@ __device__ __forceinline__ void park_logits(const f64x4_t& acc, double* red) {
 #pragma unroll
   for (int r = 0; r < 4; ++r) red[(4 * r + lane_id() / 16) * 16 + lane_id() % 16] = acc[r];
 }
-
-// x as xp [H/32][N][32], so that the row operand of a panel is one contiguous piece:
-// the 8 elements at `from`, those of token n from h on.
-template <typename T> struct PackPanels {
-  T* xp;
-  __device__ __forceinline__ void operator()(const T* from, int n, int h, int N, int) const {
-    uint4* to = reinterpret_cast<uint4*>(xp + (int64_t(h / 32) * N + n) * 32 + h % 32);
-#pragma unroll
-    for (int j = 0; j < 8 * int(sizeof(T)) / 16; ++j) to[j] = reinterpret_cast<const uint4*>(from)[j];
-  }
-};
 
 // Partial logits part[s][n][e] over rows s*512 .. of W_r for 16 experts and 16
 // tokens.  A wave has 32 rows; the waves' sums meet in LDS in wave order.  The
@@ -211,93 +199,6 @@ __device__ __forceinline__ void route_here(const Route<T>& r, int N, int H, int 
   }
   rank_pairs(v, r.bias, N, E, K, out);
   __syncthreads();
-}
-
-// ------------------------------------------------------- rows of an expert
-
-// The chosen experts, ascending, and the slots' experts, in LDS.  Workgroups are
-// numbered over the chosen experts only: they go to the XCDs in turn by their
-// number, so numbers that had nothing to do would leave some XCDs with more
-// weights to read than others.
-struct Chosen {
-  int ids[kSlots];
-  int expert[MOE_MAX_EXPERTS];
-  int counts[2 * kSlots / kWave];
-};
-
-// Builds it; returns the number of chosen experts.  All threads call it.
-__device__ __forceinline__ int chosen_experts(const int32_t* __restrict__ topk, int NK, Chosen* c) {
-  static_assert(kNT == MOE_MAX_EXPERTS, "a thread per expert");
-  const int t = threadIdx.x;
-  c->expert[t] = 0;
-  __syncthreads();
-  for (int i = t; i < NK; i += kNT) {
-    const int e = topk[i];
-    c->ids[i] = e;
-    c->expert[e] = 1;
-  }
-  __syncthreads();
-  const bool mine = c->expert[t] != 0;
-  const uint64_t mask = __ballot(mine);
-  if (lane_id() == 0) c->counts[t / kWave] = __popcll(mask);
-  __syncthreads();
-  int active = 0, at = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w == t / kWave) at = active + __popcll(mask & ((uint64_t(1) << lane_id()) - 1));
-    active += c->counts[w];
-  }
-  if (mine) c->expert[at] = t;  // every thread has read its own flag
-  __syncthreads();
-  return active;
-}
-
-// Slots n*K + k of expert e in ascending order to rows[0, count); the count.
-// All threads of the workgroup call it.
-__device__ __forceinline__ int expert_slots(Chosen* c, int NK, int e, int* rows) {
-  constexpr int R = kSlots / kNT;
-  const int w = threadIdx.x / kWave;
-  bool mine[R];
-  uint64_t mask[R];
-  __syncthreads();  // rows and counts are free
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int t = r * kNT + threadIdx.x;
-    mine[r] = t < NK && c->ids[t] == e;
-    mask[r] = __ballot(mine[r]);
-    if (lane_id() == 0) c->counts[r * kWaves + w] = __popcll(mask[r]);
-  }
-  __syncthreads();
-  int count = 0;
-#pragma unroll
-  for (int i = 0; i < R * kWaves; ++i) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i == r * kWaves + w && mine[r]) {
-        // one token names an expert once, so there are at most N <= kTok slots
-        const int at = count + __popcll(mask[r] & ((uint64_t(1) << lane_id()) - 1));
-        if (at < kTok) rows[at] = r * kNT + threadIdx.x;
-      }
-    count += c->counts[i];
-  }
-  __syncthreads();
-  return min(count, kTok);
-}
-
-// The rows of unit u: the u-th chosen expert's slots; their number, 0 when there
-// is no such unit.  One token's experts are its slots as they stand.
-__device__ __forceinline__ int unit_rows(const int32_t* __restrict__ topk, int N, int K, int u, Chosen* c, int* e,
-                                         int* rows) {
-  if (N == 1) {
-    if (u >= K) return 0;
-    *e = topk[u];
-    if (threadIdx.x == 0) rows[0] = u;
-    __syncthreads();
-    return 1;
-  }
-  if (u >= chosen_experts(topk, N * K, c)) return 0;
-  *e = c->expert[u];
-  return expert_slots(c, N * K, *e, rows);
 }
 
 // ---------------------------------------------------------------- combine

@@ -260,7 +260,6 @@ constexpr int kUnroll = NS >= 8 ? (MT * P > 3 ? 1 : 2) : NS == 4 && MT > 2 ? 2 :
 // unit u's slots are slots[start[u] .. start[u+1]).  A workgroup builds it once for
 // all its work.
 struct Units {
-  int ids[kSlots];
   int16_t slots[kSlots];
   int count[MOE_MAX_EXPERTS], first[MOE_MAX_EXPERTS];
   int expert[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS + 1];

@@ -758,7 +758,8 @@ PIECES = [(9, 1024, 128, 64, 8, 0, None), (16, 1024, 512, 16, 4, 256, None), (16
           (20, 1024, 640, 16, 2, 0, None), (30, 1024, 1152, 20, 2, 0, None), (48, 2048, 256, 24, 2, 0, None),
           (41, 512, 384, 16, 2, 0, 3), (64, 512, 384, 16, 2, 0, 15), (64, 1024, 1152, 20, 2, 0, 0),
           (33, 512, 384, 32, 2, 256, None), (64, 1024, 1024, 20, 3, 128, 7), (64, 2048, 128, 24, 2, 128, None),
-          (40, 2048, 768, 24, 4, 256, None), (64, 1024, 2304, 8, 4, 0, None), (17, 256, 1152, 16, 8, 1152, 2)]
+          (40, 2048, 768, 24, 4, 256, None), (64, 1024, 2304, 8, 4, 0, None), (17, 256, 1152, 16, 8, 1152, 2),
+          (10, 512, 1152, 24, 4, 0, None), (16, 512, 640, 20, 4, 0, None)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
