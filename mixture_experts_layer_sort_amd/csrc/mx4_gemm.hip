@@ -328,13 +328,19 @@ hipError_t product(const moe_launch::Dims& d, const Rows& x, const moe_launch::M
   constexpr int bytes = 3 * kStageBytes, BN = (GATE_UP ? 1 : 2) * 32 * kGWaves;
   const hipError_t e = allow_lds<k_mx4_product<T, GATE_UP>>(bytes);
   if (e != hipSuccess) return e;
-  const int64_t pieces = moe_launch::max_tiles(d) * (MOE_TILE_M / kRows) * ((C + BN - 1) / BN);
+  const int64_t ncols = (C + BN - 1) / BN, pieces = moe_launch::max_tiles(d) * (MOE_TILE_M / kRows) * ncols;
   if (pieces > (int64_t(1) << 31) - 512) return hipErrorInvalidValue;
   // With few rows an expert most list tiles have no second 128 rows: those workgroups, which end at once, hold
-  // up the ones behind them, so they come last.  With more, both read the expert's weights, side by side.
-  // Gate/up of 8 experts, H 4096, F 14336: 32 rows each 94 us with them last, 113 otherwise; 96 118 and 136;
-  // 128 164 and 142; down of 64 experts, H 2048, F 1408: 32 rows 21 and 27, 96 33 and 36, 128 39 and 42.
-  const bool seconds_last = d.NK() <= 96 * d.E;
+  // up the ones behind them, so they come last.  Not where the first halves are half a window of
+  // xcd_window_block or less: they would all lie on half of the XCDs.  And not with more rows, where both halves
+  // read the expert's weights, side by side.  Times with them last and otherwise:
+  //   gate/up of 64 experts, H 2048, F 1408 (704 first halves): 32 rows 42 and 55 us, 96 46 and 66, 128 70 and 70,
+  //     144 81 and 67; of 8, H 4096, F 14336 (896): 101 and 125, 106 and 134, 158 and 145, 183 and 146;
+  //   down of the same 64 experts (512): 23 and 31, 29 and 40, 41 and 43, 46 and 45; of the 8 (128): 70 and 60, 81
+  //     and 70, 85 and 72, 88 and 74;
+  //   contraction 8192, 80 rows, gate/up and down with 64 first halves 36 and 30, 42 and 40; 128: 44 and 31, 48 and
+  //     43; 192: 45 and 52, 51 and 76; 256: 51 and 74, 60 and 81.
+  const bool seconds_last = d.NK() <= 96 * d.E && std::min(d.NK(), d.E) * ncols > 128;
   const unsigned grid = unsigned((pieces + 255) / 256 * 256);
   k_mx4_product<T, GATE_UP><<<dim3(grid), dim3(kGNT), bytes, s>>>(
       x, static_cast<const char*>(w0.codes), static_cast<const char*>(w0.scales),
