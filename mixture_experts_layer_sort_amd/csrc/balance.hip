@@ -96,14 +96,14 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 }
 
 // exp(x) for x <= 0 (0 below 2^-126): the hardware's 2^h of h = x / ln 2, rounded, and the
-// first order of what the rounding (at most 2^-17) and the constant's leave out: about an
-// ulp of the hardware's, where 2^h alone is off by |x| 2^-24 of itself.
+// first order of x - h ln 2, which the rounding leaves (2^-16 at most): about an ulp of the
+// hardware's, where 2^h alone is off by |x| 2^-24 of itself.
 __device__ __forceinline__ float exp_below(float x) {
-  constexpr double kLog2E = 1.4426950408889634074;
-  constexpr float kHigh = float(kLog2E), kLow = float(kLog2E - double(kHigh));
-  x = x < -200.f ? -200.f : x;  // NaN stays
-  const float h = x * kHigh, r = __builtin_amdgcn_exp2f(h);
-  return fmaf(r, fmaf(x, kLow, fmaf(x, kHigh, -h)) * float(1.0 / kLog2E), r);
+  constexpr double kLn2 = 0.69314718055994530942;
+  constexpr float kHigh = float(kLn2), kLow = float(kLn2 - double(kHigh));
+  const float h = x * float(1.0 / kLn2), r = __builtin_amdgcn_exp2f(h);
+  const float d = fmaf(-h, kLow, fmaf(-h, kHigh, x));
+  return fmaf(r, __builtin_amdgcn_fmed3f(d, -0x1p-15f, 0x1p-15f), r);  // d of -inf is NaN, r 0
 }
 // 1 / a for a from 1 to 2: the hardware's, which is off by an ulp, and a Newton step.
 __device__ __forceinline__ float inverse(float a) {
