@@ -477,3 +477,44 @@ def test_the_layers_own_choice_in_bf16():
     out = moe_layer(x, *w, K, aux_alpha=0.01, return_topk=True)
     assert len(out) == 3 and torch.equal(out[0], y.detach()) and torch.equal(out[2], kept)
     assert torch.equal(moe_layer(x, *w, K), y.detach())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("B,T", [(2, 1), (64, 1), (40, 2), (900, 1), (7, 17)])
+def test_short_sequences_of_padding(B, T, score):
+    """Sequences that are nothing but padding, one token long too, among others: they count neither as sequences nor
+    as tokens."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    E, K = 24, 3
+    l = logits_of(B * T, E, torch.float32, seed=B)
+    ends = torch.arange(B, device="cuda") * 5 % (T + 1)
+    ends[0] = T
+    mask = (torch.arange(T, device="cuda") < ends[:, None])
+    assert B < 3 or bool((ends < T).any())
+    l[~mask.reshape(-1)] = float("nan")
+    r = MoEBalanceRunner(B * T, E, K, torch.float32, seq_len=T, alpha=0.3, z_coef=0.01, score=score)
+    loss = r.forward(l, mask=mask)
+    check(torch.where(mask.reshape(-1, 1), l, torch.zeros_like(l)), K, T, 0.3, 0.01, score, mask=mask, loss=loss,
+          counts=r.counts, d=r.backward())
+
+
+def test_runner_made_on_a_side_stream():
+    """Made on a side stream, called on the default one, by its raw handle too; first called in a capture."""
+    from mixture_experts_layer_sort_amd import MoEBalanceRunner
+    l = logits_of(500, 40, torch.float32)
+    want = MoEBalanceRunner(500, 40, 2, torch.float32).forward(l).clone()
+    side = torch.cuda.Stream()
+    for stream in (None, torch.cuda.current_stream().cuda_stream, torch.cuda.current_stream()):
+        with torch.cuda.stream(side):
+            r = MoEBalanceRunner(500, 40, 2, torch.float32)
+        assert torch.equal(r.forward(l, stream=stream), want)
+    r, g = MoEBalanceRunner(500, 40, 2, torch.float32), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r.forward(l)
+    for _ in range(3):
+        r.loss.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r.loss, want)
+    r.loss.zero_()
+    assert torch.equal(r.forward(l), want)

@@ -785,3 +785,32 @@ def test_decode_pieces(dtype, N, H, F, E, K, Fs, all_to):
     assert bool((err <= tol).all()), float((err / tol).max())
     r.y.zero_()
     assert torch.equal(r.forward(t["x"], t["w_r"], *q, bias=t["bias"], shared=qs), y)  # bit for bit
+
+
+def test_prompt_with_a_shared_expert_on_another_stream_and_captured():
+    """A runner whose first call is on a side stream, and one whose first call is captured: the same bits; products
+    behind the capture alone, before any replay, have no tiles and write nothing."""
+    from mixture_experts_layer_sort_amd import MoEMx4Runner, MoEMx4Tensor as Q
+    N, H, F, E, K = 300, 256, 384, 6, 2
+    t, w, sh = layer_inputs(N, H, F, E, torch.bfloat16, 256)
+    q, qs = [Q.weights(v) for v in w], tuple(Q.weights(v) for v in sh)
+    make = lambda: MoEMx4Runner(N, H, F, E, K, torch.bfloat16, shared_ffn=256)  # noqa: E731
+    r = make()
+    want, xq = r.forward(t["x"], t["w_r"], *q, shared=qs).clone(), Q.rows(t["x"])
+    side, r = torch.cuda.Stream(), make()
+    side.wait_stream(torch.cuda.current_stream())
+    r.forward(t["x"], t["w_r"], *q, shared=qs, stream=side)
+    side.synchronize()
+    assert torch.equal(r.y, want)
+    r, g = make(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r.forward(t["x"], t["w_r"], *q, shared=qs)
+    r.act.fill_(7.0)
+    assert bool((r.gate_up(xq, q[0], q[1]) == 7.0).all())
+    for _ in range(3):
+        r.y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r.y, want)
+    r.y.zero_()
+    assert torch.equal(r.forward(t["x"], t["w_r"], *q, shared=qs), want)
