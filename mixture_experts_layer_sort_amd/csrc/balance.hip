@@ -24,7 +24,10 @@ using namespace moe;
 constexpr int kLanes = 16;       // of a token
 constexpr int kRows = 256 / kLanes;  // tokens a workgroup has under way
 constexpr int kOneRows = 1024 / kLanes;  // where one workgroup does all
-constexpr int64_t kMostChunks = 768;  // three workgroups a CU: what the registers allow
+// Three workgroups a CU, what the registers of 256 experts allow. Kernels of fewer experts could have more, but
+// the next launch reads each chunk's sums: 131072 tokens of 64 experts as one sequence take 61 us with 768 chunks,
+// 69 with 1280, 86 with 2048; as 32 sequences 51, 50 and 48.
+constexpr int64_t kMostChunks = 768;
 
 // Over the sixteen lanes of a token, all of them getting the result: each step
 // takes the value of a lane with the lowest 1, 2, 3, 4 bits of its number mirrored.
@@ -206,8 +209,8 @@ __device__ __forceinline__ float kth_value(const float (&f)[NV], int K) {
 // The K experts of largest value l + b, each counted by the lane that holds it.  Only
 // the set matters: a value that exactly K reach tells it.  RARE: equals are rare
 // (float32 logits), so such a value is first looked for among the largest few of each
-// lane: the loss of 131072 tokens, 8 of 256 sigmoid experts, takes 62 us so and 83
-// without; bfloat16 logits, whose equals spoil it for most waves, 107 and 91.
+// lane: the loss of 131072 tokens, 8 of 256 sigmoid experts, takes 76 us so and 98
+// without; bfloat16 logits, whose equals spoil it for most waves, 115 and 97.
 // Otherwise the K-th largest is found by going down from one value to the next;
 // everything above it is chosen, and of its equals the first ones by their expert.
 template <int NV, bool VEC, bool RARE>
@@ -601,9 +604,10 @@ __global__ __launch_bounds__(256) void k_balance_bwd(const T* logits, const uint
 }
 
 // Tokens of a chunk, a whole number of a workgroup's turns: one for each CU, then up to four
-// turns, then kMostChunks chunks.  The next launch reads each chunk's sums (4 sequences of 4096
-// tokens, 64 experts: chunks of one turn take 4.5 us and the next launch 10.9, of four turns 5.9
-// and 6.2; 203 tokens of 8 experts: 3.3 and 3.7, 4.5 and 3.7).
+// turns, then about kMostChunks chunks (and at least one a sequence).  The next launch reads each
+// chunk's sums (16384 tokens of 64 experts as one sequence: chunks of one turn take 6.1 us and the
+// next launch 15.7, of four turns 7.8 and 10.1; as four sequences, choice given, 4.4 and 7.7, 5.6
+// and 6.4).
 int64_t chunk_of(const moe_balance& b) {
   const int64_t per = std::max(std::min<int64_t>(4 * kRows, b.N / 256), (b.N + kMostChunks - 1) / kMostChunks);
   return std::min<int64_t>((per + kRows - 1) / kRows * kRows, (b.seq_len + kRows - 1) / kRows * kRows);
@@ -611,8 +615,8 @@ int64_t chunk_of(const moe_balance& b) {
 int64_t chunks_of(const moe_balance& b) { return (b.seq_len + chunk_of(b) - 1) / chunk_of(b); }
 
 // Few tokens of one sequence, at most 64 experts: all in one workgroup, without the launch that adds
-// chunks up.  203 tokens of 8 experts: 5.8 us, 6.6 in two launches, and the call takes the host 2 us less;
-// 256: 6.6 and 6.6; 128 tokens of 64 experts: 6.8 and 7.0, 203: 9.1 and 7.3.
+// chunks up.  203 tokens of 8 experts: 6.2 us, 7.0 in two launches, and the call takes the host 2 us less;
+// 256: 7.2 and 7.0; 128 tokens of 64 experts: 7.2 and 7.7, 203: 9.8 and 8.4.
 bool in_one(const moe_balance& b) {
   return b.N == b.seq_len && b.N <= (b.E <= 16 ? 4 : 2) * kOneRows && b.E <= kWave;
 }

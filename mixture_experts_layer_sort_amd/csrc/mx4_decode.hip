@@ -501,8 +501,8 @@ struct Plan {
 
 // Strips of a piece, of `strips` in all: the rows are read again for each piece, so as many as
 // leave every CU one (8 strips of both kinds of product at most: their sums take the registers).
-// 64 tokens of 8 experts, H 4096, F 14336: gate/up 98 us with four strips of both matrices, 114 with
-// two, 160 with one; down (whole contractions) 83 with eight, 85 with four, 127 with two.
+// 64 tokens of 8 experts, H 4096, F 14336: gate/up 101 us with four strips of both matrices, 120 with
+// two, 167 with one; down (whole contractions) 106 with eight, 115 with four, 181 with two.
 int strips_of(int64_t strips, int most) {
   int cg = most;
   while (cg > 1 && strips / cg < kCUs) cg /= 2;
@@ -524,7 +524,7 @@ Plan plan(const moe_launch::Dims& d, int64_t Fs) {
   p.dn_cg = strips_of(strips, 8);
   // Where that leaves a CU few pieces, each takes a part of the contraction, 16 tiles or more: pieces of
   // experts with more rows take longer.  The parts' sums meet in the kernel that adds a token's.
-  // 64 tokens of 8 experts, H 4096, F 14336: down and that kernel 79 us with four parts, 90 with one.
+  // 64 tokens of 8 experts, H 4096, F 14336: down and that kernel 94 us with four parts, 111 with one.
   p.q.parts = d.N == 1 ? 1 : int(std::max<int64_t>(1, std::min<int64_t>(d.F / kMxTile / 16, 4 * kCUs * p.dn_cg / strips)));
   p.row_tiles = d.N <= 16 ? 1 : std::max(rows, Fs > 0 ? double(d.N) : 0.0) > 24.0 ? 4 : 2;
   size_t at = 0;
@@ -561,8 +561,8 @@ template <typename T> struct Args {
 
 // Workgroups for `pieces` pieces at most.  Finding the units takes a workgroup about 3 us,
 // so it does it for several pieces; two to three fit a CU, the others follow them where
-// pieces run unevenly (32 tokens of 256 experts, gate/up: 447 us with two a CU in all, 424
-// with eight; 13 of 64, down: 27.8 with two, 23.3 with four).
+// pieces run unevenly (32 tokens of 256 experts, gate/up: 428 us with two a CU in all, 424
+// with four, 421 with eight; 13 of 64, down: 29.7, 27.6 and 28.1).
 dim3 grid_of(int64_t pieces) { return dim3(unsigned(std::min(pieces, 4 * kCUs))); }
 
 template <typename T, int MTMAX, int CG>
