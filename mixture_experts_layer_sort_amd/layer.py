@@ -389,24 +389,23 @@ def _stream_of(dev: torch.device, stream):
 
 class _Made:
     """The stream on which buffers were made.  The allocator hands out memory that work queued there
-    may still use, and first values are written there, so a first call on another stream waits for it.
+    may still use, and first values are written there, so the first call on another stream waits for it.
     Later calls come in the caller's order, as they share the buffers."""
 
     def __init__(self, dev: torch.device):
         self.stream = torch.cuda.current_stream(dev) if dev.type == "cuda" else None
+        self.raw = None if self.stream is None else self.stream.cuda_stream
 
     def before(self, dev: torch.device, stream) -> int:
         """The raw handle of a call's ``stream`` (dev is current), behind the making."""
         raw = L._stream(stream)
-        if self.stream is not None:
-            if raw != self.stream.cuda_stream:
-                with _stream_of(dev, raw):
-                    # a captured call cannot wait for a stream outside its graph; torch.cuda.graph waits
-                    # for the device first
-                    if torch.cuda.is_current_stream_capturing():
-                        return raw
+        if raw != self.raw and self.stream is not None:
+            with _stream_of(dev, raw):
+                # a captured call cannot wait for a stream outside its graph; torch.cuda.graph waits for the
+                # device first
+                if not torch.cuda.is_current_stream_capturing():
                     torch.cuda.current_stream().wait_stream(self.stream)
-            self.stream = None
+                    self.stream = None
         return raw
 
 

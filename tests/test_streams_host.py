@@ -64,16 +64,17 @@ def test_a_first_call_on_another_stream_waits_for_the_making(monkeypatch):
 
     def made():
         m = layer._Made(dev)
-        m.stream = own
+        m.stream, m.raw = own, own.cuda_stream
         return m
 
     m = made()
     assert m.before(dev, 9) == 9 and side.waited == [own]
     assert m.before(dev, 9) == 9 and m.before(dev, side) == 9 and m.before(dev, own) == 7 and side.waited == [own]
-    m = made()
-    assert m.before(dev, own) == 7 and m.before(dev, side) == 9 and side.waited == [own]
+    m = made()  # calls on the stream of the making, refused ones perhaps, do not stand for the wait
+    assert m.before(dev, own) == 7 and side.waited == [own]
+    assert m.before(dev, side) == 9 and side.waited == [own, own]
     m = made()
     capturing[0] = True
-    assert m.before(dev, side) == 9 and side.waited == [own]
-    capturing[0] = False
     assert m.before(dev, side) == 9 and side.waited == [own, own]
+    capturing[0] = False
+    assert m.before(dev, side) == 9 and side.waited == [own] * 3
